@@ -20,7 +20,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmamba_scan.so")
 ARCH = "gfx950"
 
-SOURCES = ["api.cpp", "scan_fwd.hip", "scan_split.hip", "scan_bwd.hip", "state_update.hip", "conv1d.hip", "ssd.hip"]
+SOURCES = ["api.cpp", "api_block.cpp", "scan_fwd.hip", "scan_split.hip", "scan_bwd.hip", "state_update.hip",
+           "conv1d.hip", "ssd.hip", "gated.hip", "norm.hip", "conv_bwd.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-I", CSRC]
 DEVICE = ["-x", "hip", "--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang",
@@ -43,7 +44,7 @@ def _stale(src: str, obj: str) -> bool:
     if not os.path.exists(obj):
         return True
     t = os.path.getmtime(obj)
-    deps = [os.path.join(CSRC, src)] + [os.path.join(d, f) for d in (CSRC, INCLUDE)
+    deps = [os.path.join(CSRC, src)] + [os.path.join(d, f) for d in (CSRC, INCLUDE, os.path.join(INCLUDE, "block"))
                                         for f in os.listdir(d) if f.endswith(".h")]
     return any(os.path.getmtime(p) > t for p in deps)
 

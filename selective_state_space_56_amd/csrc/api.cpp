@@ -7,50 +7,36 @@
 
 #include <hip/hip_runtime_api.h>
 
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 #include <initializer_list>
 #include <string>
 
+#include "api_util.h"
 #include "conv.h"
 #include "kernels.h"
 #include "scan_split.h"
 
+namespace mscan {
+
+std::string& last_error() {
+  static thread_local std::string message;
+  return message;
+}
+
+}  // namespace mscan
+
+using mscan::check_align;
+using mscan::check_conv_desc;
+using mscan::fail;
+using mscan::io_bytes;
+using mscan::ok;
+using mscan::overlaps;
+using mscan::Span;
+using mscan::span_bytes;
+
 namespace {
 
-thread_local std::string g_last_error;
-
-mamba_status fail(mamba_status s, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  std::vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return s;
-}
-
-mamba_status ok() {
-  g_last_error.clear();
-  return MAMBA_OK;
-}
-
 bool supported_dstate(int64_t n) { return n == 1 || n == 2 || n == 4 || n == 8 || n == 16; }
-
-size_t io_bytes(int32_t io) { return io == MAMBA_BF16 ? 2 : 4; }
-
-struct Span {
-  const char* name;
-  const void* p;
-  size_t bytes;
-};
-
-bool overlaps(const Span& a, const Span& b) {
-  if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
-  const auto a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
 
 // Checks the descriptor fields common to both entry points.
 mamba_status check_desc(const mamba_scan_desc* d, const char* who) {
@@ -147,11 +133,6 @@ int64_t widest(const Rows& r) {
   return w;
 }
 
-// Bytes spanned by `rows` rows of `len` elements `stride` elements apart.
-size_t span_bytes(int64_t rows, int64_t stride, int64_t len, size_t eb) {
-  return rows > 0 ? static_cast<size_t>((rows - 1) * stride + len) * eb : 0;
-}
-
 }  // namespace
 
 extern "C" {
@@ -166,7 +147,7 @@ const char* mamba_status_string(int s) {
   }
 }
 
-const char* mamba_last_error(void) { return g_last_error.c_str(); }
+const char* mamba_last_error(void) { return mscan::last_error().c_str(); }
 
 size_t mamba_scan_workspace_size_strided(const mamba_scan_desc* d, const mamba_scan_strides* s) {
   const char* who = "mamba_scan_workspace_size";
@@ -494,40 +475,6 @@ mamba_status mamba_state_update_strided(const mamba_scan_desc* d, const mamba_sc
 
 
 }  // extern "C"
-
-namespace {
-
-// Descriptor fields common to both convolution entry points.
-mamba_status check_conv_desc(const mamba_conv_desc* d, const char* who) {
-  if (!d) return fail(MAMBA_ERR_INVALID_ARG, "%s: desc is NULL", who);
-  if (d->batch < 0 || d->seqlen < 0 || d->dim < 0)
-    return fail(MAMBA_ERR_INVALID_ARG, "%s: negative size (batch=%lld seqlen=%lld dim=%lld)", who,
-                (long long)d->batch, (long long)d->seqlen, (long long)d->dim);
-  if (d->io_dtype != MAMBA_F32 && d->io_dtype != MAMBA_BF16)
-    return fail(MAMBA_ERR_INVALID_ARG, "%s: io_dtype %d is not MAMBA_F32 or MAMBA_BF16", who,
-                (int)d->io_dtype);
-  if (d->width < 1) return fail(MAMBA_ERR_INVALID_ARG, "%s: width %lld < 1", who, (long long)d->width);
-  if (d->width > 4)
-    return fail(MAMBA_ERR_UNSUPPORTED, "%s: width %lld not supported (1 to 4)", who,
-                (long long)d->width);
-  if (d->flags != 0) return fail(MAMBA_ERR_INVALID_ARG, "%s: flags must be 0", who);
-  const int64_t lim = int64_t(1) << 40;
-  if (d->batch > 65535 || d->seqlen > lim || d->dim > (int64_t(1) << 31) ||
-      (d->batch && d->dim > (int64_t(1) << 31) / d->batch) ||
-      (d->batch * d->dim && d->seqlen > lim / (d->batch * d->dim)) ||
-      (d->seqlen + 63) / 64 > 65535)
-    return fail(MAMBA_ERR_UNSUPPORTED, "%s: problem too large", who);
-  return MAMBA_OK;
-}
-
-mamba_status check_align(const char* who, std::initializer_list<Span> spans, size_t align) {
-  for (const Span& s : spans)
-    if (s.p && reinterpret_cast<uintptr_t>(s.p) % align)
-      return fail(MAMBA_ERR_INVALID_ARG, "%s: %s is not %zu-byte aligned", who, s.name, align);
-  return MAMBA_OK;
-}
-
-}  // namespace
 
 extern "C" {
 

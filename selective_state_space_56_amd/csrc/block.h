@@ -1,0 +1,125 @@
+// Internal launch interface of the block operators around the scan: the gated
+// linear recurrence, the RMS norm and the convolution's backward
+// (api_block.cpp -> gated.hip, norm.hip, conv_bwd.hip).
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "kernels.h"
+
+namespace mscan {
+
+// Gated linear recurrence. Strides count elements between consecutive steps
+// (token rows); batch row b starts b * seqlen rows in.
+struct GatedProblem {
+  const void* x;
+  const void* r;
+  const void* g;
+  const float* A;         // (dim)
+  const float* h0;        // (batch, dim) or null
+  const uint8_t* reset;   // (batch, seqlen) or null
+  void* out;
+  float* last_state;      // (batch, dim) or null
+  float* checkpoints;     // (batch, ceil(seqlen / kGatedCheckpoint), dim) or null
+  int64_t batch, seqlen, dim;
+  int io;
+  int64_t sx, sr, sg, so;
+};
+
+struct GatedBwdProblem {
+  const void* x;
+  const void* r;
+  const void* g;
+  const float* A;
+  const uint8_t* reset;   // or null
+  const float* checkpoints;
+  const void* dout;
+  const float* dlast;     // or null
+  void* dx;
+  void* dr;
+  void* dg;
+  float* dA;
+  float* dh0;             // or null
+  int64_t batch, seqlen, dim;
+  int io;
+  int64_t sx, sr, sg, so, sdx, sdr, sdg;
+};
+
+struct GatedUpdateProblem {
+  float* state;
+  const void* x;
+  const void* r;
+  const void* g;
+  const float* A;
+  void* out;
+  int64_t batch, dim;
+  int io;
+  int64_t sx, sr, sg, so;
+};
+
+constexpr int64_t kGatedCheckpoint = 128;
+
+size_t gated_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int io);
+size_t gated_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int io);
+hipError_t launch_gated_fwd(const GatedProblem& p, void* workspace, hipStream_t stream);
+hipError_t launch_gated_bwd(const GatedBwdProblem& p, void* workspace, hipStream_t stream);
+hipError_t launch_gated_update(const GatedUpdateProblem& p, hipStream_t stream);
+
+// RMS norm over rows, with the residual's addition and either an io output or
+// an 8-bit one with scales.
+struct NormProblem {
+  const void* x;
+  const void* residual;   // or null
+  const float* weight;
+  void* out;              // io, or e4m3 bytes when scale is set
+  float* scale;           // (rows, ceil(dim / group)) or null: io output
+  void* sum;              // null without a residual
+  int64_t rows, dim, group;
+  int io, res;
+  float eps;
+  int64_t sx, sres, ssum, so;
+};
+
+struct NormBwdProblem {
+  const void* sum;
+  const float* weight;
+  const void* dout;
+  const void* dsum;       // or null
+  void* dresidual;
+  void* dx;               // or null
+  float* dweight;
+  int64_t rows, dim;
+  int io, res;
+  float eps;
+  int64_t ssum, so, sdsum, sdres, sdx;
+};
+
+constexpr int64_t kNormMaxDim = 65536;
+
+hipError_t launch_norm(const NormProblem& p, hipStream_t stream);
+size_t norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+hipError_t launch_norm_bwd(const NormBwdProblem& p, void* workspace, hipStream_t stream);
+
+// Backward of the causal convolution.
+struct ConvBwdProblem {
+  const void* xin;
+  const float* weight;
+  const float* bias;       // or null
+  const void* state_in;    // or null
+  const void* dout;
+  const float* dstate_out; // or null
+  void* dxin;
+  float* dweight;
+  float* dbias;            // or null
+  float* dstate_in;        // or null
+  int64_t batch, seqlen, dim;
+  int width;
+  int io;
+};
+
+size_t conv_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int width);
+hipError_t launch_conv_bwd(const ConvBwdProblem& p, void* workspace, hipStream_t stream);
+
+}  // namespace mscan
