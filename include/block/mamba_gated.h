@@ -65,7 +65,7 @@ typedef struct mamba_gated_strides {
 
 /* Steps between two checkpoints: checkpoint k is the state before step
  * k * MAMBA_GATED_CHECKPOINT. */
-#define MAMBA_GATED_CHECKPOINT 128
+#define MAMBA_GATED_CHECKPOINT 64
 
 /* Bytes of device workspace mamba_gated_scan_fwd / _bwd need (0 when none, or
  * for an invalid descriptor). */

@@ -17,7 +17,7 @@ import torch
 from .binding import _IO, ConvDesc, _check, _need, _row_stride, load_library
 
 F32, BF16, F8 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
-CHECKPOINT = 128  # MAMBA_GATED_CHECKPOINT
+CHECKPOINT = 64  # MAMBA_GATED_CHECKPOINT
 
 
 class GatedDesc(ctypes.Structure):

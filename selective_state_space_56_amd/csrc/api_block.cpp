@@ -122,11 +122,12 @@ mamba_status check_gated(const char* who, const mamba_gated_desc* d) {
   if (d->flags != 0) return fail(MAMBA_ERR_INVALID_ARG, "%s: flags must be 0", who);
   if (d->dim > kMaxStride)
     return fail(MAMBA_ERR_UNSUPPORTED, "%s: dim %lld too large", who, (long long)d->dim);
-  // states, tiles and tokens are counted in 31 bits, elements in 40
+  // states and tokens are counted in 31 bits, elements in 40
   const int64_t count = (int64_t(1) << 31) - 1;
   if (d->batch > count || d->seqlen > count || (d->dim > 0 && d->batch > count / d->dim) ||
       (d->batch > 0 && d->seqlen > count / d->batch) ||
-      (d->batch * d->dim > 0 && d->seqlen > kMaxElems / (d->batch * d->dim)))
+      (d->batch * d->dim > 0 && d->seqlen > kMaxElems / (d->batch * d->dim)) ||
+      mscan::gated_tiles(d->batch, d->seqlen, d->dim) > mscan::kGatedMaxTiles)
     return fail(MAMBA_ERR_UNSUPPORTED, "%s: problem too large", who);
   return MAMBA_OK;
 }

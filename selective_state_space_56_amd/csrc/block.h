@@ -59,7 +59,13 @@ struct GatedUpdateProblem {
   int64_t sx, sr, sg, so;
 };
 
-constexpr int64_t kGatedCheckpoint = 128;
+constexpr int64_t kGatedCheckpoint = 64;
+
+// Workgroups of a sequence call: kGatedCheckpoint steps of 128 channels each.
+inline int64_t gated_tiles(int64_t batch, int64_t seqlen, int64_t dim) {
+  return batch * ((dim + 127) / 128) * ((seqlen + kGatedCheckpoint - 1) / kGatedCheckpoint);
+}
+constexpr int64_t kGatedMaxTiles = (int64_t(1) << 23) - 1;  // of 512 threads: a launch holds fewer than 2^32
 
 size_t gated_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int io);
 size_t gated_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int io);

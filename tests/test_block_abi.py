@@ -88,7 +88,7 @@ def test_gated_descriptors(lib):
         assert lib.mamba_gated_scan_workspace_size(ctypes.byref(gd(**kw))) == 0
         assert lib.mamba_gated_scan_bwd_workspace_size(ctypes.byref(gd(**kw))) == 0
     for kw in (dict(dim=(1 << 26) + 1), dict(batch=1 << 16, dim=1 << 16), dict(batch=1 << 20, seqlen=1 << 20, dim=1),
-               dict(seqlen=1 << 31, dim=1), dict(batch=1, seqlen=1 << 20, dim=1 << 21), dict(batch=1 << 62)):
+               dict(seqlen=1 << 31, dim=1), dict(batch=1 << 23, seqlen=1, dim=1), dict(batch=1, seqlen=1 << 20, dim=1 << 21), dict(batch=1 << 62)):
         assert fwd(lib, gd(**kw)) == UNSUPPORTED, kw
         assert lib.mamba_gated_scan_workspace_size(ctypes.byref(gd(**kw))) == 0
     assert upd(lib, gd(seqlen=2)) == INVALID and "seqlen" in err(lib)

@@ -10,6 +10,7 @@ from block_ref import assert_within, rounded
 from gpu_common import TOL, norm_err
 from selective_state_space_56_amd import (conv1d_bwd, conv1d_fwd, conv1d_update, gated_scan_bwd, gated_scan_fwd,
                                           gated_update, rmsnorm_bwd, rmsnorm_fwd, rmsnorm_quant_fwd)
+from selective_state_space_56_amd.block import CHECKPOINT
 
 pytestmark = pytest.mark.gpu
 IO = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -48,7 +49,7 @@ def _check_gated(v, io, with_h0=True):
     want = ref.gated(v["x"], v["r"], v["g"], v["A"], h0, v["reset"], v["dout"], dlast)
     assert_within("out", out, rounded(want["out"], io))
     assert_within("last_state", last, rounded(want["last_state"], torch.float32))
-    before = tuple(t[:, ::128] for t in want["before"])
+    before = tuple(t[:, ::CHECKPOINT] for t in want["before"])
     assert_within("checkpoints", marks, rounded(before, torch.float32))
     for name in ("dx", "dr", "dg"):
         assert_within(name, d[name], rounded(want[name], io))
@@ -168,7 +169,11 @@ def test_gated_at_the_gates_limits(dev, io):
     torch.cuda.synchronize()
     want = ref.gated(v["x"], v["r"], v["g"], v["A"], v["h0"], None, v["dout"], v["dlast"])
     assert_within("out", out, rounded(want["out"], IO[io]))
-    assert bool((out[:, 10:200, 0] == out[:, 9:10, 0]).all())
+    # held to rounding: where pieces of the sequence join, the state is A h + B
+    # with the piece's map, two roundings away from the step-by-step one, and at
+    # most 200 / 8 joins lie between
+    torch.testing.assert_close(out[:, 10:200, 0].float(), out[:, 9:10, 0].float().expand(-1, 190),
+                               rtol=50 * ref.U + (2 * ref.HALF[torch.bfloat16] if io == "bf16" else 0), atol=0)
     assert bool((out[:, :, 4] == v["h0"][:, None, 4].to(IO[io])).all())
     for t in list(d.values()):
         assert bool(torch.isfinite(t).all())
