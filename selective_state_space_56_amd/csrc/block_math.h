@@ -32,20 +32,22 @@ struct Piece {
 // 1 / (1 + e^-v): 0 and 1 at the infinities
 __device__ __forceinline__ float sigmoid_f(float v) { return hw_rcp(1.0f + hw_exp2(-v * kLog2e)); }
 
-// Decay a = e^v and input weight w = sqrt(1 - a^2) of one step, v = A sigmoid(r) <= 0.
+// Decay a = e^v and 1 - a^2 of one step, v = A sigmoid(r) <= 0, from v2 = v log2(e).
 // 1 - a^2 = 1 - e^-u with u = -2v: for u < 1/4, where 1 - a^2 would cancel, six
-// terms of its series (the next is u^6 / 5040 < 5e-8 of the sum); above, a's
-// rounding of 2^-24 is at most 3e-7 of 1 - a^2 >= 0.22.
-__device__ __forceinline__ void decay_gain(float v, float& a, float& w) {
-  a = hw_exp2(v * kLog2e);
-  const float u = -2.0f * v;
-  float p = fmaf(u, -1.0f / 720.0f, 1.0f / 120.0f);
-  p = fmaf(u, p, -1.0f / 24.0f);
-  p = fmaf(u, p, 1.0f / 6.0f);
-  p = fmaf(u, p, -0.5f);
-  p = fmaf(u, p, 1.0f);
-  const float w2 = u < 0.25f ? u * p : fmaf(-a, a, 1.0f);
-  w = __builtin_amdgcn_sqrtf(w2);
+// terms of its series u - u^2/2 + u^3/6 - ... (the next is u^6 / 5040 < 5e-8 of
+// the sum), as a polynomial in v2; above, a's rounding of 2^-24 is at most 3e-7
+// of 1 - a^2 >= 0.22.
+__device__ __forceinline__ float decay_gap(float v2, float& a) {
+  constexpr float k = 2.0f * kLn2;  // u = -k v2
+  constexpr float c1 = -k, c2 = c1 * k / 2.0f, c3 = c2 * k / 3.0f, c4 = c3 * k / 4.0f, c5 = c4 * k / 5.0f,
+                  c6 = c5 * k / 6.0f;
+  a = hw_exp2(v2);
+  float p = fmaf(v2, c6, c5);
+  p = fmaf(v2, p, c4);
+  p = fmaf(v2, p, c3);
+  p = fmaf(v2, p, c2);
+  p = fmaf(v2, p, c1);
+  return v2 > -0.25f / k ? v2 * p : fmaf(-a, a, 1.0f);
 }
 
 }  // namespace mscan

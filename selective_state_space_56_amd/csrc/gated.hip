@@ -10,11 +10,6 @@ namespace mscan {
 namespace {
 
 constexpr int kLanes = 64;
-constexpr int kSteps = 8;   // steps of a tile per wave
-constexpr int kWaves = 8;   // waves per workgroup
-constexpr int kSpan = kSteps * kWaves;  // steps of a tile
-static_assert(kSpan == kGatedCheckpoint, "a tile starts at a checkpoint");
-constexpr int kThreads = kLanes * kWaves;
 constexpr int kBack = 8;    // earlier tiles looked at together
 
 using u64 = unsigned long long;
@@ -90,16 +85,22 @@ __global__ __launch_bounds__(256) void clear_kernel(uint4* p, int64_t n) {
 constexpr size_t kHeader = 256;  // bytes before the words: the counter
 
 // Tiles are handed out in the order of a counter, all channels of all batch
-// rows before the next span of time, so that a tile waits only for tiles that
-// were handed out, to workgroups that were running, before it.
+// rows before the next span of time, one to a workgroup when it starts. A tile
+// waits only for tiles handed out before it, whose workgroups are running:
+// the first unfinished tile of all waits for nobody, so every wait ends,
+// whatever the number of workgroups that run at once. (Workgroups that stay and
+// ask for their next tile early were slower: 159 against 144 us for the forward
+// of 8 x 2048 x 5120 bf16; fresh ones load while finished ones still store.)
 struct Order {
   int per_span;   // tiles of one span of time
   int tiles;      // channel tiles of one batch row
   int spans;
 };
 
-__device__ __forceinline__ int next_tile(unsigned* counter, int* shared) {
-  if (threadIdx.x == 0) *shared = counter ? static_cast<int>(atomicAdd(counter, 1u)) : static_cast<int>(blockIdx.x);
+// This workgroup's tile. Without a counter (one span: nobody waits) its own index.
+__device__ __forceinline__ int take_tile(unsigned* counter, int* shared) {
+  if (!counter) return static_cast<int>(blockIdx.x);
+  if (threadIdx.x == 0) *shared = static_cast<int>(atomicAdd(counter, 1u));
   __syncthreads();
   return __builtin_amdgcn_readfirstlane(*shared);
 }
@@ -108,16 +109,58 @@ __device__ __forceinline__ int next_tile(unsigned* counter, int* shared) {
 // last lane, when dim is not a multiple of V) take the last V channels: they
 // compute what their owner does, and what both write is the same.
 template <int V>
-__device__ __forceinline__ int lane_channel(int tile, int64_t dim) {
-  const int c = (tile * kLanes + static_cast<int>(threadIdx.x % kLanes)) * V;
-  const int last = static_cast<int>(dim) - V;
+__device__ __forceinline__ uint32_t lane_channel(int tile, int64_t dim) {
+  const uint32_t c = (tile * kLanes + threadIdx.x % kLanes) * V;
+  const uint32_t last = static_cast<uint32_t>(dim) - V;
   return c < last ? c : last;
 }
 // Whether channel c is this lane's own (only the owner tells words: a later
 // map of another tile's lane must not take the place of a state).
 template <int V>
-__device__ __forceinline__ bool owns(int tile, int c, int64_t dim) {
-  return c >= (tile * kLanes + static_cast<int>(threadIdx.x % kLanes)) * V && c < dim;
+__device__ __forceinline__ bool owns(int tile, uint32_t c, int64_t dim) {
+  return c >= (tile * kLanes + threadIdx.x % kLanes) * V && c < dim;
+}
+
+// A tile's place: its span of time (in the order the tiles are handed out),
+// its batch row and its channels, and this wave's steps of it.
+template <int V, int STEPS, int WAVES>
+struct Place {
+  int lane, wave, turn, steps, tile;
+  int64_t b, t0, row;
+  uint32_t c;
+  __device__ __forceinline__ Place(int id, const Order& o, int64_t seqlen, int64_t dim, bool backwards) {
+    lane = threadIdx.x % kLanes;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+    turn = id / o.per_span;
+    tile = id % o.per_span;
+    b = tile / o.tiles;
+    tile %= o.tiles;
+    c = lane_channel<V>(tile, dim);
+    t0 = static_cast<int64_t>(backwards ? o.spans - 1 - turn : turn) * (STEPS * WAVES) + wave * STEPS;
+    const int64_t left = seqlen - t0;
+    steps = left < 0 ? 0 : left < STEPS ? static_cast<int>(left) : STEPS;
+    row = b * seqlen + t0;
+  }
+};
+
+// Channel c of a row whose start is the same in every lane: scalar base, 32-bit
+// lane offset. (For the stores only: the loads measured 1 % slower with it.)
+template <class T>
+__device__ __forceinline__ T* in_row(T* row, uint32_t c) {
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(row) + c * static_cast<uint32_t>(sizeof(T)));
+}
+
+// A wave's steps of one tensor, all loads in flight together. Past the end
+// (never when PLAIN) the last step is loaded again; its values are not used.
+template <bool PLAIN, class IO, int V, int STEPS>
+__device__ __forceinline__ void load_steps(const void* base, int64_t row, int64_t stride, int c, int steps,
+                                           Piece<IO, V> (&to)[STEPS]) {
+  const typename IO::raw* p = static_cast<const typename IO::raw*>(base) + row * stride;
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    to[i].load(p + c);
+    if (PLAIN || i + 1 < steps) p += stride;
+  }
 }
 
 // The resets of a wave's steps, as bits.
@@ -128,91 +171,73 @@ __device__ __forceinline__ uint32_t reset_bits(const uint8_t* reset, int64_t row
   return static_cast<uint32_t>(__ballot(on));
 }
 
-// One tile: kSpan steps of 64 V channels, kSteps of them per wave. Each wave
-// turns its steps into maps, kept in registers, and joins them; the waves'
+constexpr int kFwdSteps = 16, kFwdWaves = 8;  // a tile: steps per wave, waves
+constexpr int kFwdSpan = kFwdSteps * kFwdWaves, kFwdThreads = kLanes * kFwdWaves;
+static_assert(kGatedCheckpoint % kFwdSteps == 0, "a checkpoint is where a wave's steps start");
+
+// A wave's steps as maps (a, u) in registers, and their joined map (A1, B1).
+// PLAIN: all STEPS steps are there and none is a reset.
+template <bool PLAIN, class IO, int V>
+__device__ __forceinline__ void steps_to_maps(const GatedProblem& p, const Place<V, kFwdSteps, kFwdWaves>& at,
+                                              uint32_t resets, float (&a)[kFwdSteps][V], float (&u)[kFwdSteps][V],
+                                              float (&A1)[V], float (&B1)[V]) {
+  Piece<IO, V> x[kFwdSteps], r[kFwdSteps], g[kFwdSteps];
+  float rate[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) rate[v] = p.A[at.c + v] * kLog2e;
+  load_steps<PLAIN>(p.r, at.row, p.sr, at.c, at.steps, r);
+  load_steps<PLAIN>(p.g, at.row, p.sg, at.c, at.steps, g);
+  load_steps<PLAIN>(p.x, at.row, p.sx, at.c, at.steps, x);
+#pragma unroll
+  for (int i = 0; i < kFwdSteps; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float w = __builtin_amdgcn_sqrtf(decay_gap(rate[v] * sigmoid_f(r[i].get(v)), a[i][v]));
+      const bool on = !PLAIN && (resets >> i & 1), past = !PLAIN && i >= at.steps;
+      if (on) w = 1.0f;
+      u[i][v] = w * (sigmoid_f(g[i].get(v)) * x[i].get(v));
+      if (past) {
+        a[i][v] = 1.0f;
+        u[i][v] = 0.0f;
+      }
+      B1[v] = on ? u[i][v] : fmaf(a[i][v], B1[v], u[i][v]);
+      A1[v] = on || (!PLAIN && A1[v] == 0.0f) ? 0.0f : PLAIN ? A1[v] * a[i][v] : joined(A1[v], a[i][v]);
+    }
+  if (PLAIN)
+#pragma unroll
+    for (int v = 0; v < V; ++v) A1[v] = fmaxf(A1[v], 0x1p-149f);
+}
+
+// One tile: kFwdSpan steps of 64 V channels, kFwdSteps of them per wave. Each
+// wave turns its steps into maps, kept in registers, and joins them; the waves'
 // maps meet in LDS, the last wave tells the tile's map, finds the state that
 // enters the tile and tells the one that leaves it; then every wave runs its
 // steps from its own entering state. Inputs are read once.
 template <class IO, int V>
-__global__ __launch_bounds__(kThreads) void gated_fwd_kernel(GatedProblem p, Order o, unsigned* counter, u64* words) {
+__global__ __launch_bounds__(kFwdThreads) void gated_fwd_kernel(GatedProblem p, Order o, unsigned* counter,
+                                                                u64* words) {
   using raw = typename IO::raw;
-  __shared__ float mapA[kWaves][kLanes * V], mapB[kWaves][kLanes * V], enter[kLanes * V];
+  __shared__ float mapA[kFwdWaves][V][kLanes], mapB[kFwdWaves][V][kLanes], enter[V][kLanes];
   __shared__ int shared_tile;
-  const int tile = next_tile(counter, &shared_tile);
-  const int lane = threadIdx.x % kLanes, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
-  const int span = tile / o.per_span, of_span = tile % o.per_span;
-  const int64_t b = of_span / o.tiles;
-  const int c = lane_channel<V>(of_span % o.tiles, p.dim);
-  const int64_t t0 = static_cast<int64_t>(span) * kSpan + wave * kSteps;
-  const int64_t left = p.seqlen - t0;
-  const int steps = left < 0 ? 0 : left < kSteps ? static_cast<int>(left) : kSteps;
-  const int64_t row = b * p.seqlen + t0;
-  float a[kSteps][V], u[kSteps][V];
+  const Place<V, kFwdSteps, kFwdWaves> at(take_tile(counter, &shared_tile), o, p.seqlen, p.dim, false);
+  const int lane = at.lane, wave = at.wave, steps = at.steps;
+  float a[kFwdSteps][V], u[kFwdSteps][V];
   float A1[V], B1[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     A1[v] = 1.0f;
     B1[v] = 0.0f;
   }
-  const uint32_t resets = reset_bits(p.reset, row, steps);
-  const bool plain = steps == kSteps && resets == 0;
-  if (steps > 0) {
-    Piece<IO, V> x[kSteps], r[kSteps], g[kSteps];
-    float rate[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) rate[v] = p.A[c + v];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int64_t at = row + (i < steps ? i : steps - 1);  // past the end: the last step again, not used
-      r[i].load(static_cast<const raw*>(p.r) + at * p.sr + c);
-      g[i].load(static_cast<const raw*>(p.g) + at * p.sg + c);
-      x[i].load(static_cast<const raw*>(p.x) + at * p.sx + c);
-    }
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float w;
-        decay_gain(rate[v] * sigmoid_f(r[i].get(v)), a[i][v], w);
-        u[i][v] = sigmoid_f(g[i].get(v)) * x[i].get(v);
-        if (!plain) {
-          if (resets >> i & 1) {
-            w = 1.0f;
-            a[i][v] = 0.0f;
-          }
-          if (i >= steps) {
-            a[i][v] = 1.0f;
-            u[i][v] = 0.0f;
-          }
-        }
-        u[i][v] *= w;
-      }
-    if (plain) {
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          B1[v] = fmaf(a[i][v], B1[v], u[i][v]);
-          A1[v] *= a[i][v];
-        }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const bool on = resets >> i & 1;
-          B1[v] = on ? u[i][v] : fmaf(a[i][v], B1[v], u[i][v]);
-          A1[v] = on ? 0.0f : A1[v] == 0.0f ? 0.0f : joined(A1[v], a[i][v]);
-        }
-    }
-    if (plain)
-#pragma unroll
-      for (int v = 0; v < V; ++v) A1[v] = fmaxf(A1[v], 0x1p-149f);
-  }
+  const uint32_t resets = reset_bits(p.reset, at.row, steps);
+  const bool plain = steps == kFwdSteps && resets == 0;
+  if (plain)
+    steps_to_maps<true, IO, V>(p, at, resets, a, u, A1, B1);
+  else if (steps > 0)
+    steps_to_maps<false, IO, V>(p, at, resets, a, u, A1, B1);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    mapA[wave][lane * V + v] = A1[v];
-    mapB[wave][lane * V + v] = B1[v];
+    mapA[wave][v][lane] = A1[v];
+    mapB[wave][v][lane] = B1[v];
   }
   __syncthreads();
   // the maps of the waves before this one, joined
@@ -225,51 +250,74 @@ __global__ __launch_bounds__(kThreads) void gated_fwd_kernel(GatedProblem p, Ord
   for (int k = 0; k < wave; ++k)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float Ak = mapA[k][lane * V + v], Bk = mapB[k][lane * V + v];
-      B0[v] = through(Ak, Bk, B0[v]);
+      const float Ak = mapA[k][v][lane];
+      B0[v] = through(Ak, mapB[k][v][lane], B0[v]);
       A0[v] = Ak == 0.0f || A0[v] == 0.0f ? 0.0f : joined(A0[v], Ak);
     }
-  if (wave == kWaves - 1) {
+  if (wave == kFwdWaves - 1) {
     float At[V], Bt[V];
-    const bool tells = span + 1 < o.spans;
-    u64* word = words + (static_cast<int64_t>(span) * p.batch + b) * p.dim + c;
-    const int64_t step = p.batch * p.dim;
+    const bool tells = at.turn + 1 < o.spans;
+    const int64_t step = p.batch * p.dim, state = at.b * p.dim + at.c;
+    u64* word = words + at.turn * step + state;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       At[v] = A1[v] == 0.0f || A0[v] == 0.0f ? 0.0f : joined(A0[v], A1[v]);
       Bt[v] = through(A1[v], B1[v], B0[v]);
-      if (tells && span > 0 && owns<V>(of_span % o.tiles, c + v, p.dim)) tell(word + v, word_of_map(At[v], Bt[v]));
+      if (tells && at.turn > 0 && owns<V>(at.tile, at.c + v, p.dim)) tell(word + v, word_of_map(At[v], Bt[v]));
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float h;
-      if (span > 0)
-        h = state_before(word + v - step, step, span);
+      if (at.turn > 0)
+        h = state_before(word + v - step, step, at.turn);
       else
-        h = p.h0 ? p.h0[b * p.dim + c + v] : 0.0f;
-      enter[lane * V + v] = h;
-      if (p.checkpoints) p.checkpoints[(b * o.spans + span) * p.dim + c + v] = h;
+        h = p.h0 ? p.h0[state + v] : 0.0f;
+      enter[v][lane] = h;
       const float out = through(At[v], Bt[v], h);
       if (tells) {
-        if (owns<V>(of_span % o.tiles, c + v, p.dim)) tell(word + v, word_of_state(out));
-      } else if (p.last_state)
-        p.last_state[b * p.dim + c + v] = out;
+        if (owns<V>(at.tile, at.c + v, p.dim)) tell(word + v, word_of_state(out));
+      } else if (p.last_state) {
+        p.last_state[state + v] = out;
+      }
     }
   }
   __syncthreads();
   if (steps == 0) return;
   float h[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = through(A0[v], B0[v], enter[lane * V + v]);
+  for (int v = 0; v < V; ++v) h[v] = through(A0[v], B0[v], enter[v][lane]);
+  if (p.checkpoints && at.t0 % kGatedCheckpoint == 0) {
+    const int64_t marks = (p.seqlen + kGatedCheckpoint - 1) / kGatedCheckpoint;
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
+    for (int v = 0; v < V; ++v)
+      p.checkpoints[(at.b * marks + at.t0 / kGatedCheckpoint) * p.dim + at.c + v] = h[v];
+  }
+  raw* out = static_cast<raw*>(p.out) + at.row * p.so;
+  if (plain) {
+#pragma unroll
+    for (int i = 0; i < kFwdSteps; ++i) {
+      Piece<IO, V> y;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        h[v] = fmaf(a[i][v], h[v], u[i][v]);
+        y.set(v, h[v]);
+      }
+      y.store(in_row(out, at.c));
+      out += p.so;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kFwdSteps; ++i) {
+    if (i >= steps) continue;
     Piece<IO, V> y;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      h[v] = !plain && (resets >> i & 1) ? u[i][v] : fmaf(a[i][v], h[v], u[i][v]);
+      h[v] = resets >> i & 1 ? u[i][v] : fmaf(a[i][v], h[v], u[i][v]);
       y.set(v, h[v]);
     }
-    if (i < steps) y.store(static_cast<raw*>(p.out) + (row + i) * p.so + c);
+    y.store(in_row(out, at.c));
+    out += p.so;
   }
 }
 
@@ -279,171 +327,220 @@ __global__ __launch_bounds__(256) void gated_no_steps_kernel(const float* from, 
   if (i < n) to[i] = from ? from[i] : 0.0f;
 }
 
+constexpr int kBwdSteps = 16, kBwdWaves = 4;
+constexpr int kBwdThreads = kLanes * kBwdWaves;
+static_assert(kBwdSteps * kBwdWaves == kGatedCheckpoint, "a tile starts at a checkpoint");
+
+// What the backward keeps of a wave's steps: the decay a, the input gate sg and
+// its product with the weight p = w sg, the recurrence gate sr, and d, the
+// slope of h_t along log a: first a^2 / w sg x, then a h_{t-1} minus that.
+template <class IO, int V>
+struct Steps {
+  float a[kBwdSteps][V], p[kBwdSteps][V], sg[kBwdSteps][V], sr[kBwdSteps][V], d[kBwdSteps][V];
+  Piece<IO, V> x[kBwdSteps], dy[kBwdSteps];
+};
+
+// Loads a wave's steps and joins their maps: (A1, B1) of the states, (A1, M1)
+// of the adjoint, from the last step to the first.
+template <bool PLAIN, class IO, int V>
+__device__ __forceinline__ void bwd_maps(const GatedBwdProblem& p, const Place<V, kBwdSteps, kBwdWaves>& at,
+                                         uint32_t resets, const float (&rate)[V], Steps<IO, V>& s, float (&A1)[V],
+                                         float (&B1)[V], float (&M1)[V]) {
+  Piece<IO, V> r[kBwdSteps], g[kBwdSteps];
+  load_steps<PLAIN>(p.r, at.row, p.sr, at.c, at.steps, r);
+  load_steps<PLAIN>(p.g, at.row, p.sg, at.c, at.steps, g);
+  load_steps<PLAIN>(p.x, at.row, p.sx, at.c, at.steps, s.x);
+  load_steps<PLAIN>(p.dout, at.row, p.so, at.c, at.steps, s.dy);
+#pragma unroll
+  for (int i = 0; i < kBwdSteps; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool on = !PLAIN && (resets >> i & 1), past = !PLAIN && i >= at.steps;
+      const float sr = sigmoid_f(r[i].get(v)), sg = sigmoid_f(g[i].get(v)), xv = s.x[i].get(v);
+      float a;
+      const float gap = decay_gap(rate[v] * kLog2e * sr, a);
+      const float inv = gap > 0.0f ? __builtin_amdgcn_rsqf(gap) : 0.0f;  // 1 / w; no slope where the state is held
+      float w = gap * inv;
+      if (on) w = 1.0f;
+      if (past) {
+        a = 1.0f;
+        w = 0.0f;
+      }
+      const float pg = w * sg, u = past ? 0.0f : pg * xv;
+      s.a[i][v] = a;
+      s.p[i][v] = pg;
+      s.sg[i][v] = sg;
+      s.sr[i][v] = sr;
+      s.d[i][v] = a * a * inv * (sg * xv);
+      B1[v] = on ? u : fmaf(a, B1[v], u);
+      A1[v] = on || (!PLAIN && A1[v] == 0.0f) ? 0.0f : PLAIN ? A1[v] * a : joined(A1[v], a);
+    }
+  if (PLAIN)
+#pragma unroll
+    for (int v = 0; v < V; ++v) A1[v] = fmaxf(A1[v], 0x1p-149f);
+#pragma unroll
+  for (int i = kBwdSteps - 1; i >= 0; --i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!PLAIN && i >= at.steps) continue;
+      M1[v] = !PLAIN && (resets >> i & 1) ? 0.0f : s.a[i][v] * (s.dy[i].get(v) + M1[v]);
+    }
+}
+
+// The states before a wave's steps, from h before the first, into d.
+template <bool PLAIN, class IO, int V>
+__device__ __forceinline__ void bwd_states(int steps, uint32_t resets, float (&h)[V], Steps<IO, V>& s) {
+#pragma unroll
+  for (int i = 0; i < kBwdSteps; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!PLAIN && i >= steps) continue;
+      const float u = s.p[i][v] * s.x[i].get(v), kept = s.a[i][v] * h[v];
+      const bool on = !PLAIN && (resets >> i & 1);
+      s.d[i][v] = on ? 0.0f : kept - s.d[i][v];
+      h[v] = on ? u : kept + u;
+    }
+}
+
+// A wave's gradients, from the adjoint m that enters its last step.
+template <bool PLAIN, class IO, int V>
+__device__ __forceinline__ void bwd_grads(const GatedBwdProblem& p, const Place<V, kBwdSteps, kBwdWaves>& at,
+                                          uint32_t resets, const float (&rate)[V], const Steps<IO, V>& s,
+                                          float (&m)[V], float (&dA)[V]) {
+  using raw = typename IO::raw;
+  const int64_t end = at.row + at.steps - 1;
+  raw* dxp = static_cast<raw*>(p.dx) + end * p.sdx;
+  raw* drp = static_cast<raw*>(p.dr) + end * p.sdr;
+  raw* dgp = static_cast<raw*>(p.dg) + end * p.sdg;
+#pragma unroll
+  for (int i = kBwdSteps - 1; i >= 0; --i) {
+    if (!PLAIN && i >= at.steps) continue;
+    Piece<IO, V> dx, dr, dg;
+    const bool on = !PLAIN && (resets >> i & 1);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float lam = s.dy[i].get(v) + m[v], lp = lam * s.p[i][v];
+      const float dvr = on ? 0.0f : lam * s.d[i][v] * s.sr[i][v];
+      m[v] = on ? 0.0f : s.a[i][v] * lam;
+      dA[v] += dvr;
+      dx.set(v, lp);
+      dg.set(v, lp * s.x[i].get(v) * (1.0f - s.sg[i][v]));
+      dr.set(v, dvr * rate[v] * (1.0f - s.sr[i][v]));
+    }
+    dx.store(in_row(dxp, at.c));
+    dr.store(in_row(drp, at.c));
+    dg.store(in_row(dgp, at.c));
+    dxp -= p.sdx;
+    drp -= p.sdr;
+    dgp -= p.sdg;
+  }
+}
+
 // One tile of the backward, handed out from the last span to the first. The
 // steps' maps give the states before them (from the checkpoint) and, run from
 // the end, the adjoint: m -> a (dout + m) from step t to the one before, where
 // m enters step t from the one after it, so that lam_t = dout_t + m. Each wave
-// keeps its steps' gates in registers, finds its entering state and adjoint as
-// the forward does, and writes its steps' gradients. parts: one row of dA per tile.
+// keeps its steps in registers, finds its entering state and adjoint as the
+// forward does, and writes its steps' gradients. parts: one row of dA per span
+// and batch row.
 template <class IO, int V>
-__global__ __launch_bounds__(kThreads) void gated_bwd_kernel(GatedBwdProblem p, Order o, unsigned* counter, u64* words,
-                                                             float* parts) {
-  using raw = typename IO::raw;
-  __shared__ float mapA[kWaves][kLanes * V], mapB[kWaves][kLanes * V], mapM[kWaves][kLanes * V], enter[kLanes * V];
+__global__ __launch_bounds__(kBwdThreads, 2) void gated_bwd_kernel(GatedBwdProblem p, Order o, unsigned* counter,
+                                                                   u64* words, float* parts) {
+  __shared__ float mapA[kBwdWaves][V][kLanes], mapB[kBwdWaves][V][kLanes], mapM[kBwdWaves][V][kLanes], enter[V][kLanes];
   __shared__ int shared_tile;
-  const int tile = next_tile(counter, &shared_tile);
-  const int lane = threadIdx.x % kLanes, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
-  const int turn = tile / o.per_span, of_span = tile % o.per_span, span = o.spans - 1 - turn;
-  const int64_t b = of_span / o.tiles;
-  const int c = lane_channel<V>(of_span % o.tiles, p.dim);
-  const int64_t t0 = static_cast<int64_t>(span) * kSpan + wave * kSteps;
-  const int64_t left = p.seqlen - t0;
-  const int steps = left < 0 ? 0 : left < kSteps ? static_cast<int>(left) : kSteps;
-  const int64_t row = b * p.seqlen + t0;
-  float a[kSteps][V], w[kSteps][V], sr[kSteps][V], sg[kSteps][V], rate[V];
-  Piece<IO, V> x[kSteps], dy[kSteps];
-  float A1[V], B1[V], M1[V], mark[V];
+  const Place<V, kBwdSteps, kBwdWaves> at(take_tile(counter, &shared_tile), o, p.seqlen, p.dim, true);
+  const int lane = at.lane, wave = at.wave, span = o.spans - 1 - at.turn;
+  const int64_t step = p.batch * p.dim, state = at.b * p.dim + at.c;
+  Steps<IO, V> s;
+  float rate[V], A1[V], B1[V], M1[V], h[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     A1[v] = 1.0f;
     B1[v] = M1[v] = 0.0f;
-    rate[v] = p.A[c + v];
-    mark[v] = p.checkpoints[(b * o.spans + span) * p.dim + c + v];
+    rate[v] = p.A[at.c + v];
+    h[v] = p.checkpoints[(at.b * o.spans + span) * p.dim + at.c + v];
   }
-  const uint32_t resets = reset_bits(p.reset, row, steps);
-  if (steps > 0) {
-    Piece<IO, V> r[kSteps], g[kSteps];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int64_t at = row + (i < steps ? i : steps - 1);
-      r[i].load(static_cast<const raw*>(p.r) + at * p.sr + c);
-      g[i].load(static_cast<const raw*>(p.g) + at * p.sg + c);
-      x[i].load(static_cast<const raw*>(p.x) + at * p.sx + c);
-      dy[i].load(static_cast<const raw*>(p.dout) + at * p.so + c);
-    }
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        sr[i][v] = sigmoid_f(r[i].get(v));
-        sg[i][v] = sigmoid_f(g[i].get(v));
-        decay_gain(rate[v] * sr[i][v], a[i][v], w[i][v]);
-        const bool on = resets >> i & 1;
-        if (on) w[i][v] = 1.0f;
-        if (i >= steps) a[i][v] = 1.0f;
-        const float u = i < steps ? w[i][v] * (sg[i][v] * x[i].get(v)) : 0.0f;
-        B1[v] = on ? u : fmaf(a[i][v], B1[v], u);
-        A1[v] = on || A1[v] == 0.0f ? 0.0f : joined(A1[v], a[i][v]);
-      }
-#pragma unroll
-    for (int i = kSteps - 1; i >= 0; --i)
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (i < steps) M1[v] = resets >> i & 1 ? 0.0f : a[i][v] * (dy[i].get(v) + M1[v]);
-  }
+  const uint32_t resets = reset_bits(p.reset, at.row, at.steps);
+  const bool plain = at.steps == kBwdSteps && resets == 0;
+  if (plain)
+    bwd_maps<true>(p, at, resets, rate, s, A1, B1, M1);
+  else if (at.steps > 0)
+    bwd_maps<false>(p, at, resets, rate, s, A1, B1, M1);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    mapA[wave][lane * V + v] = A1[v];
-    mapB[wave][lane * V + v] = B1[v];
-    mapM[wave][lane * V + v] = M1[v];
+    mapA[wave][v][lane] = A1[v];
+    mapB[wave][v][lane] = B1[v];
+    mapM[wave][v][lane] = M1[v];
   }
   __syncthreads();
   if (wave == 0) {
     float At[V], Mt[V];
     const bool tells = span > 0;
-    const int64_t step = p.batch * p.dim;
-    u64* word = words + (static_cast<int64_t>(turn) * p.batch + b) * p.dim + c;
+    u64* word = words + at.turn * step + state;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       At[v] = 1.0f;
       Mt[v] = 0.0f;
     }
-    for (int k = kWaves - 1; k >= 0; --k)
+    for (int k = kBwdWaves - 1; k >= 0; --k)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float Ak = mapA[k][lane * V + v];
-        Mt[v] = through(Ak, mapM[k][lane * V + v], Mt[v]);
+        const float Ak = mapA[k][v][lane];
+        Mt[v] = through(Ak, mapM[k][v][lane], Mt[v]);
         At[v] = Ak == 0.0f || At[v] == 0.0f ? 0.0f : joined(At[v], Ak);
       }
-    if (tells && turn > 0)
+    if (tells && at.turn > 0)
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (owns<V>(of_span % o.tiles, c + v, p.dim)) tell(word + v, word_of_map(At[v], Mt[v]));
+        if (owns<V>(at.tile, at.c + v, p.dim)) tell(word + v, word_of_map(At[v], Mt[v]));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float m;
-      if (turn > 0)
-        m = state_before(word + v - step, step, turn);
+      if (at.turn > 0)
+        m = state_before(word + v - step, step, at.turn);
       else
-        m = p.dlast ? p.dlast[b * p.dim + c + v] : 0.0f;
-      enter[lane * V + v] = m;
+        m = p.dlast ? p.dlast[state + v] : 0.0f;
+      enter[v][lane] = m;
       const float out = through(At[v], Mt[v], m);
       if (tells) {
-        if (owns<V>(of_span % o.tiles, c + v, p.dim)) tell(word + v, word_of_state(out));
-      } else if (p.dh0)
-        p.dh0[b * p.dim + c + v] = out;
+        if (owns<V>(at.tile, at.c + v, p.dim)) tell(word + v, word_of_state(out));
+      } else if (p.dh0) {
+        p.dh0[state + v] = out;
+      }
     }
   }
-  // the states before this wave's steps
-  float before[kSteps][V];
-  {
-    float h[V];
+  for (int k = 0; k < wave; ++k)
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = mark[v];
-    for (int k = 0; k < wave; ++k)
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = through(mapA[k][lane * V + v], mapB[k][lane * V + v], h[v]);
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        before[i][v] = h[v];
-        const float u = w[i][v] * (sg[i][v] * x[i].get(v));
-        h[v] = resets >> i & 1 ? u : fmaf(a[i][v], h[v], u);
-      }
-  }
+    for (int v = 0; v < V; ++v) h[v] = through(mapA[k][v][lane], mapB[k][v][lane], h[v]);
+  if (plain)
+    bwd_states<true>(at.steps, resets, h, s);
+  else
+    bwd_states<false>(at.steps, resets, h, s);
   __syncthreads();
-  float dA[V];
+  float dA[V], m[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) dA[v] = 0.0f;
-  if (steps > 0) {
-    float m[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) m[v] = enter[lane * V + v];
-    for (int k = kWaves - 1; k > wave; --k)
-#pragma unroll
-      for (int v = 0; v < V; ++v) m[v] = through(mapA[k][lane * V + v], mapM[k][lane * V + v], m[v]);
-#pragma unroll
-    for (int i = kSteps - 1; i >= 0; --i) {
-      if (i >= steps) continue;
-      Piece<IO, V> dx, dr, dg;
-      const bool on = resets >> i & 1;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float xv = x[i].get(v), lam = dy[i].get(v) + m[v], lw = lam * w[i][v] * sg[i][v];
-        const float slope = w[i][v] > 0.0f ? a[i][v] * a[i][v] * hw_rcp(w[i][v]) : 0.0f;
-        const float dv = on ? 0.0f : lam * fmaf(a[i][v], before[i][v], -slope * sg[i][v] * xv);
-        m[v] = on ? 0.0f : a[i][v] * lam;
-        dA[v] = fmaf(dv, sr[i][v], dA[v]);
-        dx.set(v, lw);
-        dg.set(v, lw * xv * (1.0f - sg[i][v]));
-        dr.set(v, dv * rate[v] * sr[i][v] * (1.0f - sr[i][v]));
-      }
-      dx.store(static_cast<raw*>(p.dx) + (row + i) * p.sdx + c);
-      dr.store(static_cast<raw*>(p.dr) + (row + i) * p.sdr + c);
-      dg.store(static_cast<raw*>(p.dg) + (row + i) * p.sdg + c);
-    }
+  for (int v = 0; v < V; ++v) {
+    dA[v] = 0.0f;
+    m[v] = enter[v][lane];
   }
+  for (int k = kBwdWaves - 1; k > wave; --k)
+#pragma unroll
+    for (int v = 0; v < V; ++v) m[v] = through(mapA[k][v][lane], mapM[k][v][lane], m[v]);
+  if (plain)
+    bwd_grads<true>(p, at, resets, rate, s, m, dA);
+  else if (at.steps > 0)
+    bwd_grads<false>(p, at, resets, rate, s, m, dA);
   // the waves' parts of dA, added in their order (mapB is read no more)
 #pragma unroll
-  for (int v = 0; v < V; ++v) mapB[wave][lane * V + v] = dA[v];
+  for (int v = 0; v < V; ++v) mapB[wave][v][lane] = dA[v];
   __syncthreads();
   if (wave == 0)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float s = 0.0f;
-      for (int k = 0; k < kWaves; ++k) s += mapB[k][lane * V + v];
-      parts[(static_cast<int64_t>(turn) * p.batch + b) * p.dim + c + v] = s;
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kBwdWaves; ++k) sum += mapB[k][v][lane];
+      parts[at.turn * step + state + v] = sum;
     }
 }
 
@@ -457,27 +554,29 @@ __global__ __launch_bounds__(256) void gated_update_kernel(GatedUpdateProblem p)
   const float x = IO::load(static_cast<const raw*>(p.x) + b * p.sx + c);
   const float sr = sigmoid_f(IO::load(static_cast<const raw*>(p.r) + b * p.sr + c));
   const float sg = sigmoid_f(IO::load(static_cast<const raw*>(p.g) + b * p.sg + c));
-  float a, w;
-  decay_gain(p.A[c] * sr, a, w);
+  float a;
+  const float w = __builtin_amdgcn_sqrtf(decay_gap(p.A[c] * kLog2e * sr, a));
   const float h = fmaf(a, p.state[i], w * (sg * x));
   p.state[i] = h;
   static_cast<raw*>(p.out)[b * p.so + c] = IO::from_f32(h);
 }
 
-Order order_of(int64_t batch, int64_t seqlen, int64_t dim, int V) {
+Order order_of(int64_t batch, int64_t seqlen, int64_t dim, int V, int64_t span) {
   Order o;
   o.tiles = static_cast<int>((dim + kLanes * V - 1) / (kLanes * V));
   o.per_span = static_cast<int>(batch * o.tiles);
-  o.spans = static_cast<int>((seqlen + kSpan - 1) / kSpan);
+  o.spans = static_cast<int>((seqlen + span - 1) / span);
   return o;
 }
+
+dim3 grid_of(const Order& o) { return dim3(static_cast<unsigned>(o.per_span) * o.spans); }
 
 size_t rounded_up(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
 // The counter and one word per channel of every span but the last; nothing for
 // sequences of one span, whose tiles wait for nobody.
-size_t words_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
-  const int64_t spans = (seqlen + kSpan - 1) / kSpan;
+size_t words_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t span) {
+  const int64_t spans = (seqlen + span - 1) / span;
   return spans > 1 && batch * dim > 0 ? kHeader + rounded_up(static_cast<size_t>((spans - 1) * batch * dim) * 8) : 0;
 }
 
@@ -490,23 +589,23 @@ hipError_t clear_words(void* workspace, size_t bytes, hipStream_t stream) {
 
 template <class IO, int V>
 hipError_t launch_fwd(const GatedProblem& p, void* workspace, hipStream_t stream) {
-  const Order o = order_of(p.batch, p.seqlen, p.dim, V);
-  const size_t bytes = words_bytes(p.batch, p.seqlen, p.dim);
+  const Order o = order_of(p.batch, p.seqlen, p.dim, V, kFwdSpan);
+  const size_t bytes = words_bytes(p.batch, p.seqlen, p.dim, kFwdSpan);
   if (bytes) {
     const hipError_t e = clear_words(workspace, bytes, stream);
     if (e != hipSuccess) return e;
   }
   unsigned* counter = bytes ? static_cast<unsigned*>(workspace) : nullptr;
   u64* words = bytes ? reinterpret_cast<u64*>(static_cast<char*>(workspace) + kHeader) : nullptr;
-  hipLaunchKernelGGL((gated_fwd_kernel<IO, V>), dim3(static_cast<unsigned>(o.per_span) * o.spans), dim3(kThreads), 0,
+  hipLaunchKernelGGL((gated_fwd_kernel<IO, V>), grid_of(o), dim3(kFwdThreads), 0,
                      stream, p, o, counter, words);
   return hipGetLastError();
 }
 
 template <class IO, int V>
 hipError_t launch_bwd(const GatedBwdProblem& p, void* workspace, hipStream_t stream) {
-  const Order o = order_of(p.batch, p.seqlen, p.dim, V);
-  const size_t bytes = words_bytes(p.batch, p.seqlen, p.dim);
+  const Order o = order_of(p.batch, p.seqlen, p.dim, V, kGatedCheckpoint);
+  const size_t bytes = words_bytes(p.batch, p.seqlen, p.dim, kGatedCheckpoint);
   if (bytes) {
     const hipError_t e = clear_words(workspace, bytes, stream);
     if (e != hipSuccess) return e;
@@ -515,7 +614,7 @@ hipError_t launch_bwd(const GatedBwdProblem& p, void* workspace, hipStream_t str
   unsigned* counter = bytes ? reinterpret_cast<unsigned*>(ws) : nullptr;
   u64* words = bytes ? reinterpret_cast<u64*>(ws + kHeader) : nullptr;
   float* parts = reinterpret_cast<float*>(ws + bytes);
-  hipLaunchKernelGGL((gated_bwd_kernel<IO, V>), dim3(static_cast<unsigned>(o.per_span) * o.spans), dim3(kThreads), 0,
+  hipLaunchKernelGGL((gated_bwd_kernel<IO, V>), grid_of(o), dim3(kBwdThreads), 0,
                      stream, p, o, counter, words, parts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -525,12 +624,12 @@ hipError_t launch_bwd(const GatedBwdProblem& p, void* workspace, hipStream_t str
 }  // namespace
 
 size_t gated_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int) {
-  return words_bytes(batch, seqlen, dim);
+  return words_bytes(batch, seqlen, dim, kFwdSpan);
 }
 
 size_t gated_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int) {
-  const int64_t spans = (seqlen + kSpan - 1) / kSpan;
-  return words_bytes(batch, seqlen, dim) + rounded_up(static_cast<size_t>(spans * batch * dim) * 4);
+  const int64_t spans = (seqlen + kGatedCheckpoint - 1) / kGatedCheckpoint;
+  return words_bytes(batch, seqlen, dim, kGatedCheckpoint) + rounded_up(static_cast<size_t>(spans * batch * dim) * 4);
 }
 
 hipError_t launch_gated_fwd(const GatedProblem& p, void* workspace, hipStream_t stream) {
@@ -555,7 +654,7 @@ hipError_t launch_gated_bwd(const GatedBwdProblem& p, void* workspace, hipStream
     return hipGetLastError();
   }
   if (p.io == kIoBf16) return p.dim > 1 ? launch_bwd<Bf16Io, 2>(p, workspace, stream) : launch_bwd<Bf16Io, 1>(p, workspace, stream);
-  return p.dim > 1 ? launch_bwd<F32Io, 2>(p, workspace, stream) : launch_bwd<F32Io, 1>(p, workspace, stream);
+  return launch_bwd<F32Io, 1>(p, workspace, stream);
 }
 
 hipError_t launch_gated_update(const GatedUpdateProblem& p, hipStream_t stream) {
