@@ -1,6 +1,14 @@
 // RMS norm of a block's entry: y = s rstd w with s = x + residual and
 // rstd = 1 / sqrt(mean s^2 + eps), as an io output or as e4m3 with scales, and
 // its backward.
+//
+// Bound by HBM: every element is read once and written once. Up to kRegDim
+// channels a row stays in its workgroup's registers from the first load to the
+// last store, 8 channels per lane, and the next row's loads are in flight while
+// the current row is reduced and written. Wider rows are read again for each
+// use (from the L2 cache, which holds them). Rows of any alignment take the same
+// path (the last piece of a row element by element where the row is not whole
+// pieces).
 #include "block.h"
 #include "block_math.h"
 #include "colsum.h"
@@ -9,134 +17,414 @@ namespace mscan {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kPiece = 8;        // channels per lane and access
+constexpr int kMaxWaves = 16;
+constexpr int kRegDim = kMaxWaves * 64 * kPiece;
 constexpr float kE4m3Max = 448.0f;
 constexpr float kTiny = 0x1p-100f;
 
-__device__ __forceinline__ float load_any(const void* p, int io, int64_t i) {
-  return io == kIoBf16 ? Bf16Io::load(static_cast<const uint16_t*>(p) + i) : static_cast<const float*>(p)[i];
-}
+template <class IO>
+using Row8 = Piece<IO, kPiece>;
 
-__device__ __forceinline__ void store_any(void* p, int io, int64_t i, float v) {
-  if (io == kIoBf16)
-    static_cast<uint16_t*>(p)[i] = Bf16Io::from_f32(v);
+template <class IO>
+__device__ __forceinline__ void load8(Row8<IO>& to, const typename IO::raw* row, int d, int dim) {
+  if (d + kPiece <= dim)
+    to.load(row + d);
   else
-    static_cast<float*>(p)[i] = v;
+    to.load_some(row + d, dim - d);
 }
 
-__device__ __forceinline__ float rounded(int io, float v) {
-  return io == kIoBf16 ? Bf16Io::to_f32(Bf16Io::from_f32(v)) : v;
+template <class IO>
+__device__ __forceinline__ void store8(const Row8<IO>& from, typename IO::raw* row, int d, int dim) {
+  if (d + kPiece <= dim)
+    from.store(row + d);
+  else
+    from.store_some(row + d, dim - d);
 }
 
-// Sum (or maximum) over the workgroup, the same in every thread.
-template <bool MAX>
-__device__ float over_block(float v, float* scratch) {
-  const int t = threadIdx.x;
+struct AddOp {
+  static __device__ __forceinline__ float of(float a, float b) { return a + b; }
+};
+struct MaxOp {
+  static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
+};
+
+// The value of the lane N places round within its 16 lanes.
+template <int N>
+__device__ __forceinline__ float turned(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + N, 0xf, 0xf, true));
+}
+
+// Over 16 neighbouring lanes (the channels of one group of 128), in each of them.
+template <class Op>
+__device__ __forceinline__ float over_16(float v) {
+  v = Op::of(v, turned<8>(v));
+  v = Op::of(v, turned<4>(v));
+  v = Op::of(v, turned<2>(v));
+  return Op::of(v, turned<1>(v));
+}
+
+template <class Op>
+__device__ __forceinline__ float over_wave(float v) {
+  v = over_16<Op>(v);
+  v = Op::of(v, __shfl_xor(v, 16));
+  return Op::of(v, __shfl_xor(v, 32));
+}
+
+// N values over the workgroup, in every thread and the same in each (the waves'
+// values are joined in their order). One barrier: two calls in a row use two
+// different `scratch` arrays.
+template <class Op, int N>
+__device__ __forceinline__ void over_block(float (&v)[N], float (&scratch)[N][kMaxWaves]) {
+  const int waves = blockDim.x / 64, wave = threadIdx.x / 64;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = over_wave<Op>(v[i]);
+  if (waves == 1) return;
+  if (threadIdx.x % 64 == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) scratch[i][wave] = v[i];
   __syncthreads();
-  scratch[t] = v;
-  __syncthreads();
-  for (int k = kThreads / 2; k > 0; k /= 2) {
-    if (t < k) scratch[t] = MAX ? fmaxf(scratch[t], scratch[t + k]) : scratch[t] + scratch[t + k];
-    __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = scratch[i][0];
+    for (int k = 1; k < waves; ++k) v[i] = Op::of(v[i], scratch[i][k]);
   }
-  return scratch[0];
 }
 
-__device__ __forceinline__ uint8_t e4m3(float v) {
-  v = v > kE4m3Max ? kE4m3Max : v < -kE4m3Max ? -kE4m3Max : v;  // keeps NaN
-  return static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xff);
+__device__ __forceinline__ float rstd_of(float ss, float dim, float eps) { return 1.0f / sqrtf(ss / dim + eps); }
+
+__device__ __forceinline__ float top_of(const float (&y)[kPiece]) {
+  float top = kTiny;
+#pragma unroll
+  for (int j = 0; j < kPiece; ++j) top = fmaxf(top, fabsf(y[j]));
+  return top;
 }
 
-// One workgroup per row, the row read again for each of its uses.
-__device__ void norm_row(const NormProblem& p, int64_t row, float* scratch) {
-  const auto s_at = [&](int64_t d) {
-    if (p.sum) return load_any(p.sum, p.res, row * p.ssum + d);
-    return load_any(p.x, p.io, row * p.sx + d);
+// 8 values as e4m3. |y| inv is at most 448 and a rounding, which rounds to
+// 448: nothing to saturate.
+__device__ __forceinline__ void store_e4m3(const float (&y)[kPiece], float inv, uint8_t* row, int d, int dim) {
+  uint32_t q[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int word = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h] * inv, y[4 * h + 1] * inv, 0, false);
+    word = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h + 2] * inv, y[4 * h + 3] * inv, word, true);
+    q[h] = static_cast<uint32_t>(word);
+  }
+  if (d + kPiece <= dim)
+    __builtin_memcpy(row + d, q, 8);
+  else
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j)
+      if (d + j < dim) row[d + j] = static_cast<uint8_t>(q[j / 4] >> (8 * (j % 4)));
+}
+
+enum Out { kIo, kRowScale, kGroupScale };
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ..., channels 8 t .. 8 t + 7 in thread t.
+template <class IO, class RES, int OUT>
+__global__ __launch_bounds__(1024) void norm_kernel(NormProblem p) {
+  using raw = typename IO::raw;
+  using res_raw = typename RES::raw;
+  __shared__ float sums[2][1][kMaxWaves], tops[2][1][kMaxWaves];
+  const int dim = static_cast<int>(p.dim), d = static_cast<int>(threadIdx.x) * kPiece;
+  Row8<F32Io> w;
+  load8(w, p.weight, d, dim);
+  Row8<IO> x;
+  Row8<RES> r;
+  const auto load = [&](int64_t row) {
+    load8(x, static_cast<const raw*>(p.x) + row * p.sx, d, dim);
+    if (p.residual) load8(r, static_cast<const res_raw*>(p.residual) + row * p.sres, d, dim);
   };
-  float ss = 0.0f;
-  for (int64_t d = threadIdx.x; d < p.dim; d += kThreads) {
-    float s = load_any(p.x, p.io, row * p.sx + d);
+  load(blockIdx.x);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    float s[kPiece], ss[1] = {0.0f};
     if (p.residual) {
-      s = rounded(p.res, s + load_any(p.residual, p.res, row * p.sres + d));
-      store_any(p.sum, p.res, row * p.ssum + d, s);
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) {
+        r.set(j, x.get(j) + r.get(j));  // rounded to the stream's type here
+        s[j] = r.get(j);
+      }
+      store8(r, static_cast<res_raw*>(p.sum) + row * p.ssum, d, dim);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) s[j] = x.get(j);
     }
-    ss = fmaf(s, s, ss);
-  }
-  const float rstd = 1.0f / sqrtf(over_block<false>(ss, scratch) / static_cast<float>(p.dim) + p.eps);
-  if (!p.scale) {
-    for (int64_t d = threadIdx.x; d < p.dim; d += kThreads)
-      store_any(p.out, p.io, row * p.so + d, s_at(d) * rstd * p.weight[d]);
-    return;
-  }
-  const int64_t group = p.group ? p.group : p.dim, groups = (p.dim + group - 1) / group;
-  for (int64_t k = 0; k < groups; ++k) {
-    const int64_t end = (k + 1) * group < p.dim ? (k + 1) * group : p.dim;
-    float top = kTiny;
-    for (int64_t d = k * group + threadIdx.x; d < end; d += kThreads)
-      top = fmaxf(top, fabsf(s_at(d) * rstd * p.weight[d]));
-    const float scale = over_block<true>(top, scratch) / kE4m3Max;
-    for (int64_t d = k * group + threadIdx.x; d < end; d += kThreads)
-      static_cast<uint8_t*>(p.out)[row * p.so + d] = e4m3(s_at(d) * rstd * p.weight[d] / scale);
-    if (threadIdx.x == 0) p.scale[row * groups + k] = scale;
+    if (row + gridDim.x < p.rows) load(row + gridDim.x);
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) ss[0] = fmaf(s[j], s[j], ss[0]);
+    over_block<AddOp>(ss, sums[turn]);
+    const float rstd = rstd_of(ss[0], static_cast<float>(dim), p.eps);
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) s[j] = s[j] * rstd * w.get(j);
+    if constexpr (OUT == kIo) {
+      Row8<IO> y;
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) y.set(j, s[j]);
+      store8(y, static_cast<raw*>(p.out) + row * p.so, d, dim);
+    } else {
+      // channels past the end are 0 and do not raise a maximum
+      float top[1] = {top_of(s)};
+      if constexpr (OUT == kGroupScale) {
+        top[0] = over_16<MaxOp>(top[0]);
+        if (threadIdx.x % 16 == 0 && d < dim) p.scale[row * ((dim + 127) / 128) + d / 128] = top[0] / kE4m3Max;
+      } else {
+        over_block<MaxOp>(top, tops[turn]);
+        if (threadIdx.x == 0) p.scale[row] = top[0] / kE4m3Max;
+      }
+      store_e4m3(s, kE4m3Max / top[0], static_cast<uint8_t*>(p.out) + row * p.so, d, dim);
+    }
   }
 }
 
-constexpr int64_t kMaxGrid = 65536;
-
-__global__ __launch_bounds__(kThreads) void norm_kernel(NormProblem p) {
-  __shared__ float scratch[kThreads];
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) norm_row(p, row, scratch);
-}
-
-constexpr int64_t kParts = 256;  // workgroups of the backward, each with a part of dweight
-
-__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdProblem p, float* parts) {
-  __shared__ float scratch[kThreads];
-  float* part = parts + blockIdx.x * p.dim;
-  for (int64_t d = threadIdx.x; d < p.dim; d += kThreads) part[d] = 0.0f;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    float ss = 0.0f, su = 0.0f;
-    for (int64_t d = threadIdx.x; d < p.dim; d += kThreads) {
-      const float s = load_any(p.sum, p.res, row * p.ssum + d);
-      ss = fmaf(s, s, ss);
-      su = fmaf(s, p.weight[d] * load_any(p.dout, p.io, row * p.so + d), su);
+// Rows of more than kRegDim channels, in turns of 1024 pieces.
+template <class IO, class RES>
+__global__ __launch_bounds__(1024) void norm_wide_kernel(NormProblem p) {
+  using raw = typename IO::raw;
+  using res_raw = typename RES::raw;
+  __shared__ float sums[2][1][kMaxWaves], tops[2][1][kMaxWaves];
+  const int dim = static_cast<int>(p.dim), first = static_cast<int>(threadIdx.x) * kPiece;
+  const int whole = (dim + kRegDim - 1) / kRegDim * kRegDim;  // every thread takes every turn
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const raw* xr = static_cast<const raw*>(p.x) + row * p.sx;
+    res_raw* sr = static_cast<res_raw*>(p.sum) + row * p.ssum;
+    float ss[1] = {0.0f};
+    for (int d = first; d < dim; d += kRegDim) {
+      Row8<IO> x;
+      load8(x, xr, d, dim);
+      float s[kPiece];
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) s[j] = x.get(j);
+      if (p.residual) {
+        Row8<RES> r;
+        load8(r, static_cast<const res_raw*>(p.residual) + row * p.sres, d, dim);
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) {
+          r.set(j, s[j] + r.get(j));
+          s[j] = r.get(j);
+        }
+        store8(r, sr, d, dim);
+      }
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) ss[0] = fmaf(s[j], s[j], ss[0]);
     }
-    const float n = static_cast<float>(p.dim);
-    const float rstd = 1.0f / sqrtf(over_block<false>(ss, scratch) / n + p.eps);
-    const float mean = over_block<false>(su, scratch) * rstd / n;
-    for (int64_t d = threadIdx.x; d < p.dim; d += kThreads) {
-      const float norm = load_any(p.sum, p.res, row * p.ssum + d) * rstd;
-      const float dy = load_any(p.dout, p.io, row * p.so + d);
-      float ds = rstd * (p.weight[d] * dy - norm * mean);
-      if (p.dsum) ds += load_any(p.dsum, p.res, row * p.sdsum + d);
-      store_any(p.dresidual, p.res, row * p.sdres + d, ds);
-      if (p.dx) store_any(p.dx, p.io, row * p.sdx + d, ds);
-      part[d] = fmaf(dy, norm, part[d]);
+    over_block<AddOp>(ss, sums[turn]);
+    const float rstd = rstd_of(ss[0], static_cast<float>(dim), p.eps);
+    // y of a piece, from the stream that this same thread has stored (or x)
+    const auto normed = [&](int d, float (&y)[kPiece]) {
+      Row8<F32Io> w;
+      load8(w, p.weight, d, dim);
+      if (p.residual) {
+        Row8<RES> r;
+        load8(r, sr, d, dim);
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) y[j] = r.get(j) * rstd * w.get(j);
+      } else {
+        Row8<IO> x;
+        load8(x, xr, d, dim);
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) y[j] = x.get(j) * rstd * w.get(j);
+      }
+    };
+    float y[kPiece], top[1] = {kTiny};
+    if (p.scale && !p.group) {
+      for (int d = first; d < dim; d += kRegDim) {
+        normed(d, y);
+        top[0] = fmaxf(top[0], top_of(y));
+      }
+      over_block<MaxOp>(top, tops[turn]);
+      if (threadIdx.x == 0) p.scale[row] = top[0] / kE4m3Max;
+    }
+    for (int d = first; d < whole; d += kRegDim) {
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) y[j] = 0.0f;
+      if (d < dim) normed(d, y);
+      if (p.scale && p.group) {
+        top[0] = over_16<MaxOp>(top_of(y));
+        if (threadIdx.x % 16 == 0 && d < dim) p.scale[row * ((dim + 127) / 128) + d / 128] = top[0] / kE4m3Max;
+      }
+      if (d >= dim) continue;
+      if (p.scale) {
+        store_e4m3(y, kE4m3Max / top[0], static_cast<uint8_t*>(p.out) + row * p.so, d, dim);
+      } else {
+        Row8<IO> out;
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) out.set(j, y[j]);
+        store8(out, static_cast<raw*>(p.out) + row * p.so, d, dim);
+      }
     }
   }
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ..., each read once: both sums
+// (s^2 and s u, u = w dout) in one reduction, then the row's gradient from the
+// registers. Every workgroup keeps its rows' sum of dout s rstd: one row of parts.
+template <class IO, class RES>
+__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdProblem p, float* parts) {
+  using raw = typename IO::raw;
+  using res_raw = typename RES::raw;
+  __shared__ float sums[2][2][kMaxWaves];
+  const int dim = static_cast<int>(p.dim), d = static_cast<int>(threadIdx.x) * kPiece;
+  Row8<F32Io> w, dw;
+  load8(w, p.weight, d, dim);
+#pragma unroll
+  for (int j = 0; j < kPiece; ++j) dw.set(j, 0.0f);
+  Row8<RES> s, ds;
+  Row8<IO> dy;
+  const auto load = [&](int64_t row) {
+    load8(s, static_cast<const res_raw*>(p.sum) + row * p.ssum, d, dim);
+    load8(dy, static_cast<const raw*>(p.dout) + row * p.so, d, dim);
+    if (p.dsum) load8(ds, static_cast<const res_raw*>(p.dsum) + row * p.sdsum, d, dim);
+  };
+  load(blockIdx.x);
+  int turn = 0;
+  const float n = static_cast<float>(dim);
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    Row8<RES> s0 = s, ds0;
+    if (p.dsum) ds0 = ds;
+    const Row8<IO> dy0 = dy;
+    if (row + gridDim.x < p.rows) load(row + gridDim.x);
+    float both[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+      const float sv = s0.get(j);
+      both[0] = fmaf(sv, sv, both[0]);
+      both[1] = fmaf(sv, w.get(j) * dy0.get(j), both[1]);
+    }
+    over_block<AddOp>(both, sums[turn]);
+    const float rstd = rstd_of(both[0], n, p.eps), mean = both[1] * rstd / n;
+    Row8<IO> dx;
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+      const float norm = s0.get(j) * rstd, g = dy0.get(j);
+      dw.set(j, fmaf(g, norm, dw.get(j)));
+      float v = rstd * fmaf(-norm, mean, w.get(j) * g);
+      if (p.dsum) v += ds0.get(j);
+      s0.set(j, v);
+      dx.set(j, v);
+    }
+    store8(s0, static_cast<res_raw*>(p.dresidual) + row * p.sdres, d, dim);
+    if (p.dx) store8(dx, static_cast<raw*>(p.dx) + row * p.sdx, d, dim);
+  }
+  store8(dw, parts + static_cast<int64_t>(blockIdx.x) * dim, d, dim);
+}
+
+// Rows of more than kRegDim channels; the parts of dweight are kept in memory.
+template <class IO, class RES>
+__global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdProblem p, float* parts) {
+  using raw = typename IO::raw;
+  using res_raw = typename RES::raw;
+  __shared__ float sums[2][2][kMaxWaves];
+  const int dim = static_cast<int>(p.dim), first = static_cast<int>(threadIdx.x) * kPiece;
+  float* part = parts + static_cast<int64_t>(blockIdx.x) * dim;
+  const float n = static_cast<float>(dim);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const res_raw* sr = static_cast<const res_raw*>(p.sum) + row * p.ssum;
+    const raw* yr = static_cast<const raw*>(p.dout) + row * p.so;
+    float both[2] = {0.0f, 0.0f};
+    for (int d = first; d < dim; d += kRegDim) {
+      Row8<RES> s;
+      Row8<IO> dy;
+      Row8<F32Io> w;
+      load8(s, sr, d, dim);
+      load8(dy, yr, d, dim);
+      load8(w, p.weight, d, dim);
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) {
+        both[0] = fmaf(s.get(j), s.get(j), both[0]);
+        both[1] = fmaf(s.get(j), w.get(j) * dy.get(j), both[1]);
+      }
+    }
+    over_block<AddOp>(both, sums[turn]);
+    const float rstd = rstd_of(both[0], n, p.eps), mean = both[1] * rstd / n;
+    for (int d = first; d < dim; d += kRegDim) {
+      Row8<RES> s, ds;
+      Row8<IO> dy, dx;
+      Row8<F32Io> w, dw;
+      load8(s, sr, d, dim);
+      load8(dy, yr, d, dim);
+      load8(w, p.weight, d, dim);
+      if (p.dsum) load8(ds, static_cast<const res_raw*>(p.dsum) + row * p.sdsum, d, dim);
+      if (row != blockIdx.x) load8(dw, part, d, dim);
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) {
+        const float norm = s.get(j) * rstd, g = dy.get(j);
+        dw.set(j, fmaf(g, norm, row != blockIdx.x ? dw.get(j) : 0.0f));
+        float v = rstd * fmaf(-norm, mean, w.get(j) * g);
+        if (p.dsum) v += ds.get(j);
+        s.set(j, v);
+        dx.set(j, v);
+      }
+      store8(s, static_cast<res_raw*>(p.dresidual) + row * p.sdres, d, dim);
+      if (p.dx) store8(dx, static_cast<raw*>(p.dx) + row * p.sdx, d, dim);
+      store8(dw, part, d, dim);
+    }
+  }
+}
+
+// Threads of a row: one piece each, in whole waves.
+unsigned threads_of(int64_t dim) {
+  const int64_t waves = (dim + 64 * kPiece - 1) / (64 * kPiece);
+  return static_cast<unsigned>(64 * (waves < kMaxWaves ? waves : kMaxWaves));
+}
+
+constexpr int64_t kWavesPerCu = 20;  // of one launch's workgroups
+constexpr int64_t kBwdWavesPerCu = 10;
+
+unsigned grid_of(int64_t rows, int64_t dim, int64_t waves_per_cu) {
+  const int64_t waves = threads_of(dim) / 64, groups = (waves_per_cu + waves - 1) / waves * device_cu_count();
+  return static_cast<unsigned>(rows < groups ? rows : groups);
+}
+
+template <class IO, class RES>
+hipError_t launch_types(const NormProblem& p, hipStream_t stream) {
+  const dim3 grid(grid_of(p.rows, p.dim, kWavesPerCu)), block(threads_of(p.dim));
+  if (p.dim > kRegDim)
+    hipLaunchKernelGGL((norm_wide_kernel<IO, RES>), grid, block, 0, stream, p);
+  else if (!p.scale)
+    hipLaunchKernelGGL((norm_kernel<IO, RES, kIo>), grid, block, 0, stream, p);
+  else if (p.group)
+    hipLaunchKernelGGL((norm_kernel<IO, RES, kGroupScale>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((norm_kernel<IO, RES, kRowScale>), grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+
+template <class IO, class RES>
+hipError_t launch_types(const NormBwdProblem& p, unsigned groups, float* parts, hipStream_t stream) {
+  const dim3 grid(groups), block(threads_of(p.dim));
+  if (p.dim > kRegDim)
+    hipLaunchKernelGGL((norm_bwd_wide_kernel<IO, RES>), grid, block, 0, stream, p, parts);
+  else
+    hipLaunchKernelGGL((norm_bwd_kernel<IO, RES>), grid, block, 0, stream, p, parts);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_norm(const NormProblem& p, hipStream_t stream) {
-  hipLaunchKernelGGL(norm_kernel, dim3(static_cast<unsigned>(p.rows < kMaxGrid ? p.rows : kMaxGrid)), dim3(kThreads), 0, stream, p);
-  return hipGetLastError();
+  if (p.io == kIoF32) return launch_types<F32Io, F32Io>(p, stream);
+  if (p.res == kIoF32) return launch_types<Bf16Io, F32Io>(p, stream);
+  return launch_types<Bf16Io, Bf16Io>(p, stream);
 }
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t dim) {
-  const int64_t parts = rows < kParts ? rows : kParts;
-  return (static_cast<size_t>(parts * dim) * 4 + 255) / 256 * 256;
+  if (rows == 0 || dim == 0) return 0;
+  return (static_cast<size_t>(grid_of(rows, dim, kBwdWavesPerCu)) * dim * 4 + 255) / 256 * 256;
 }
 
 hipError_t launch_norm_bwd(const NormBwdProblem& p, void* workspace, hipStream_t stream) {
-  const int64_t n = p.rows < kParts ? p.rows : kParts;
+  const unsigned groups = p.rows > 0 ? grid_of(p.rows, p.dim, kBwdWavesPerCu) : 0;
   float* parts = static_cast<float*>(workspace);
-  if (n > 0) {
-    hipLaunchKernelGGL(norm_bwd_kernel, dim3(static_cast<unsigned>(n)), dim3(kThreads), 0, stream, p, parts);
-    const hipError_t e = hipGetLastError();
+  if (groups > 0) {
+    const hipError_t e = p.io == kIoF32    ? launch_types<F32Io, F32Io>(p, groups, parts, stream)
+                         : p.res == kIoF32 ? launch_types<Bf16Io, F32Io>(p, groups, parts, stream)
+                                           : launch_types<Bf16Io, Bf16Io>(p, groups, parts, stream);
     if (e != hipSuccess) return e;
   }
-  return launch_colsum(parts, n, p.dim, StoreFlat{p.dweight}, stream);
+  return launch_colsum(parts, groups, p.dim, StoreFlat{p.dweight}, stream);
 }
 
 }  // namespace mscan
