@@ -8,27 +8,38 @@
 
 namespace mscan {
 
-constexpr int kColsumCols = 64;    // columns per workgroup, one per lane
-constexpr int kColsumWaves = 16;   // waves per workgroup, each with its own rows
+constexpr int kColsumCols = 32;    // columns per workgroup: one 128-byte piece of a row
+constexpr int kColsumRuns = 32;    // threads per column, each with its own rows
+constexpr int kColsumAhead = 8;    // loads in flight per thread
 
-// parts (rows, cols) -> out[column]; Store(column, sum) places it. Each wave
-// adds rows w, w + 16, ... in that order and wave 0 adds the waves' sums in
-// order, so the result does not depend on how the waves run.
+// parts (rows, cols) -> out[column]; Store(column, sum) places it. Thread k of a
+// column adds rows k, k + 32, ... in that order and one thread adds the 32 sums
+// in order, so the result does not depend on how the waves run.
 template <class Store>
-__global__ __launch_bounds__(kColsumCols* kColsumWaves) void colsum_kernel(const float* parts, int64_t rows,
-                                                                           int64_t cols, Store store) {
-  __shared__ float sums[kColsumWaves][kColsumCols];
-  const int lane = threadIdx.x % kColsumCols, wave = threadIdx.x / kColsumCols;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kColsumCols + lane;
+__global__ __launch_bounds__(kColsumCols* kColsumRuns) void colsum_kernel(const float* parts, int64_t rows,
+                                                                          int64_t cols, Store store) {
+  __shared__ float sums[kColsumRuns][kColsumCols + 1];
+  const int col = threadIdx.x % kColsumCols, run = threadIdx.x / kColsumCols;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kColsumCols + col;
   float s = 0.0f;
-  if (c < cols)
-    for (int64_t r = wave; r < rows; r += kColsumWaves) s += parts[r * cols + c];
-  sums[wave][lane] = s;
+  if (c < cols) {
+    const float* p = parts + c;
+    int64_t r = run;
+    for (; r + (kColsumAhead - 1) * kColsumRuns < rows; r += kColsumAhead * kColsumRuns) {
+      float v[kColsumAhead];
+#pragma unroll
+      for (int k = 0; k < kColsumAhead; ++k) v[k] = p[(r + k * kColsumRuns) * cols];
+#pragma unroll
+      for (int k = 0; k < kColsumAhead; ++k) s += v[k];
+    }
+    for (; r < rows; r += kColsumRuns) s += p[r * cols];
+  }
+  sums[run][col] = s;
   __syncthreads();
-  if (wave == 0 && c < cols) {
+  if (run == 0 && c < cols) {
     float t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kColsumWaves; ++k) t += sums[k][lane];
+    for (int k = 0; k < kColsumRuns; ++k) t += sums[k][col];
     store(c, t);
   }
 }
@@ -41,7 +52,7 @@ struct StoreFlat {
 template <class Store>
 hipError_t launch_colsum(const float* parts, int64_t rows, int64_t cols, Store store, hipStream_t stream) {
   hipLaunchKernelGGL((colsum_kernel<Store>), dim3(static_cast<unsigned>((cols + kColsumCols - 1) / kColsumCols)),
-                     dim3(kColsumCols * kColsumWaves), 0, stream, parts, rows, cols, store);
+                     dim3(kColsumCols * kColsumRuns), 0, stream, parts, rows, cols, store);
   return hipGetLastError();
 }
 

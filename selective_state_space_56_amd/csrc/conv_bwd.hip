@@ -10,76 +10,133 @@ namespace mscan {
 namespace {
 
 constexpr int kThreads = 64;
-constexpr int kSpan = 64;  // time steps per thread
+constexpr int kVec = 2;    // channels per thread (1 where there is one)
+constexpr int kGroup = 8;  // steps whose loads are in flight together
 
-// One channel of one batch row per thread, kSpan steps: v and dv are formed in
+// V channels of one batch row per thread, `span` steps: v and dv are formed in
 // time order and kept for W steps; a step's dx is ready W - 1 steps later, so a
-// span reads W - 1 steps past its end (and those add nothing to its dw).
-template <class IO, int W>
-__global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdProblem p, float* parts) {
+// span reads W - 1 steps past its end (and those add nothing to its dw). The
+// next group's loads are in flight while the current group is computed.
+// Threads past the last channel take the last V channels: they compute what
+// their owner does, and what both write is the same.
+template <class IO, int W, int V>
+__global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdProblem p, int span, float* parts) {
   using raw = typename IO::raw;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (c >= p.dim) return;
+  const int64_t own = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * V;
+  const int64_t c = own < p.dim - V ? own : p.dim - V;
   const int64_t b = blockIdx.z;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * kSpan;
-  const int64_t t1 = t0 + kSpan < p.seqlen ? t0 + kSpan : p.seqlen;
-  const raw* xin = static_cast<const raw*>(p.xin);
-  const raw* sin = static_cast<const raw*>(p.state_in);
-  float w[W], dw[W], x[W], dv[W];  // x[j] = input t - (W-1) + j, dv[j] = dv at t - j
-  const float bias = p.bias ? p.bias[c] : 0.0f;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * span;
+  const int64_t t1 = t0 + span < p.seqlen ? t0 + span : p.seqlen;
+  const raw* xin = static_cast<const raw*>(p.xin) + b * p.seqlen * p.dim + c;
+  const raw* dout = static_cast<const raw*>(p.dout) + b * p.seqlen * p.dim + c;
+  raw* dxin = static_cast<raw*>(p.dxin) + b * p.seqlen * p.dim + c;
+  const int64_t state = (b * p.dim + c) * (W - 1);
+  float w[W][V], dw[W][V], bias[V], db[V];
+  float x[W][V], dv[W][V];  // x[j] = input t - (W-1) + j, dv[j] = dv at t - j
 #pragma unroll
-  for (int j = 0; j < W; ++j) {
-    w[j] = p.weight[c * W + j];
-    dw[j] = 0.0f;
-    x[j] = 0.0f;
-    dv[j] = 0.0f;
+  for (int k = 0; k < V; ++k) {
+    bias[k] = p.bias ? p.bias[c + k] : 0.0f;
+    db[k] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      w[j][k] = p.weight[(c + k) * W + j];
+      dw[j][k] = dv[j][k] = x[j][k] = 0.0f;
+    }
   }
-  const auto input = [&](int64_t t) {
-    if (t >= 0) return IO::load(xin + (b * p.seqlen + t) * p.dim + c);
-    return sin ? IO::load(sin + (b * p.dim + c) * (W - 1) + (W - 1) + t) : 0.0f;
-  };
-  float db = 0.0f;
+  // the W - 1 inputs before the span
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) x[j + 1] = input(t0 - (W - 1) + j);
-  // steps t0 .. t1 + W - 2: the inputs at t - (W-1) get their gradient at step t.
+  for (int j = 0; j < W - 1; ++j) {
+    const int64_t t = t0 - (W - 1) + j;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (t >= 0)
+        x[j + 1][k] = IO::load(xin + t * p.dim + k);
+      else if (p.state_in)
+        x[j + 1][k] = IO::load(static_cast<const raw*>(p.state_in) + state + k * (W - 1) + (W - 1) + t);
+    }
+  }
+  // steps t0 .. end - 1: the inputs at t - (W-1) get their gradient at step t.
   // The first span also covers the state's inputs, the last those up to the end.
-  for (int64_t t = t0; t < t1 + W - 1; ++t) {
+  const int64_t end = t1 + W - 1;
+  Piece<IO, V> xr[kGroup], yr[kGroup];
+  const auto load = [&](int64_t t) {
 #pragma unroll
-    for (int j = 0; j + 1 < W; ++j) x[j] = x[j + 1];
+    for (int i = 0; i < kGroup; ++i) {
+      const int64_t at = (t + i < p.seqlen ? t + i : p.seqlen - 1) * p.dim;  // past the end: not used
+      xr[i].load(xin + at);
+      yr[i].load(dout + at);
+    }
+  };
+  if (p.seqlen > 0) load(t0);
+  for (int64_t t = t0; t < end; t += kGroup) {
+    Piece<IO, V> x0[kGroup], y0[kGroup];
 #pragma unroll
-    for (int j = W - 1; j > 0; --j) dv[j] = dv[j - 1];
-    dv[0] = 0.0f;
-    if (t < p.seqlen) {
-      x[W - 1] = input(t);
-      float v = bias;
+    for (int i = 0; i < kGroup; ++i) {
+      x0[i] = xr[i];
+      y0[i] = yr[i];
+    }
+    if (t + kGroup < end && p.seqlen > 0) load(t + kGroup);
 #pragma unroll
-      for (int j = 0; j < W; ++j) v = fmaf(w[j], x[j], v);
-      const float sig = sigmoid_f(v);
-      dv[0] = IO::load(static_cast<const raw*>(p.dout) + (b * p.seqlen + t) * p.dim + c) * sig *
-              fmaf(v, 1.0f - sig, 1.0f);
-      if (t < t1) {
-        db += dv[0];
+    for (int i = 0; i < kGroup; ++i) {
+      const int64_t now = t + i, at = now - (W - 1);
+      if (now >= end) break;
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[j] = fmaf(dv[0], x[j], dw[j]);
+      for (int k = 0; k < V; ++k) {
+#pragma unroll
+        for (int j = 0; j + 1 < W; ++j) x[j][k] = x[j + 1][k];
+#pragma unroll
+        for (int j = W - 1; j > 0; --j) dv[j][k] = dv[j - 1][k];
+        dv[0][k] = 0.0f;
+      }
+      if (now < p.seqlen) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          x[W - 1][k] = x0[i].get(k);
+          float v = bias[k];
+#pragma unroll
+          for (int j = 0; j < W; ++j) v = fmaf(w[j][k], x[j][k], v);
+          const float sig = sigmoid_f(v);
+          dv[0][k] = y0[i].get(k) * sig * fmaf(v, 1.0f - sig, 1.0f);
+        }
+        if (now < t1)
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            db[k] += dv[0][k];
+#pragma unroll
+            for (int j = 0; j < W; ++j) dw[j][k] = fmaf(dv[0][k], x[j][k], dw[j][k]);
+          }
+      }
+      if (at < t0 && blockIdx.y > 0) continue;  // the span before writes it
+      float d[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        d[k] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) d[k] = fmaf(w[j][k], dv[j][k], d[k]);
+      }
+      // the forward's last W - 1 inputs are its state_out
+      const int64_t slot = at - (p.seqlen - (W - 1));
+      if (W > 1 && slot >= 0 && p.dstate_out)
+#pragma unroll
+        for (int k = 0; k < V; ++k) d[k] += p.dstate_out[state + k * (W - 1) + slot];
+      if (at >= 0) {
+        Piece<IO, V> dx;
+#pragma unroll
+        for (int k = 0; k < V; ++k) dx.set(k, d[k]);
+        dx.store(dxin + at * p.dim);
+      } else if (p.dstate_in) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) p.dstate_in[state + k * (W - 1) + (W - 1) + at] = d[k];
       }
     }
-    const int64_t at = t - (W - 1);  // this span's own inputs only; the first span's state inputs too
-    if (at < t0 && blockIdx.y > 0) continue;
-    float d = 0.0f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) d = fmaf(w[j], dv[j], d);
-    // the forward's last W - 1 inputs are its state_out
-    const int64_t slot = at - (p.seqlen - (W - 1));
-    if (W > 1 && slot >= 0 && p.dstate_out) d += p.dstate_out[(b * p.dim + c) * (W - 1) + slot];
-    if (at >= 0)
-      static_cast<raw*>(p.dxin)[(b * p.seqlen + at) * p.dim + c] = IO::from_f32(d);
-    else if (p.dstate_in)
-      p.dstate_in[(b * p.dim + c) * (W - 1) + (W - 1) + at] = d;
   }
-  float* part = parts + (b * gridDim.y + blockIdx.y) * (W + 1) * p.dim;
+  float* part = parts + (b * gridDim.y + blockIdx.y) * (W + 1) * p.dim + c;
 #pragma unroll
-  for (int j = 0; j < W; ++j) part[j * p.dim + c] = dw[j];
-  part[W * p.dim + c] = db;
+  for (int k = 0; k < V; ++k) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) part[j * p.dim + k] = dw[j][k];
+    part[W * p.dim + k] = db[k];
+  }
 }
 
 // column j * dim + c of the parts: tap j's sum, or the bias's for j = width
@@ -97,35 +154,55 @@ struct StoreTaps {
   }
 };
 
-int64_t spans_of(int64_t seqlen) { return seqlen > 0 ? (seqlen + kSpan - 1) / kSpan : 1; }
+// Steps per thread: 64, and fewer, down to 16, while that gives fewer than four
+// waves per compute unit. (8 x 2048 x 5120 bf16, 20480 waves of 32 to 128 steps:
+// 124 to 126 us; 3 x 301 x 771 fp32: 39 us at 128 steps, 23 at 64.)
+int span_of(int64_t batch, int64_t seqlen, int64_t dim) {
+  const int64_t groups = batch * ((dim + kThreads * kVec - 1) / (kThreads * kVec));
+  int span = 64;
+  while (span > 16 && groups * ((seqlen + span - 1) / span) < 4 * device_cu_count()) span /= 2;
+  return span;
+}
 
-template <class IO>
+int64_t spans_of(int64_t batch, int64_t seqlen, int64_t dim) {
+  const int span = span_of(batch, seqlen, dim);
+  return seqlen > 0 ? (seqlen + span - 1) / span : 1;
+}
+
+template <class IO, int V>
 hipError_t launch_io(const ConvBwdProblem& p, float* parts, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((p.dim + kThreads - 1) / kThreads),
-                  static_cast<unsigned>(spans_of(p.seqlen)), static_cast<unsigned>(p.batch));
+  const dim3 grid(static_cast<unsigned>((p.dim + kThreads * V - 1) / (kThreads * V)),
+                  static_cast<unsigned>(spans_of(p.batch, p.seqlen, p.dim)), static_cast<unsigned>(p.batch));
+  const int span = span_of(p.batch, p.seqlen, p.dim);
   switch (p.width) {
-    case 1: hipLaunchKernelGGL((conv_bwd_kernel<IO, 1>), grid, dim3(kThreads), 0, stream, p, parts); break;
-    case 2: hipLaunchKernelGGL((conv_bwd_kernel<IO, 2>), grid, dim3(kThreads), 0, stream, p, parts); break;
-    case 3: hipLaunchKernelGGL((conv_bwd_kernel<IO, 3>), grid, dim3(kThreads), 0, stream, p, parts); break;
-    case 4: hipLaunchKernelGGL((conv_bwd_kernel<IO, 4>), grid, dim3(kThreads), 0, stream, p, parts); break;
+    case 1: hipLaunchKernelGGL((conv_bwd_kernel<IO, 1, V>), grid, dim3(kThreads), 0, stream, p, span, parts); break;
+    case 2: hipLaunchKernelGGL((conv_bwd_kernel<IO, 2, V>), grid, dim3(kThreads), 0, stream, p, span, parts); break;
+    case 3: hipLaunchKernelGGL((conv_bwd_kernel<IO, 3, V>), grid, dim3(kThreads), 0, stream, p, span, parts); break;
+    case 4: hipLaunchKernelGGL((conv_bwd_kernel<IO, 4, V>), grid, dim3(kThreads), 0, stream, p, span, parts); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
 }
 
+template <class IO>
+hipError_t launch_dim(const ConvBwdProblem& p, float* parts, hipStream_t stream) {
+  if (p.dim < kVec) return launch_io<IO, 1>(p, parts, stream);
+  return launch_io<IO, kVec>(p, parts, stream);
+}
+
 }  // namespace
 
 size_t conv_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int width) {
-  return (static_cast<size_t>(batch * spans_of(seqlen) * (width + 1) * dim) * 4 + 255) / 256 * 256;
+  return (static_cast<size_t>(batch * spans_of(batch, seqlen, dim) * (width + 1) * dim) * 4 + 255) / 256 * 256;
 }
 
 hipError_t launch_conv_bwd(const ConvBwdProblem& p, void* workspace, hipStream_t stream) {
   float* parts = static_cast<float*>(workspace);
   if (p.batch > 0) {
-    const hipError_t e = p.io == kIoBf16 ? launch_io<Bf16Io>(p, parts, stream) : launch_io<F32Io>(p, parts, stream);
+    const hipError_t e = p.io == kIoBf16 ? launch_dim<Bf16Io>(p, parts, stream) : launch_dim<F32Io>(p, parts, stream);
     if (e != hipSuccess) return e;
   }
-  return launch_colsum(parts, p.batch * spans_of(p.seqlen), (p.width + 1) * p.dim,
+  return launch_colsum(parts, p.batch * spans_of(p.batch, p.seqlen, p.dim), (p.width + 1) * p.dim,
                        StoreTaps{p.dweight, p.dbias, p.dim, p.width}, stream);
 }
 

@@ -544,21 +544,61 @@ __global__ __launch_bounds__(kBwdThreads, 2) void gated_bwd_kernel(GatedBwdProbl
     }
 }
 
-// One decode token per (batch row, channel).
+constexpr int kTokenVec = 4;    // channels per thread
+constexpr int kTokenRows = 4;   // batch rows per thread, one after the other
+
+// One decode token: kTokenVec channels of kTokenRows batch rows per thread.
+// Bound by HBM: state in and out, three inputs, one output.
 template <class IO>
-__global__ __launch_bounds__(256) void gated_update_kernel(GatedUpdateProblem p) {
+__global__ __launch_bounds__(kLanes) void gated_update_kernel(GatedUpdateProblem p) {
   using raw = typename IO::raw;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= p.batch * p.dim) return;
-  const int64_t b = i / p.dim, c = i % p.dim;
-  const float x = IO::load(static_cast<const raw*>(p.x) + b * p.sx + c);
-  const float sr = sigmoid_f(IO::load(static_cast<const raw*>(p.r) + b * p.sr + c));
-  const float sg = sigmoid_f(IO::load(static_cast<const raw*>(p.g) + b * p.sg + c));
-  float a;
-  const float w = __builtin_amdgcn_sqrtf(decay_gap(p.A[c] * kLog2e * sr, a));
-  const float h = fmaf(a, p.state[i], w * (sg * x));
-  p.state[i] = h;
-  static_cast<raw*>(p.out)[b * p.so + c] = IO::from_f32(h);
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * kLanes + threadIdx.x) * kTokenVec;
+  if (c >= p.dim) return;
+  const int n = p.dim - c < kTokenVec ? static_cast<int>(p.dim - c) : kTokenVec;
+  const auto load = [&](auto& to, const auto* from) {
+    if (n == kTokenVec)
+      to.load(from);
+    else
+      to.load_some(from, n);
+  };
+  const auto store = [&](const auto& from, auto* to) {
+    if (n == kTokenVec)
+      from.store(to);
+    else
+      from.store_some(to, n);
+  };
+  Piece<F32Io, kTokenVec> A;
+  load(A, p.A + c);
+  for (int64_t b0 = static_cast<int64_t>(blockIdx.y) * kTokenRows; b0 < p.batch;
+       b0 += static_cast<int64_t>(gridDim.y) * kTokenRows) {
+    Piece<IO, kTokenVec> x[kTokenRows], r[kTokenRows], g[kTokenRows];
+    Piece<F32Io, kTokenVec> h[kTokenRows];
+#pragma unroll
+    for (int i = 0; i < kTokenRows; ++i) {
+      const int64_t b = b0 + i;
+      if (b >= p.batch) break;
+      load(h[i], p.state + b * p.dim + c);
+      load(x[i], static_cast<const raw*>(p.x) + b * p.sx + c);
+      load(r[i], static_cast<const raw*>(p.r) + b * p.sr + c);
+      load(g[i], static_cast<const raw*>(p.g) + b * p.sg + c);
+    }
+#pragma unroll
+    for (int i = 0; i < kTokenRows; ++i) {
+      const int64_t b = b0 + i;
+      if (b >= p.batch) break;
+      Piece<IO, kTokenVec> y;
+#pragma unroll
+      for (int v = 0; v < kTokenVec; ++v) {
+        float a;
+        const float w = __builtin_amdgcn_sqrtf(decay_gap(A.get(v) * kLog2e * sigmoid_f(r[i].get(v)), a));
+        const float next = fmaf(a, h[i].get(v), w * (sigmoid_f(g[i].get(v)) * x[i].get(v)));
+        h[i].set(v, next);
+        y.set(v, next);
+      }
+      store(h[i], p.state + b * p.dim + c);
+      store(y, static_cast<raw*>(p.out) + b * p.so + c);
+    }
+  }
 }
 
 Order order_of(int64_t batch, int64_t seqlen, int64_t dim, int V, int64_t span) {
@@ -658,11 +698,13 @@ hipError_t launch_gated_bwd(const GatedBwdProblem& p, void* workspace, hipStream
 }
 
 hipError_t launch_gated_update(const GatedUpdateProblem& p, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((p.batch * p.dim + 255) / 256));
+  const int64_t rows = (p.batch + kTokenRows - 1) / kTokenRows;
+  const dim3 grid(static_cast<unsigned>((p.dim + kLanes * kTokenVec - 1) / (kLanes * kTokenVec)),
+                  static_cast<unsigned>(rows < 65535 ? rows : 65535));
   if (p.io == kIoBf16)
-    hipLaunchKernelGGL((gated_update_kernel<Bf16Io>), grid, dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((gated_update_kernel<Bf16Io>), grid, dim3(kLanes), 0, stream, p);
   else
-    hipLaunchKernelGGL((gated_update_kernel<F32Io>), grid, dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((gated_update_kernel<F32Io>), grid, dim3(kLanes), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -261,7 +261,7 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormProblem p) {
 // (s^2 and s u, u = w dout) in one reduction, then the row's gradient from the
 // registers. Every workgroup keeps its rows' sum of dout s rstd: one row of parts.
 template <class IO, class RES>
-__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdProblem p, float* parts) {
+__global__ __launch_bounds__(1024, 5) void norm_bwd_kernel(NormBwdProblem p, float* parts) {
   using raw = typename IO::raw;
   using res_raw = typename RES::raw;
   __shared__ float sums[2][2][kMaxWaves];
@@ -370,17 +370,18 @@ unsigned threads_of(int64_t dim) {
   return static_cast<unsigned>(64 * (waves < kMaxWaves ? waves : kMaxWaves));
 }
 
-constexpr int64_t kWavesPerCu = 20;  // of one launch's workgroups
-constexpr int64_t kBwdWavesPerCu = 10;
-
-unsigned grid_of(int64_t rows, int64_t dim, int64_t waves_per_cu) {
-  const int64_t waves = threads_of(dim) / 64, groups = (waves_per_cu + waves - 1) / waves * device_cu_count();
-  return static_cast<unsigned>(rows < groups ? rows : groups);
+// Workgroups of a launch: what runs at once (of the backward 4 waves per SIMD
+// and what packs into them), each with the same number of rows, but for the last.
+unsigned grid_of(int64_t rows, int64_t dim, bool backward) {
+  const int64_t waves = threads_of(dim) / 64;
+  const int64_t per_cu = backward ? 16 / waves : (20 + waves - 1) / waves;
+  const int64_t most = per_cu * device_cu_count(), each = (rows + most - 1) / most;
+  return static_cast<unsigned>((rows + each - 1) / each);
 }
 
 template <class IO, class RES>
 hipError_t launch_types(const NormProblem& p, hipStream_t stream) {
-  const dim3 grid(grid_of(p.rows, p.dim, kWavesPerCu)), block(threads_of(p.dim));
+  const dim3 grid(grid_of(p.rows, p.dim, false)), block(threads_of(p.dim));
   if (p.dim > kRegDim)
     hipLaunchKernelGGL((norm_wide_kernel<IO, RES>), grid, block, 0, stream, p);
   else if (!p.scale)
@@ -412,11 +413,11 @@ hipError_t launch_norm(const NormProblem& p, hipStream_t stream) {
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t dim) {
   if (rows == 0 || dim == 0) return 0;
-  return (static_cast<size_t>(grid_of(rows, dim, kBwdWavesPerCu)) * dim * 4 + 255) / 256 * 256;
+  return (static_cast<size_t>(grid_of(rows, dim, true)) * dim * 4 + 255) / 256 * 256;
 }
 
 hipError_t launch_norm_bwd(const NormBwdProblem& p, void* workspace, hipStream_t stream) {
-  const unsigned groups = p.rows > 0 ? grid_of(p.rows, p.dim, kBwdWavesPerCu) : 0;
+  const unsigned groups = p.rows > 0 ? grid_of(p.rows, p.dim, true) : 0;
   float* parts = static_cast<float*>(workspace);
   if (groups > 0) {
     const hipError_t e = p.io == kIoF32    ? launch_types<F32Io, F32Io>(p, groups, parts, stream)
