@@ -85,16 +85,25 @@ def _on(dev):
     return _here if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
+# the current stream's handle without a Stream object around it (1.7 us less per
+# call, of about 9 for a small one), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev.index) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _plain(t, shape, dtype, dev):
+    """Whether t is a contiguous tensor of this kind."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.device == dev)
 
 
 def _rows(t, name, shape, dtype, dev, rows_axis):
     """_row_stride of a tensor that may be a column slice, without its walk
     over the axes for the contiguous tensor of the right kind; 0 for None."""
-    if t is None:
-        return 0
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+    if t is None or _plain(t, shape, dtype, dev):
         return 0
     s = _row_stride(t, name, shape, dtype, dev, rows_axis)
     # rows apart by less than a row's length share elements: reading them is
@@ -105,8 +114,7 @@ def _rows(t, name, shape, dtype, dev, rows_axis):
 
 
 def _whole(t, name, shape, dtype, dev):
-    if t is not None and not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape
-                              and t.device == dev and t.is_contiguous()):
+    if t is not None and not _plain(t, shape, dtype, dev):
         _need(t, name, shape, dtype, dev)
 
 
