@@ -6,9 +6,9 @@
 
 namespace mscan {
 
-// V consecutive io values, as one access of V * sizeof(raw) bytes. gfx950's
-// global loads and stores take any alignment of the element's size, so rows of
-// odd lengths and odd first columns use the same path as aligned ones.
+// V consecutive io values, as one access of their size. gfx950's global loads
+// and stores take any alignment of the element's size, so rows of odd lengths
+// and odd first columns use the same path as aligned ones.
 template <class IO, int V>
 struct Piece {
   using raw = typename IO::raw;
@@ -26,8 +26,48 @@ struct Piece {
       if (k < n) p[k] = v[k];
   }
   __device__ __forceinline__ float get(int k) const { return IO::to_f32(v[k]); }
-  __device__ __forceinline__ void set(int k, float f) { v[k] = IO::from_f32(f); }
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = IO::from_f32(f[k]);
+  }
 };
+
+// bf16 in pairs: kept as the words that the access moves. (Held as single
+// values, a piece that lives on past a branch or a loop's end is taken apart as
+// soon as it arrives, so that every load is waited for where it was started.)
+template <int V>
+struct BfPiece {
+  static_assert(V % 2 == 0, "whole words");
+  using raw = uint16_t;
+  uint32_t w[V / 2];
+  __device__ __forceinline__ void load(const raw* p) { __builtin_memcpy(w, p, sizeof(w)); }
+  __device__ __forceinline__ void store(raw* p) const { __builtin_memcpy(p, w, sizeof(w)); }
+  __device__ __forceinline__ void load_some(const raw* p, int n) {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      const uint32_t low = 2 * k < n ? p[2 * k] : 0u, high = 2 * k + 1 < n ? p[2 * k + 1] : 0u;
+      w[k] = low | (high << 16);
+    }
+  }
+  __device__ __forceinline__ void store_some(raw* p, int n) const {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (k < n) p[k] = static_cast<uint16_t>(w[k / 2] >> (16 * (k % 2)));
+  }
+  __device__ __forceinline__ float get(int k) const {
+    return __uint_as_float(k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+  }
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k)
+      w[k] = static_cast<uint32_t>(Bf16Io::from_f32(f[2 * k])) |
+             (static_cast<uint32_t>(Bf16Io::from_f32(f[2 * k + 1])) << 16);
+  }
+};
+template <>
+struct Piece<Bf16Io, 2> : BfPiece<2> {};
+template <>
+struct Piece<Bf16Io, 8> : BfPiece<8> {};
 
 // 1 / (1 + e^-v): 0 and 1 at the infinities
 __device__ __forceinline__ float sigmoid_f(float v) { return hw_rcp(1.0f + hw_exp2(-v * kLog2e)); }

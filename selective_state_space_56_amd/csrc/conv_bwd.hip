@@ -121,8 +121,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdProblem p, in
         for (int k = 0; k < V; ++k) d[k] += p.dstate_out[state + k * (W - 1) + slot];
       if (at >= 0) {
         Piece<IO, V> dx;
-#pragma unroll
-        for (int k = 0; k < V; ++k) dx.set(k, d[k]);
+        dx.set(d);
         dx.store(dxin + at * p.dim);
       } else if (p.dstate_in) {
 #pragma unroll

@@ -298,10 +298,8 @@ __global__ __launch_bounds__(kFwdThreads) void gated_fwd_kernel(GatedProblem p, 
     for (int i = 0; i < kFwdSteps; ++i) {
       Piece<IO, V> y;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        h[v] = fmaf(a[i][v], h[v], u[i][v]);
-        y.set(v, h[v]);
-      }
+      for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], u[i][v]);
+      y.set(h);
       y.store(in_row(out, at.c));
       out += p.so;
     }
@@ -312,10 +310,8 @@ __global__ __launch_bounds__(kFwdThreads) void gated_fwd_kernel(GatedProblem p, 
     if (i >= steps) continue;
     Piece<IO, V> y;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = resets >> i & 1 ? u[i][v] : fmaf(a[i][v], h[v], u[i][v]);
-      y.set(v, h[v]);
-    }
+    for (int v = 0; v < V; ++v) h[v] = resets >> i & 1 ? u[i][v] : fmaf(a[i][v], h[v], u[i][v]);
+    y.set(h);
     y.store(in_row(out, at.c));
     out += p.so;
   }
@@ -415,7 +411,7 @@ __device__ __forceinline__ void bwd_grads(const GatedBwdProblem& p, const Place<
 #pragma unroll
   for (int i = kBwdSteps - 1; i >= 0; --i) {
     if (!PLAIN && i >= at.steps) continue;
-    Piece<IO, V> dx, dr, dg;
+    float xs[V], rs[V], gs[V];
     const bool on = !PLAIN && (resets >> i & 1);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -423,10 +419,14 @@ __device__ __forceinline__ void bwd_grads(const GatedBwdProblem& p, const Place<
       const float dvr = on ? 0.0f : lam * s.d[i][v] * s.sr[i][v];
       m[v] = on ? 0.0f : s.a[i][v] * lam;
       dA[v] += dvr;
-      dx.set(v, lp);
-      dg.set(v, lp * s.x[i].get(v) * (1.0f - s.sg[i][v]));
-      dr.set(v, dvr * rate[v] * (1.0f - s.sr[i][v]));
+      xs[v] = lp;
+      gs[v] = lp * s.x[i].get(v) * (1.0f - s.sg[i][v]);
+      rs[v] = dvr * rate[v] * (1.0f - s.sr[i][v]);
     }
+    Piece<IO, V> dx, dr, dg;
+    dx.set(xs);
+    dr.set(rs);
+    dg.set(gs);
     dx.store(in_row(dxp, at.c));
     dr.store(in_row(drp, at.c));
     dg.store(in_row(dgp, at.c));

@@ -141,10 +141,10 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormProblem p) {
     float s[kPiece], ss[1] = {0.0f};
     if (p.residual) {
 #pragma unroll
-      for (int j = 0; j < kPiece; ++j) {
-        r.set(j, x.get(j) + r.get(j));  // rounded to the stream's type here
-        s[j] = r.get(j);
-      }
+      for (int j = 0; j < kPiece; ++j) s[j] = x.get(j) + r.get(j);
+      r.set(s);  // rounded to the stream's type here
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) s[j] = r.get(j);
       store8(r, static_cast<res_raw*>(p.sum) + row * p.ssum, d, dim);
     } else {
 #pragma unroll
@@ -159,8 +159,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormProblem p) {
     for (int j = 0; j < kPiece; ++j) s[j] = s[j] * rstd * w.get(j);
     if constexpr (OUT == kIo) {
       Row8<IO> y;
-#pragma unroll
-      for (int j = 0; j < kPiece; ++j) y.set(j, s[j]);
+      y.set(s);
       store8(y, static_cast<raw*>(p.out) + row * p.so, d, dim);
     } else {
       // channels past the end are 0 and do not raise a maximum
@@ -200,10 +199,10 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormProblem p) {
         Row8<RES> r;
         load8(r, static_cast<const res_raw*>(p.residual) + row * p.sres, d, dim);
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) {
-          r.set(j, s[j] + r.get(j));
-          s[j] = r.get(j);
-        }
+        for (int j = 0; j < kPiece; ++j) s[j] += r.get(j);
+        r.set(s);
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) s[j] = r.get(j);
         store8(r, sr, d, dim);
       }
 #pragma unroll
@@ -249,8 +248,7 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormProblem p) {
         store_e4m3(y, kE4m3Max / top[0], static_cast<uint8_t*>(p.out) + row * p.so, d, dim);
       } else {
         Row8<IO> out;
-#pragma unroll
-        for (int j = 0; j < kPiece; ++j) out.set(j, y[j]);
+        out.set(y);
         store8(out, static_cast<raw*>(p.out) + row * p.so, d, dim);
       }
     }
@@ -269,7 +267,7 @@ __global__ __launch_bounds__(1024, 5) void norm_bwd_kernel(NormBwdProblem p, flo
   Row8<F32Io> w, dw;
   load8(w, p.weight, d, dim);
 #pragma unroll
-  for (int j = 0; j < kPiece; ++j) dw.set(j, 0.0f);
+  for (int j = 0; j < kPiece; ++j) dw.v[j] = 0.0f;
   Row8<RES> s, ds;
   Row8<IO> dy;
   const auto load = [&](int64_t row) {
@@ -294,16 +292,17 @@ __global__ __launch_bounds__(1024, 5) void norm_bwd_kernel(NormBwdProblem p, flo
     }
     over_block<AddOp>(both, sums[turn]);
     const float rstd = rstd_of(both[0], n, p.eps), mean = both[1] * rstd / n;
-    Row8<IO> dx;
+    float v[kPiece];
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) {
       const float norm = s0.get(j) * rstd, g = dy0.get(j);
-      dw.set(j, fmaf(g, norm, dw.get(j)));
-      float v = rstd * fmaf(-norm, mean, w.get(j) * g);
-      if (p.dsum) v += ds0.get(j);
-      s0.set(j, v);
-      dx.set(j, v);
+      dw.v[j] = fmaf(g, norm, dw.v[j]);
+      v[j] = rstd * fmaf(-norm, mean, w.get(j) * g);
+      if (p.dsum) v[j] += ds0.get(j);
     }
+    Row8<IO> dx;
+    s0.set(v);
+    dx.set(v);
     store8(s0, static_cast<res_raw*>(p.dresidual) + row * p.sdres, d, dim);
     if (p.dx) store8(dx, static_cast<raw*>(p.dx) + row * p.sdx, d, dim);
   }
@@ -348,15 +347,16 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdProblem p, f
       load8(w, p.weight, d, dim);
       if (p.dsum) load8(ds, static_cast<const res_raw*>(p.dsum) + row * p.sdsum, d, dim);
       if (row != blockIdx.x) load8(dw, part, d, dim);
+      float v[kPiece];
 #pragma unroll
       for (int j = 0; j < kPiece; ++j) {
         const float norm = s.get(j) * rstd, g = dy.get(j);
-        dw.set(j, fmaf(g, norm, row != blockIdx.x ? dw.get(j) : 0.0f));
-        float v = rstd * fmaf(-norm, mean, w.get(j) * g);
-        if (p.dsum) v += ds.get(j);
-        s.set(j, v);
-        dx.set(j, v);
+        dw.v[j] = fmaf(g, norm, row != blockIdx.x ? dw.v[j] : 0.0f);
+        v[j] = rstd * fmaf(-norm, mean, w.get(j) * g);
+        if (p.dsum) v[j] += ds.get(j);
       }
+      s.set(v);
+      dx.set(v);
       store8(s, static_cast<res_raw*>(p.dresidual) + row * p.sdres, d, dim);
       if (p.dx) store8(dx, static_cast<raw*>(p.dx) + row * p.sdx, d, dim);
       store8(dw, part, d, dim);
