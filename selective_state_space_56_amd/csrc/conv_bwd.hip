@@ -11,7 +11,7 @@ namespace {
 
 constexpr int kThreads = 64;
 constexpr int kVec = 2;    // channels per thread (1 where there is one)
-constexpr int kGroup = 8;  // steps whose loads are in flight together
+constexpr int kGroup = 4;  // steps whose loads are in flight together
 
 // V channels of one batch row per thread, `span` steps: v and dv are formed in
 // time order and kept for W steps; a step's dx is ready W - 1 steps later, so a
@@ -67,6 +67,44 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdProblem p, in
       yr[i].load(dout + at);
     }
   };
+  // the windows move on by a step
+  const auto shift = [&] {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+#pragma unroll
+      for (int j = 0; j + 1 < W; ++j) x[j][k] = x[j + 1][k];
+#pragma unroll
+      for (int j = W - 1; j > 0; --j) dv[j][k] = dv[j - 1][k];
+      dv[0][k] = 0.0f;
+    }
+  };
+  const auto output = [&](const Piece<IO, V>& in, const Piece<IO, V>& dy) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      x[W - 1][k] = in.get(k);
+      float v = bias[k];
+#pragma unroll
+      for (int j = 0; j < W; ++j) v = fmaf(w[j][k], x[j][k], v);
+      const float sig = sigmoid_f(v);
+      dv[0][k] = dy.get(k) * sig * fmaf(v, 1.0f - sig, 1.0f);
+    }
+  };
+  const auto sums = [&] {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      db[k] += dv[0][k];
+#pragma unroll
+      for (int j = 0; j < W; ++j) dw[j][k] = fmaf(dv[0][k], x[j][k], dw[j][k]);
+    }
+  };
+  const auto input_grad = [&](float (&d)[V]) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      d[k] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) d[k] = fmaf(w[j][k], dv[j][k], d[k]);
+    }
+  };
   if (p.seqlen > 0) load(t0);
   for (int64_t t = t0; t < end; t += kGroup) {
     Piece<IO, V> x0[kGroup], y0[kGroup];
@@ -76,44 +114,33 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdProblem p, in
       y0[i] = yr[i];
     }
     if (t + kGroup < end && p.seqlen > 0) load(t + kGroup);
+    // inside the span every step is an output's and its oldest input is the span's
+    if (t >= t0 + W - 1 && t + kGroup <= t1) {
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        float d[V];
+        shift();
+        output(x0[i], y0[i]);
+        sums();
+        input_grad(d);
+        Piece<IO, V> dx;
+        dx.set(d);
+        dx.store(dxin + (t + i - (W - 1)) * p.dim);
+      }
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) {
       const int64_t now = t + i, at = now - (W - 1);
       if (now >= end) break;
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-#pragma unroll
-        for (int j = 0; j + 1 < W; ++j) x[j][k] = x[j + 1][k];
-#pragma unroll
-        for (int j = W - 1; j > 0; --j) dv[j][k] = dv[j - 1][k];
-        dv[0][k] = 0.0f;
-      }
+      shift();
       if (now < p.seqlen) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          x[W - 1][k] = x0[i].get(k);
-          float v = bias[k];
-#pragma unroll
-          for (int j = 0; j < W; ++j) v = fmaf(w[j][k], x[j][k], v);
-          const float sig = sigmoid_f(v);
-          dv[0][k] = y0[i].get(k) * sig * fmaf(v, 1.0f - sig, 1.0f);
-        }
-        if (now < t1)
-#pragma unroll
-          for (int k = 0; k < V; ++k) {
-            db[k] += dv[0][k];
-#pragma unroll
-            for (int j = 0; j < W; ++j) dw[j][k] = fmaf(dv[0][k], x[j][k], dw[j][k]);
-          }
+        output(x0[i], y0[i]);
+        if (now < t1) sums();
       }
       if (at < t0 && blockIdx.y > 0) continue;  // the span before writes it
       float d[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        d[k] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) d[k] = fmaf(w[j][k], dv[j][k], d[k]);
-      }
+      input_grad(d);
       // the forward's last W - 1 inputs are its state_out
       const int64_t slot = at - (p.seqlen - (W - 1));
       if (W > 1 && slot >= 0 && p.dstate_out)
