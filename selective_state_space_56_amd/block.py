@@ -8,7 +8,6 @@ current.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import threading
 
@@ -77,14 +76,6 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-_here = contextlib.nullcontext()
-
-
-def _on(dev):
-    """A context in which `dev` is the current device."""
-    return _here if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
 # the current stream's handle without a Stream object around it (1.7 us less per
 # call, of about 9 for a small one), where this torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -92,6 +83,28 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(dev):
     return _raw_stream(dev.index) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _run(dev, f, *args):
+    """f(*args, the current stream of dev) with dev as the current device."""
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _stream(dev))
+    if st:
+        _check(_library(), st)
+
+
+def _workspace(dev, size, d):
+    """(workspace or None, its bytes) by the size function, which may go by the
+    current device's compute units."""
+    if dev.index == torch.cuda.current_device():
+        n = size(d)
+    else:
+        with torch.cuda.device(dev):
+            n = size(d)
+    return (torch.empty(n, dtype=torch.uint8, device=dev) if n else None), n
 
 
 def _plain(t, shape, dtype, dev):
@@ -177,12 +190,9 @@ def gated_scan_fwd(x, r, g, A, *, h0=None, reset=None, out=None, last_state=None
     _whole(last_state, "last_state", (batch, dim), F32, dev)
     marks = _new((batch, -(-L // CHECKPOINT), dim), F32, dev) if return_checkpoints else None
     d = ctypes.byref(GatedDesc(batch, L, dim, _IO[io], 0))
-    with _on(dev):
-        nbytes = lib.mamba_gated_scan_workspace_size(d)
-        ws = _new(nbytes, torch.uint8, dev) if nbytes else None
-        st = lib.mamba_gated_scan_fwd(d, _strides(GatedStrides, sx, sr, sg, so), _p(x), _p(r), _p(g), _p(A), _p(h0),
-                                      _p(reset), _p(out), _p(last_state), _p(marks), _p(ws), nbytes, _stream(dev))
-    _check(lib, st)
+    ws, nbytes = _workspace(dev, lib.mamba_gated_scan_workspace_size, d)
+    _run(dev, lib.mamba_gated_scan_fwd, d, _strides(GatedStrides, sx, sr, sg, so), _p(x), _p(r), _p(g), _p(A), _p(h0),
+         _p(reset), _p(out), _p(last_state), _p(marks), _p(ws), nbytes)
     return (out, last_state, marks) if return_checkpoints else (out, last_state)
 
 
@@ -213,16 +223,13 @@ def gated_scan_bwd(x, r, g, A, dout, checkpoints, *, reset=None, dlast=None, dx=
     sdx = _rows(dx, "dx", shape, io, dev, 1)
     sdr = _rows(dr, "dr", shape, io, dev, 1)
     sdg = _rows(dg, "dg", shape, io, dev, 1)
-    dA = _new((dim,), F32, dev)
+    dA = torch.empty_like(A)
     dh0 = _new((batch, dim), F32, dev) if want_dh0 else None
     d = ctypes.byref(GatedDesc(batch, L, dim, _IO[io], 0))
-    with _on(dev):
-        nbytes = lib.mamba_gated_scan_bwd_workspace_size(d)
-        ws = _new(nbytes, torch.uint8, dev) if nbytes else None
-        st = lib.mamba_gated_scan_bwd(d, _strides(GatedStrides, sx, sr, sg, so, sdx, sdr, sdg), _p(x), _p(r), _p(g),
-                                      _p(A), _p(reset), _p(checkpoints), _p(dout), _p(dlast), _p(dx), _p(dr), _p(dg),
-                                      _p(dA), _p(dh0), _p(ws), nbytes, _stream(dev))
-    _check(lib, st)
+    ws, nbytes = _workspace(dev, lib.mamba_gated_scan_bwd_workspace_size, d)
+    _run(dev, lib.mamba_gated_scan_bwd, d, _strides(GatedStrides, sx, sr, sg, so, sdx, sdr, sdg), _p(x), _p(r), _p(g),
+         _p(A), _p(reset), _p(checkpoints), _p(dout), _p(dlast), _p(dx), _p(dr), _p(dg), _p(dA), _p(dh0), _p(ws),
+         nbytes)
     return {"dx": dx, "dr": dr, "dg": dg, "dA": dA, "dh0": dh0}
 
 
@@ -242,11 +249,8 @@ def gated_update(state, x, r, g, A, *, out=None):
     if out is None:
         out = _new(shape, io, dev)
     so = _rows(out, "out", shape, io, dev, 0)
-    with _on(dev):
-        st = lib.mamba_gated_update(ctypes.byref(GatedDesc(batch, 1, dim, _IO[io], 0)),
-                                    _strides(GatedStrides, sx, sr, sg, so), _p(state), _p(x), _p(r), _p(g), _p(A),
-                                    _p(out), _stream(dev))
-    _check(lib, st)
+    _run(dev, lib.mamba_gated_update, ctypes.byref(GatedDesc(batch, 1, dim, _IO[io], 0)),
+         _strides(GatedStrides, sx, sr, sg, so), _p(state), _p(x), _p(r), _p(g), _p(A), _p(out))
     return out
 
 
@@ -279,10 +283,8 @@ def rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, out=None, sum=None):
     if out is None:
         out = _new(shape, io, dev)
     so = _rows(out, "out", shape, io, dev, 0)
-    with _on(dev):
-        st = lib.mamba_rmsnorm_fwd(ctypes.byref(d), _strides(NormStrides, *s, so), _p(x), _p(residual), _p(weight),
-                                   _p(out), _p(sum), _stream(dev))
-    _check(lib, st)
+    _run(dev, lib.mamba_rmsnorm_fwd, ctypes.byref(d), _strides(NormStrides, *s, so), _p(x), _p(residual), _p(weight),
+         _p(out), _p(sum))
     return out, sum
 
 
@@ -300,10 +302,8 @@ def rmsnorm_quant_fwd(x, weight, residual=None, *, eps=1e-6, group=0, out=None, 
     if scale is None:
         scale = _new(scales, F32, dev)
     _whole(scale, "scale", scales, F32, dev)
-    with _on(dev):
-        st = lib.mamba_rmsnorm_quant_fwd(ctypes.byref(d), _strides(NormStrides, *s, so), _p(x), _p(residual),
-                                         _p(weight), _p(out), _p(scale), _p(sum), _stream(dev))
-    _check(lib, st)
+    _run(dev, lib.mamba_rmsnorm_quant_fwd, ctypes.byref(d), _strides(NormStrides, *s, so), _p(x), _p(residual),
+         _p(weight), _p(out), _p(scale), _p(sum))
     return out, scale, sum
 
 
@@ -328,15 +328,11 @@ def rmsnorm_bwd(sum, weight, dout, *, ds=None, eps=1e-6, dresidual=None):
         dresidual = _new(shape, res, dev)
     sdr = _rows(dresidual, "dresidual", shape, res, dev, 0)
     dx = None if res is io else _new(shape, io, dev)
-    dweight = _new((shape[1],), F32, dev)
+    dweight = torch.empty_like(weight)
     d = ctypes.byref(NormDesc(shape[0], shape[1], 0, _IO[io], _IO[res], eps, 0))
-    with _on(dev):
-        nbytes = lib.mamba_rmsnorm_bwd_workspace_size(d)
-        ws = _new(nbytes, torch.uint8, dev) if nbytes else None
-        st = lib.mamba_rmsnorm_bwd(d, _strides(NormStrides, 0, 0, ssum, so, sds, sdr, 0), _p(sum), _p(weight),
-                                   _p(dout), _p(ds), _p(dresidual), _p(dx), _p(dweight), _p(ws), nbytes,
-                                   _stream(dev))
-    _check(lib, st)
+    ws, nbytes = _workspace(dev, lib.mamba_rmsnorm_bwd_workspace_size, d)
+    _run(dev, lib.mamba_rmsnorm_bwd, d, _strides(NormStrides, 0, 0, ssum, so, sds, sdr, 0), _p(sum), _p(weight),
+         _p(dout), _p(ds), _p(dresidual), _p(dx), _p(dweight), _p(ws), nbytes)
     return {"dx": dresidual if dx is None else dx, "dresidual": dresidual, "dweight": dweight}
 
 
@@ -361,14 +357,10 @@ def conv1d_bwd(xin, weight, dout, bias=None, state_in=None, *, dstate_out=None, 
     _whole(bias, "bias", (dim,), F32, dev)
     _whole(state_in, "state_in", state, io, dev)
     _whole(dstate_out, "dstate_out", state, F32, dev)
-    g = {"dxin": _new(shape, io, dev), "dweight": _new((dim, width), F32, dev), "dbias": _new((dim,), F32, dev),
+    g = {"dxin": torch.empty_like(xin), "dweight": torch.empty_like(weight), "dbias": _new((dim,), F32, dev),
          "dstate_in": _new(state, F32, dev) if want_dstate else None}
     d = ctypes.byref(ConvDesc(batch, L, dim, width, _IO[io], 0))
-    with _on(dev):
-        nbytes = lib.mamba_conv1d_bwd_workspace_size(d)
-        ws = _new(nbytes, torch.uint8, dev) if nbytes else None
-        st = lib.mamba_conv1d_bwd(d, _p(xin), _p(weight), _p(bias), _p(state_in), _p(dout), _p(dstate_out),
-                                  _p(g["dxin"]), _p(g["dweight"]), _p(g["dbias"]), _p(g["dstate_in"]), _p(ws), nbytes,
-                                  _stream(dev))
-    _check(lib, st)
+    ws, nbytes = _workspace(dev, lib.mamba_conv1d_bwd_workspace_size, d)
+    _run(dev, lib.mamba_conv1d_bwd, d, _p(xin), _p(weight), _p(bias), _p(state_in), _p(dout), _p(dstate_out),
+         _p(g["dxin"]), _p(g["dweight"]), _p(g["dbias"]), _p(g["dstate_in"]), _p(ws), nbytes)
     return g
