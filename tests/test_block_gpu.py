@@ -576,3 +576,140 @@ def test_two_streams_at_once(dev):
     for k, (w, o, d) in enumerate(got):
         assert all(torch.equal(p, q) for p, q in zip(w, o))
         assert all(torch.equal(d[n], wantd[k % 2][n]) for n in d)
+
+
+def test_offsets_past_32_bits(dev):
+    """Tensors of more than 2^31 elements: the end of a long sequence is what
+    a call on the end alone gives, from the state that enters it."""
+    L, dim, tail = 262144 + 65, 8200, 128 + 65
+    g = torch.Generator(device=dev).manual_seed(9)
+    x, r, i = (torch.randn((1, L, dim), generator=g, device=dev, dtype=torch.bfloat16) for _ in range(3))
+    A = -0.01 - torch.rand(dim, generator=g, device=dev)
+    assert x.numel() > 2 ** 31 and (L - tail) % 128 == 0
+    out, last, marks = gated_scan_fwd(x, r, i, A, return_checkpoints=True)
+    e = [t[:, -tail:].contiguous() for t in (x, r, i)]
+    o, h, m = gated_scan_fwd(*e, A, h0=marks[:, (L - tail) // CHECKPOINT].contiguous(), return_checkpoints=True)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:, -tail:], o) and torch.equal(last, h) and torch.equal(marks[:, -m.shape[1]:], m)
+    d = gated_scan_bwd(x, r, i, A, out, marks)
+    de = gated_scan_bwd(*e, A, o, m)
+    torch.cuda.synchronize()
+    for k in ("dx", "dr", "dg"):
+        assert torch.equal(d[k][:, -tail:], de[k]), k
+    del d, de, marks, r, i
+    w, b = torch.randn((dim, 4), generator=g, device=dev), torch.randn(dim, generator=g, device=dev)
+    dc = conv1d_bwd(x, w, out, b, want_dstate=False)
+    ec = conv1d_bwd(x[:, -tail:].contiguous(), w, out[:, -tail:].contiguous(), b,
+                    x[:, -tail - 3:-tail].transpose(1, 2).contiguous(), want_dstate=False)
+    torch.cuda.synchronize()
+    assert torch.equal(dc["dxin"][:, -tail + 3:], ec["dxin"][:, 3:])
+    y, _ = rmsnorm_fwd(x.view(L, dim), torch.ones(dim, device=dev))
+    ye, _ = rmsnorm_fwd(x.view(L, dim)[-tail:], torch.ones(dim, device=dev))
+    torch.cuda.synchronize()
+    assert torch.equal(y[-tail:], ye)
+
+
+def test_strides_past_32_bits(dev):
+    """Rows so far apart that offsets within a tile pass 32 bits."""
+    wide, dim, L = 1 << 26, 66, 37
+    room = torch.empty((1, L, wide), dtype=torch.bfloat16, device=dev)
+    v = _gated_inputs(dev, 1, L, dim, torch.bfloat16)
+    x, out = room[..., 5:5 + dim], room[..., wide - dim:]
+    x.copy_(v["x"])
+    _, last, marks = gated_scan_fwd(x, v["r"], v["g"], v["A"], out=out, return_checkpoints=True)
+    dx = room[..., wide // 2:wide // 2 + dim]
+    d = gated_scan_bwd(x, v["r"], v["g"], v["A"], v["dout"], marks, dx=dx)
+    torch.cuda.synchronize()
+    want = ref.gated(v["x"], v["r"], v["g"], v["A"], None, None, v["dout"])
+    assert_within("out", out, rounded(want["out"], torch.bfloat16))
+    assert_within("dx", dx, rounded(want["dx"], torch.bfloat16))
+    assert_within("dA", d["dA"], rounded(want["dA"], torch.float32))
+    rows = room[0]
+    y, _ = rmsnorm_fwd(rows[:, 5:5 + dim], torch.ones(dim, device=dev), out=rows[:, wide - dim:])
+    torch.cuda.synchronize()
+    assert_within("norm", y, rounded(ref.norm(v["x"][0], torch.ones(dim), None, 1e-6)["out"], torch.bfloat16))
+    st = torch.zeros((L, dim), device=dev)
+    o = gated_update(st, rows[:, 5:5 + dim], v["r"][0], v["g"][0], v["A"], out=rows[:, wide - dim:])
+    torch.cuda.synchronize()
+    one = ref.gated(v["x"][0][:, None], v["r"][0][:, None], v["g"][0][:, None], v["A"])
+    assert_within("token", o, rounded(tuple(t[:, 0] for t in one["out"]), torch.bfloat16))
+
+
+def test_gated_beside_other_work(dev):
+    """Workgroups that start late, because another stream fills the GPU, change nothing."""
+    v = _gated_inputs(dev, 4, 6000, 384, torch.bfloat16, resets=0.001)
+
+    def both():
+        out, last, marks = gated_scan_fwd(v["x"], v["r"], v["g"], v["A"], reset=v["reset"], return_checkpoints=True)
+        d = gated_scan_bwd(v["x"], v["r"], v["g"], v["A"], v["dout"], marks, reset=v["reset"])
+        return [out, last, marks] + [d[k] for k in ("dx", "dr", "dg", "dA", "dh0")]
+
+    want = both()
+    torch.cuda.synchronize()
+    side, a = torch.cuda.Stream(), torch.randn((4096, 4096), device=dev)
+    b = torch.empty((1 << 27,), device=dev)
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                a @ a
+                b.fill_(1.0)
+        got = both()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(want, got))
+
+
+def test_python_refusals(dev):
+    """What a call must not be given, by name, before anything is launched."""
+    from selective_state_space_56_amd.binding import MambaScanError
+    v = _gated_inputs(dev, 2, 10, 16, torch.float32)
+    x, r, g, A = v["x"], v["r"], v["g"], v["A"]
+    marks = torch.zeros((2, 1, 16), device=dev)
+    with pytest.raises(TypeError, match="r has dtype"):
+        gated_scan_fwd(x, r.bfloat16(), g, A)
+    with pytest.raises(ValueError, match="g has shape"):
+        gated_scan_fwd(x, r, g[:, :5], A)
+    with pytest.raises(ValueError, match="A has shape"):
+        gated_scan_fwd(x, r, g, A[:8])
+    with pytest.raises(ValueError, match="h0 is on cpu"):
+        gated_scan_fwd(x, r, g, A, h0=torch.zeros((2, 16)))
+    with pytest.raises(ValueError, match="reset has shape"):
+        gated_scan_fwd(x, r, g, A, reset=torch.zeros((2, 9), dtype=torch.bool, device=dev))
+    with pytest.raises(ValueError, match="must be contiguous"):
+        gated_scan_fwd(x, r, g, A, reset=torch.zeros((10, 2), dtype=torch.uint8, device=dev).t())
+    with pytest.raises(MambaScanError, match="out overlaps x"):
+        gated_scan_fwd(x, r, g, A, out=x)
+    with pytest.raises(MambaScanError, match="A is NULL"):
+        gated_scan_fwd(x, r, g, None)
+    with pytest.raises(MambaScanError, match="dr overlaps dg"):
+        gated_scan_bwd(x, r, g, A, v["dout"], marks, dr=(t := torch.empty_like(x)), dg=t)
+    with pytest.raises(MambaScanError, match="checkpoints is NULL"):
+        gated_scan_bwd(x, r, g, A, v["dout"], None)
+    with pytest.raises(ValueError, match="checkpoints has shape"):
+        gated_scan_bwd(x, r, g, A, v["dout"], torch.zeros((2, 2, 16), device=dev))
+    with pytest.raises(MambaScanError, match="out overlaps x"):
+        gated_update(v["h0"], x[:, 0], r[:, 0], g[:, 0], A, out=x[:, 0])
+    s = torch.randn((4, 16), device=dev)
+    w = torch.ones(16, device=dev)
+    with pytest.raises(TypeError, match="residual has dtype"):
+        rmsnorm_fwd(s, w, s.bfloat16())
+    with pytest.raises(ValueError, match="there is none without a residual"):
+        rmsnorm_fwd(s, w, sum=s.clone())
+    with pytest.raises(MambaScanError, match="sum overlaps x"):
+        rmsnorm_fwd(s, w, s.clone(), sum=s)
+    with pytest.raises(MambaScanError, match="group 32 is not"):
+        rmsnorm_quant_fwd(s, w, group=32)
+    with pytest.raises(MambaScanError, match="eps"):
+        rmsnorm_fwd(s, w, eps=-1.0)
+    with pytest.raises(MambaScanError, match="dim 65537 too large"):
+        rmsnorm_fwd(torch.zeros((1, 65537), device=dev), torch.ones(65537, device=dev))
+    with pytest.raises(ValueError, match="weight has shape"):
+        rmsnorm_bwd(s, w[:4], s.clone())
+    with pytest.raises(MambaScanError, match="dresidual overlaps sum"):
+        rmsnorm_bwd(s, w, s.clone(), dresidual=s)
+    c = torch.zeros((1, 6, 16), device=dev)
+    with pytest.raises(MambaScanError, match="width 5 not supported"):
+        conv1d_bwd(c, torch.zeros((16, 5), device=dev), c.clone())
+    with pytest.raises(ValueError, match="dout has shape"):
+        conv1d_bwd(c, torch.zeros((16, 4), device=dev), c[:, :3].contiguous())
+    with pytest.raises(ValueError, match="must be contiguous"):
+        conv1d_bwd(torch.zeros((1, 6, 32), device=dev)[..., ::2], torch.zeros((16, 4), device=dev), c)
