@@ -30,7 +30,9 @@ extern "C" {
 #endif
 
 /* Bytes of device workspace mamba_conv1d_bwd needs (0 when none, or for an
- * invalid descriptor). */
+ * invalid descriptor). The amount depends on the sizes and on the compute-unit
+ * count of the current device: call it with the device current that the
+ * backward will run on. */
 size_t mamba_conv1d_bwd_workspace_size(const mamba_conv_desc *desc);
 
 /*

@@ -85,7 +85,9 @@ mamba_status mamba_rmsnorm_quant_fwd(const mamba_norm_desc *desc,
                                      void *sum, void *stream);
 
 /* Bytes of device workspace mamba_rmsnorm_bwd needs (0 when none, or for an
- * invalid descriptor). */
+ * invalid descriptor). The amount depends on the sizes and on the compute-unit
+ * count of the current device: call it with the device current that the
+ * backward will run on. */
 size_t mamba_rmsnorm_bwd_workspace_size(const mamba_norm_desc *desc);
 
 /*

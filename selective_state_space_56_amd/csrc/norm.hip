@@ -9,6 +9,11 @@
 // use (from the L2 cache, which holds them). Rows of any alignment take the same
 // path (the last piece of a row element by element where the row is not whole
 // pieces).
+//
+// Measured on an MI355X (a plain copy moves 5.3 TB/s): 16384 x 2560, bf16 with
+// an fp32 stream, to 8 bits 82 us (461 MB, 5.6 TB/s); bf16 with a bf16 stream 56 us
+// (336 MB, 6.0 TB/s), its backward 78 us and 5 for dweight (336 MB and 8 MB of
+// parts, 4.4 TB/s: three workgroups per compute unit, each with one row ahead).
 #include "block.h"
 #include "block_math.h"
 #include "colsum.h"
@@ -370,12 +375,17 @@ unsigned threads_of(int64_t dim) {
   return static_cast<unsigned>(64 * (waves < kMaxWaves ? waves : kMaxWaves));
 }
 
-// Workgroups of a launch: what runs at once (of the backward 4 waves per SIMD
-// and what packs into them), each with the same number of rows, but for the last.
+// Workgroups of a launch: what runs at once (of the backward four waves per
+// SIMD, less what does not pack), each with the same number of rows but for the
+// last. The backward takes two rows at least: a part of dweight per row is
+// as much to write and read as half a row (1023 x 1541 fp32: 11.3 + 3.9 us with
+// two, 12.0 + 6.2 with one, 13.3 + 3.9 with four).
 unsigned grid_of(int64_t rows, int64_t dim, bool backward) {
   const int64_t waves = threads_of(dim) / 64;
   const int64_t per_cu = backward ? 16 / waves : (20 + waves - 1) / waves;
-  const int64_t most = per_cu * device_cu_count(), each = (rows + most - 1) / most;
+  const int64_t most = per_cu * device_cu_count(), least = backward ? 2 : 1;
+  int64_t each = (rows + most - 1) / most;
+  each = each < least ? least : each;
   return static_cast<unsigned>((rows + each - 1) / each);
 }
 
