@@ -72,8 +72,11 @@ __device__ __forceinline__ float over_16(float v) {
 template <class Op>
 __device__ __forceinline__ float over_wave(float v) {
   v = over_16<Op>(v);
-  v = Op::of(v, __shfl_xor(v, 16));
-  return Op::of(v, __shfl_xor(v, 32));
+  // swapping rows of 16 lanes, then halves, of two copies leaves each with one side's value
+  const auto rows = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = Op::of(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
+  const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return Op::of(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
 }
 
 // N values over the workgroup, in every thread and the same in each (the waves'
@@ -96,7 +99,12 @@ __device__ __forceinline__ void over_block(float (&v)[N], float (&scratch)[N][kM
   }
 }
 
-__device__ __forceinline__ float rstd_of(float ss, float dim, float eps) { return 1.0f / sqrtf(ss / dim + eps); }
+// 1 / sqrt(ss / dim + eps). The hardware's root takes values below its normal
+// range as 0, so those are lifted by 2^64 first.
+__device__ __forceinline__ float rstd_of(float ss, float inv_dim, float eps) {
+  const float m = fmaf(ss, inv_dim, eps);
+  return m < 0x1p-100f ? __builtin_amdgcn_rsqf(m * 0x1p64f) * 0x1p32f : __builtin_amdgcn_rsqf(m);
+}
 
 __device__ __forceinline__ float top_of(const float (&y)[kPiece]) {
   float top = kTiny;
@@ -132,6 +140,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormProblem p) {
   using res_raw = typename RES::raw;
   __shared__ float sums[2][1][kMaxWaves], tops[2][1][kMaxWaves];
   const int dim = static_cast<int>(p.dim), d = static_cast<int>(threadIdx.x) * kPiece;
+  const float inv_dim = 1.0f / static_cast<float>(dim);
   Row8<F32Io> w;
   load8(w, p.weight, d, dim);
   Row8<IO> x;
@@ -159,7 +168,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormProblem p) {
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) ss[0] = fmaf(s[j], s[j], ss[0]);
     over_block<AddOp>(ss, sums[turn]);
-    const float rstd = rstd_of(ss[0], static_cast<float>(dim), p.eps);
+    const float rstd = rstd_of(ss[0], inv_dim, p.eps);
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) s[j] = s[j] * rstd * w.get(j);
     if constexpr (OUT == kIo) {
@@ -188,6 +197,7 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormProblem p) {
   using res_raw = typename RES::raw;
   __shared__ float sums[2][1][kMaxWaves], tops[2][1][kMaxWaves];
   const int dim = static_cast<int>(p.dim), first = static_cast<int>(threadIdx.x) * kPiece;
+  const float inv_dim = 1.0f / static_cast<float>(dim);
   const int whole = (dim + kRegDim - 1) / kRegDim * kRegDim;  // every thread takes every turn
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
@@ -214,7 +224,7 @@ __global__ __launch_bounds__(1024) void norm_wide_kernel(NormProblem p) {
       for (int j = 0; j < kPiece; ++j) ss[0] = fmaf(s[j], s[j], ss[0]);
     }
     over_block<AddOp>(ss, sums[turn]);
-    const float rstd = rstd_of(ss[0], static_cast<float>(dim), p.eps);
+    const float rstd = rstd_of(ss[0], inv_dim, p.eps);
     // y of a piece, from the stream that this same thread has stored (or x)
     const auto normed = [&](int d, float (&y)[kPiece]) {
       Row8<F32Io> w;
@@ -282,7 +292,7 @@ __global__ __launch_bounds__(1024, 5) void norm_bwd_kernel(NormBwdProblem p, flo
   };
   load(blockIdx.x);
   int turn = 0;
-  const float n = static_cast<float>(dim);
+  const float inv_dim = 1.0f / static_cast<float>(dim);
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
     Row8<RES> s0 = s, ds0;
     if (p.dsum) ds0 = ds;
@@ -296,7 +306,7 @@ __global__ __launch_bounds__(1024, 5) void norm_bwd_kernel(NormBwdProblem p, flo
       both[1] = fmaf(sv, w.get(j) * dy0.get(j), both[1]);
     }
     over_block<AddOp>(both, sums[turn]);
-    const float rstd = rstd_of(both[0], n, p.eps), mean = both[1] * rstd / n;
+    const float rstd = rstd_of(both[0], inv_dim, p.eps), mean = both[1] * rstd * inv_dim;
     float v[kPiece];
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) {
@@ -322,7 +332,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdProblem p, f
   __shared__ float sums[2][2][kMaxWaves];
   const int dim = static_cast<int>(p.dim), first = static_cast<int>(threadIdx.x) * kPiece;
   float* part = parts + static_cast<int64_t>(blockIdx.x) * dim;
-  const float n = static_cast<float>(dim);
+  const float inv_dim = 1.0f / static_cast<float>(dim);
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
     const res_raw* sr = static_cast<const res_raw*>(p.sum) + row * p.ssum;
@@ -342,7 +352,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(NormBwdProblem p, f
       }
     }
     over_block<AddOp>(both, sums[turn]);
-    const float rstd = rstd_of(both[0], n, p.eps), mean = both[1] * rstd / n;
+    const float rstd = rstd_of(both[0], inv_dim, p.eps), mean = both[1] * rstd * inv_dim;
     for (int d = first; d < dim; d += kRegDim) {
       Row8<RES> s, ds;
       Row8<IO> dy, dx;
