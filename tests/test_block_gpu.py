@@ -713,3 +713,49 @@ def test_python_refusals(dev):
         conv1d_bwd(c, torch.zeros((16, 4), device=dev), c[:, :3].contiguous())
     with pytest.raises(ValueError, match="must be contiguous"):
         conv1d_bwd(torch.zeros((1, 6, 32), device=dev)[..., ::2], torch.zeros((16, 4), device=dev), c)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(dev, seed):
+    """Seeded shapes and options of all the operators, each value within its bound."""
+    import random
+    rng = random.Random(1000 + seed)
+
+    def between(lo, hi):
+        return int(round(lo * (hi / lo) ** rng.random()))
+
+    io = rng.choice([torch.bfloat16, torch.float32])
+    dim, batch = between(1, 700), rng.choice([1, 1, 2, 3, 7])
+    L = between(1, 200000 // (dim * batch) + 2)
+    v = _gated_inputs(dev, batch, L, dim, io, rng.random() < 0.5, rng.choice([0.0, 0.01, 0.3]), seed)
+    print(f"seed {seed}: {batch}x{L}x{dim} {io}", flush=True)
+    _check_gated(v, io, rng.random() < 0.5)
+    rows, wide = between(1, 400), between(1, 3000)
+    res = rng.choice([None, torch.float32, io])
+    x, residual, w, dout, ds = _norm_inputs(dev, rows, wide, io, res, seed)
+    y, total = rmsnorm_fwd(x, w, residual, eps=1e-5)
+    q, scale, _ = rmsnorm_quant_fwd(x, w, residual, eps=1e-5, group=rng.choice([0, 128]))
+    stream = x if residual is None else total
+    d = rmsnorm_bwd(stream, w, dout, ds=ds, eps=1e-5)
+    torch.cuda.synchronize()
+    want = ref.norm(x, w, residual, 1e-5, dout, ds)
+    assert_within("norm", y, rounded(want["out"], io))
+    _check_quant(q, scale, want, 0 if scale.shape[1] == 1 and wide > 128 else 128)
+    assert_within("dresidual", d["dresidual"], rounded(want["dresidual"], stream.dtype))
+    assert_within("dx", d["dx"], rounded(want["dresidual"], io))
+    assert_within("dweight", d["dweight"], rounded(want["dweight"], torch.float32))
+    width = rng.choice([1, 2, 3, 4])
+    g = torch.Generator().manual_seed(seed)
+
+    def normal(*shape, to=torch.float32):
+        return torch.randn(shape, generator=g).to(to).to(dev)
+
+    cx, cd, cw, cb = normal(batch, L, dim, to=io), normal(batch, L, dim, to=io), normal(dim, width), normal(dim)
+    st = normal(batch, dim, width - 1, to=io) if rng.random() < 0.5 else None
+    dst = normal(batch, dim, width - 1) if rng.random() < 0.5 else None
+    d = conv1d_bwd(cx, cw, cd, cb, st, dstate_out=dst)
+    torch.cuda.synchronize()
+    want = ref.conv_bwd(cx, cw, cd, cb, st, dst)
+    assert_within("dxin", d["dxin"], rounded(want["dxin"], io))
+    for name in ("dweight", "dbias", "dstate_in"):
+        assert_within(name, d[name], rounded(want[name], torch.float32))
