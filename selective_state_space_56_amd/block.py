@@ -114,10 +114,18 @@ def _plain(t, shape, dtype, dev):
 
 
 def _rows(t, name, shape, dtype, dev, rows_axis):
-    """_row_stride of a tensor that may be a column slice, without its walk
-    over the axes for the contiguous tensor of the right kind; 0 for None."""
-    if t is None or _plain(t, shape, dtype, dev):
+    """_row_stride of a tensor that may be a column slice; 0 for a contiguous
+    one and for None. The usual layouts are recognised without its walk over
+    the axes."""
+    if t is None:
         return 0
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev:
+        if t.is_contiguous():
+            return 0
+        step = t.stride()
+        row = step[rows_axis]
+        if step[-1] == 1 and row >= shape[-1] and (rows_axis == 0 or step[0] == row * shape[1]):
+            return row
     s = _row_stride(t, name, shape, dtype, dev, rows_axis)
     # rows apart by less than a row's length share elements: reading them is
     # only well defined for the layouts the library takes
