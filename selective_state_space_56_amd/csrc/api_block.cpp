@@ -166,12 +166,12 @@ extern "C" {
 
 size_t mamba_gated_scan_workspace_size(const mamba_gated_desc* d) {
   if (check_gated("mamba_gated_scan_workspace_size", d) != MAMBA_OK) return 0;
-  return mscan::gated_fwd_workspace_bytes(d->batch, d->seqlen, d->dim, d->io_dtype);
+  return mscan::gated_fwd_workspace_bytes(d->batch, d->seqlen, d->dim);
 }
 
 size_t mamba_gated_scan_bwd_workspace_size(const mamba_gated_desc* d) {
   if (check_gated("mamba_gated_scan_bwd_workspace_size", d) != MAMBA_OK) return 0;
-  return mscan::gated_bwd_workspace_bytes(d->batch, d->seqlen, d->dim, d->io_dtype);
+  return mscan::gated_bwd_workspace_bytes(d->batch, d->seqlen, d->dim);
 }
 
 mamba_status mamba_gated_scan_fwd(const mamba_gated_desc* d, const mamba_gated_strides* strides,

@@ -67,8 +67,8 @@ inline int64_t gated_tiles(int64_t batch, int64_t seqlen, int64_t dim) {
 }
 constexpr int64_t kGatedMaxTiles = (int64_t(1) << 23) - 1;  // of 512 threads: a launch holds fewer than 2^32
 
-size_t gated_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int io);
-size_t gated_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int io);
+size_t gated_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
+size_t gated_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
 hipError_t launch_gated_fwd(const GatedProblem& p, void* workspace, hipStream_t stream);
 hipError_t launch_gated_bwd(const GatedBwdProblem& p, void* workspace, hipStream_t stream);
 hipError_t launch_gated_update(const GatedUpdateProblem& p, hipStream_t stream);

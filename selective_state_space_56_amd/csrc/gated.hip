@@ -473,7 +473,7 @@ __device__ __forceinline__ void bwd_grads(const GatedBwdProblem& p, const Place<
       dA[v] += dvr;
       xs[v] = lp;
       gs[v] = lp * s.x[i].get(v) * (1.0f - s.sg[i][v]);
-      rs[v] = dvr * rate[v] * (1.0f - s.sr[i][v]);
+      rs[v] = on ? 0.0f : dvr * rate[v] * (1.0f - s.sr[i][v]);  // 0 whatever r is
     }
     Piece<IO, V> dx, dr, dg;
     dx.set(xs);
@@ -665,11 +665,11 @@ hipError_t launch_bwd(const GatedBwdProblem& p, void* workspace, hipStream_t str
 
 }  // namespace
 
-size_t gated_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int) {
+size_t gated_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
   return words_bytes(batch, seqlen, dim, kFwdSpan);
 }
 
-size_t gated_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int) {
+size_t gated_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
   const int64_t spans = (seqlen + kGatedCheckpoint - 1) / kGatedCheckpoint;
   return words_bytes(batch, seqlen, dim, kGatedCheckpoint) + rounded_up(static_cast<size_t>(spans * batch * dim) * 4);
 }

@@ -12,8 +12,8 @@
 static int g_launched = 0;
 
 namespace mscan {
-size_t gated_fwd_workspace_bytes(int64_t b, int64_t, int64_t d, int) { return b * d > 0 ? 512 : 0; }
-size_t gated_bwd_workspace_bytes(int64_t b, int64_t, int64_t d, int) { return b * d > 0 ? 512 : 0; }
+size_t gated_fwd_workspace_bytes(int64_t b, int64_t, int64_t d) { return b * d > 0 ? 512 : 0; }
+size_t gated_bwd_workspace_bytes(int64_t b, int64_t, int64_t d) { return b * d > 0 ? 512 : 0; }
 size_t norm_bwd_workspace_bytes(int64_t r, int64_t d) { return r * d > 0 ? 256 : 0; }
 size_t conv_bwd_workspace_bytes(int64_t b, int64_t, int64_t d, int) { return b * d > 0 ? 256 : 0; }
 hipError_t launch_gated_fwd(const GatedProblem&, void*, hipStream_t) { return ++g_launched, hipSuccess; }

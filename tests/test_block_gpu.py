@@ -759,3 +759,21 @@ def test_random_shapes(dev, seed):
     assert_within("dxin", d["dxin"], rounded(want["dxin"], io))
     for name in ("dweight", "dbias", "dstate_in"):
         assert_within(name, d[name], rounded(want[name], torch.float32))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_gated_ignores_the_gate_of_a_reset(dev, io):
+    """At a reset the recurrence gate is not looked at: NaN and infinities there
+    change no value, and get no gradient."""
+    v = _gated_inputs(dev, 2, 90, 33, IO[io], resets=0.2)
+    clean = _check_gated(v, IO[io])
+    at = v["reset"].nonzero()
+    for k, (b, t) in enumerate(at.tolist()):
+        v["r"][b, t] = (NAN, INF, -INF)[k % 3]
+    out, last, marks = gated_scan_fwd(v["x"], v["r"], v["g"], v["A"], h0=v["h0"], reset=v["reset"], return_checkpoints=True)
+    d = gated_scan_bwd(v["x"], v["r"], v["g"], v["A"], v["dout"], marks, reset=v["reset"], dlast=v["dlast"])
+    torch.cuda.synchronize()
+    assert torch.equal(out, clean[0]) and torch.equal(last, clean[1]) and torch.equal(marks, clean[2])
+    for k in ("dx", "dr", "dg", "dA", "dh0"):
+        assert torch.equal(d[k], clean[3][k]), k
+    assert float(d["dr"][v["reset"]].abs().max()) == 0.0
