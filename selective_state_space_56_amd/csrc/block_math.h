@@ -9,10 +9,34 @@ namespace mscan {
 // V consecutive io values, as one access of their size. gfx950's global loads
 // and stores take any alignment of the element's size, so rows of odd lengths
 // and odd first columns use the same path as aligned ones.
+// load_last and store_last carry the non-temporal hint: for data that is not read
+// again soon, so that it does not push out what is.
+template <class T, int N, int ALIGN>
+using Words = T __attribute__((ext_vector_type(N), aligned(ALIGN)));
+
+template <class T, int N, int ALIGN>
+__device__ __forceinline__ void load_streamed(const void* p, T (&to)[N]) {
+  using W = Words<T, N, ALIGN>;
+  const W w = __builtin_nontemporal_load(static_cast<const W*>(p));
+#pragma unroll
+  for (int k = 0; k < N; ++k) to[k] = w[k];
+}
+
+template <class T, int N, int ALIGN>
+__device__ __forceinline__ void store_streamed(void* p, const T (&from)[N]) {
+  using W = Words<T, N, ALIGN>;
+  W w;
+#pragma unroll
+  for (int k = 0; k < N; ++k) w[k] = from[k];
+  __builtin_nontemporal_store(w, static_cast<W*>(p));
+}
+
 template <class IO, int V>
 struct Piece {
   using raw = typename IO::raw;
   raw v[V];
+  __device__ __forceinline__ void load_last(const raw* p) { load_streamed<raw, V, sizeof(raw)>(p, v); }
+  __device__ __forceinline__ void store_last(raw* p) const { store_streamed<raw, V, sizeof(raw)>(p, v); }
   __device__ __forceinline__ void load(const raw* p) { __builtin_memcpy(v, p, sizeof(v)); }
   __device__ __forceinline__ void store(raw* p) const { __builtin_memcpy(p, v, sizeof(v)); }
   // the first n < V values only; the others are 0
@@ -24,6 +48,20 @@ struct Piece {
 #pragma unroll
     for (int k = 0; k < V; ++k)
       if (k < n) p[k] = v[k];
+  }
+  template <bool LAST>
+  __device__ __forceinline__ void load_if(const raw* p) {
+    if constexpr (LAST)
+      load_last(p);
+    else
+      load(p);
+  }
+  template <bool LAST>
+  __device__ __forceinline__ void store_if(raw* p) const {
+    if constexpr (LAST)
+      store_last(p);
+    else
+      store(p);
   }
   __device__ __forceinline__ float get(int k) const { return IO::to_f32(v[k]); }
   __device__ __forceinline__ void set(const float (&f)[V]) {
@@ -40,6 +78,8 @@ struct BfPiece {
   static_assert(V % 2 == 0, "whole words");
   using raw = uint16_t;
   uint32_t w[V / 2];
+  __device__ __forceinline__ void load_last(const raw* p) { load_streamed<uint32_t, V / 2, 2>(p, w); }
+  __device__ __forceinline__ void store_last(raw* p) const { store_streamed<uint32_t, V / 2, 2>(p, w); }
   __device__ __forceinline__ void load(const raw* p) { __builtin_memcpy(w, p, sizeof(w)); }
   __device__ __forceinline__ void store(raw* p) const { __builtin_memcpy(p, w, sizeof(w)); }
   __device__ __forceinline__ void load_some(const raw* p, int n) {
@@ -53,6 +93,20 @@ struct BfPiece {
 #pragma unroll
     for (int k = 0; k < V; ++k)
       if (k < n) p[k] = static_cast<uint16_t>(w[k / 2] >> (16 * (k % 2)));
+  }
+  template <bool LAST>
+  __device__ __forceinline__ void load_if(const raw* p) {
+    if constexpr (LAST)
+      load_last(p);
+    else
+      load(p);
+  }
+  template <bool LAST>
+  __device__ __forceinline__ void store_if(raw* p) const {
+    if constexpr (LAST)
+      store_last(p);
+    else
+      store(p);
   }
   __device__ __forceinline__ float get(int k) const {
     return __uint_as_float(k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);

@@ -4,8 +4,8 @@
 //
 // Streaming and bound by HBM: x and dout in, dx out (503 MB for 8 x 2048 x 5120
 // bf16), and 11 % on top for the W - 1 steps that neighbouring spans both read
-// and for the parts of dw. That takes 107 us and 7 for the sums of dw on an
-// MI355X, 5.2 TB/s of what is moved; a plain copy reaches 5.3.
+// and for the parts of dw. That takes 103 us and 7 for the sums of dw on an
+// MI355X, 5.4 TB/s of what is moved.
 #include "block.h"
 #include "block_math.h"
 #include "colsum.h"
@@ -16,8 +16,8 @@ namespace {
 
 constexpr int kThreads = 64;
 // Channels per thread (1 where there is one), steps whose loads are in flight
-// together. 8 x 2048 x 5120 bf16, with the sums: two channels and 4 steps 115 us, 2
-// steps 119, 6 steps 128, 8 steps 121; four channels and 4 steps 142.
+// together. 8 x 2048 x 5120 bf16, with the sums and plain loads: two channels and 4
+// steps 115 us, 2 steps 119, 6 steps 128, 8 steps 121; four channels and 4 steps 142.
 constexpr int kVec = 2;
 constexpr int kGroup = 4;
 
@@ -27,7 +27,7 @@ constexpr int kGroup = 4;
 // next group's loads are in flight while the current group is computed.
 // Threads past the last channel take the last V channels: they compute what
 // their owner does, and what both write is the same.
-template <class IO, int W, int V>
+template <class IO, int W, int V, bool LAST>
 __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdProblem p, int span, float* parts) {
   using raw = typename IO::raw;
   const int64_t own = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * V;
@@ -71,8 +71,8 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdProblem p, in
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) {
       const int64_t at = (t + i < p.seqlen ? t + i : p.seqlen - 1) * p.dim;  // past the end: not used
-      xr[i].load(xin + at);
-      yr[i].load(dout + at);
+      xr[i].template load_if<LAST>(xin + at);
+      yr[i].template load_if<LAST>(dout + at);
     }
   };
   // the windows move on by a step
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdProblem p, in
         input_grad(d);
         Piece<IO, V> dx;
         dx.set(d);
-        dx.store(dxin + (t + i - (W - 1)) * p.dim);
+        dx.template store_if<LAST>(dxin + (t + i - (W - 1)) * p.dim);
       }
       continue;
     }
@@ -203,25 +203,25 @@ int64_t spans_of(int64_t batch, int64_t seqlen, int64_t dim) {
   return seqlen > 0 ? (seqlen + span - 1) / span : 1;
 }
 
-template <class IO, int V>
-hipError_t launch_io(const ConvBwdProblem& p, float* parts, hipStream_t stream) {
+template <class IO, int V, bool LAST>
+hipError_t launch_width(const ConvBwdProblem& p, float* parts, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>((p.dim + kThreads * V - 1) / (kThreads * V)),
                   static_cast<unsigned>(spans_of(p.batch, p.seqlen, p.dim)), static_cast<unsigned>(p.batch));
   const int span = span_of(p.batch, p.seqlen, p.dim);
-  switch (p.width) {
-    case 1: hipLaunchKernelGGL((conv_bwd_kernel<IO, 1, V>), grid, dim3(kThreads), 0, stream, p, span, parts); break;
-    case 2: hipLaunchKernelGGL((conv_bwd_kernel<IO, 2, V>), grid, dim3(kThreads), 0, stream, p, span, parts); break;
-    case 3: hipLaunchKernelGGL((conv_bwd_kernel<IO, 3, V>), grid, dim3(kThreads), 0, stream, p, span, parts); break;
-    case 4: hipLaunchKernelGGL((conv_bwd_kernel<IO, 4, V>), grid, dim3(kThreads), 0, stream, p, span, parts); break;
-    default: return hipErrorInvalidValue;
-  }
+  const auto kernel = p.width == 1   ? conv_bwd_kernel<IO, 1, V, LAST>
+                      : p.width == 2 ? conv_bwd_kernel<IO, 2, V, LAST>
+                      : p.width == 3 ? conv_bwd_kernel<IO, 3, V, LAST>
+                                     : conv_bwd_kernel<IO, 4, V, LAST>;
+  hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, p, span, parts);
   return hipGetLastError();
 }
 
 template <class IO>
 hipError_t launch_dim(const ConvBwdProblem& p, float* parts, hipStream_t stream) {
-  if (p.dim < kVec) return launch_io<IO, 1>(p, parts, stream);
-  return launch_io<IO, kVec>(p, parts, stream);
+  if (p.dim < kVec) return launch_width<IO, 1, false>(p, parts, stream);
+  if (streams(3 * p.batch * p.seqlen * p.dim * static_cast<int64_t>(sizeof(typename IO::raw))))
+    return launch_width<IO, kVec, true>(p, parts, stream);
+  return launch_width<IO, kVec, false>(p, parts, stream);
 }
 
 }  // namespace

@@ -173,13 +173,13 @@ __device__ __forceinline__ T* in_row(T* row, uint32_t c) {
 
 // A wave's steps of one tensor, all loads in flight together. Past the end
 // (never when PLAIN) the last step is loaded again; its values are not used.
-template <bool PLAIN, class IO, int V, int STEPS>
+template <bool PLAIN, bool LAST, class IO, int V, int STEPS>
 __device__ __forceinline__ void load_steps(const void* base, int64_t row, int64_t stride, int c, int steps,
                                            Piece<IO, V> (&to)[STEPS]) {
   const typename IO::raw* p = static_cast<const typename IO::raw*>(base) + row * stride;
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
-    to[i].load(p + c);
+    to[i].template load_if<LAST>(p + c);
     if (PLAIN || i + 1 < steps) p += stride;
   }
 }
@@ -244,7 +244,7 @@ static_assert(kGatedCheckpoint % kFwdSteps == 0, "a checkpoint is where a wave's
 
 // A wave's steps as maps (a, u) in registers, and their joined map (A1, B1).
 // PLAIN: all STEPS steps are there and none is a reset.
-template <bool PLAIN, class IO, int V>
+template <bool PLAIN, bool LAST, class IO, int V>
 __device__ __forceinline__ void steps_to_maps(const GatedProblem& p, const Place<V, kFwdSteps, kFwdWaves>& at,
                                               uint32_t resets, float (&a)[kFwdSteps][V], float (&u)[kFwdSteps][V],
                                               float (&A1)[V], float (&B1)[V]) {
@@ -252,9 +252,9 @@ __device__ __forceinline__ void steps_to_maps(const GatedProblem& p, const Place
   float rate[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) rate[v] = p.A[at.c + v] * kLog2e;
-  load_steps<PLAIN>(p.r, at.row, p.sr, at.c, at.steps, r);
-  load_steps<PLAIN>(p.g, at.row, p.sg, at.c, at.steps, g);
-  load_steps<PLAIN>(p.x, at.row, p.sx, at.c, at.steps, x);
+  load_steps<PLAIN, LAST>(p.r, at.row, p.sr, at.c, at.steps, r);
+  load_steps<PLAIN, LAST>(p.g, at.row, p.sg, at.c, at.steps, g);
+  load_steps<PLAIN, LAST>(p.x, at.row, p.sx, at.c, at.steps, x);
 #pragma unroll
   for (int i = 0; i < kFwdSteps; ++i)
 #pragma unroll
@@ -280,7 +280,7 @@ __device__ __forceinline__ void steps_to_maps(const GatedProblem& p, const Place
 // maps meet in LDS, one wave per channel of a lane tells the tile's map, finds
 // the state that enters the tile and tells the one that leaves it; then every
 // wave runs its steps from its own entering state.
-template <class IO, int V>
+template <class IO, int V, bool LAST>
 __global__ __launch_bounds__(kFwdThreads) void gated_fwd_kernel(GatedProblem p, Order o, unsigned* counter,
                                                                 u64* words) {
   using raw = typename IO::raw;
@@ -297,9 +297,9 @@ __global__ __launch_bounds__(kFwdThreads) void gated_fwd_kernel(GatedProblem p, 
   const uint32_t resets = reset_bits(p.reset, at.row, steps);
   const bool plain = steps == kFwdSteps && resets == 0;
   if (plain)
-    steps_to_maps<true, IO, V>(p, at, resets, a, u, A1, B1);
+    steps_to_maps<true, LAST, IO, V>(p, at, resets, a, u, A1, B1);
   else if (steps > 0)
-    steps_to_maps<false, IO, V>(p, at, resets, a, u, A1, B1);
+    steps_to_maps<false, LAST, IO, V>(p, at, resets, a, u, A1, B1);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     sh.A[wave][v][lane] = A1[v];
@@ -390,15 +390,15 @@ struct Steps {
 
 // Loads a wave's steps and joins their maps: (A1, B1) of the states, (A1, M1)
 // of the adjoint, from the last step to the first.
-template <bool PLAIN, class IO, int V>
+template <bool PLAIN, bool LAST, class IO, int V>
 __device__ __forceinline__ void bwd_maps(const GatedBwdProblem& p, const Place<V, kBwdSteps, kBwdWaves>& at,
                                          uint32_t resets, const float (&rate)[V], Steps<IO, V>& s, float (&A1)[V],
                                          float (&B1)[V], float (&M1)[V]) {
   Piece<IO, V> r[kBwdSteps], g[kBwdSteps];
-  load_steps<PLAIN>(p.r, at.row, p.sr, at.c, at.steps, r);
-  load_steps<PLAIN>(p.g, at.row, p.sg, at.c, at.steps, g);
-  load_steps<PLAIN>(p.x, at.row, p.sx, at.c, at.steps, s.x);
-  load_steps<PLAIN>(p.dout, at.row, p.so, at.c, at.steps, s.dy);
+  load_steps<PLAIN, LAST>(p.r, at.row, p.sr, at.c, at.steps, r);
+  load_steps<PLAIN, LAST>(p.g, at.row, p.sg, at.c, at.steps, g);
+  load_steps<PLAIN, LAST>(p.x, at.row, p.sx, at.c, at.steps, s.x);
+  load_steps<PLAIN, LAST>(p.dout, at.row, p.so, at.c, at.steps, s.dy);
 #pragma unroll
   for (int i = 0; i < kBwdSteps; ++i)
 #pragma unroll
@@ -450,8 +450,11 @@ __device__ __forceinline__ void bwd_states(int steps, uint32_t resets, float (&h
     }
 }
 
-// A wave's gradients, from the adjoint m that enters its last step.
-template <bool PLAIN, class IO, int V>
+// A wave's gradients, from the adjoint m that enters its last step. Their stores
+// take the non-temporal hint too where the call streams (a training step of
+// 8 x 2048 x 5120 bf16 391 -> 377 us); the forward's output does not (1 x 131072 x
+// 5120 982 us without, 1005 with it).
+template <bool PLAIN, bool LAST, class IO, int V>
 __device__ __forceinline__ void bwd_grads(const GatedBwdProblem& p, const Place<V, kBwdSteps, kBwdWaves>& at,
                                           uint32_t resets, const float (&rate)[V], const Steps<IO, V>& s,
                                           float (&m)[V], float (&dA)[V]) {
@@ -479,9 +482,9 @@ __device__ __forceinline__ void bwd_grads(const GatedBwdProblem& p, const Place<
     dx.set(xs);
     dr.set(rs);
     dg.set(gs);
-    dx.store(in_row(dxp, at.c));
-    dr.store(in_row(drp, at.c));
-    dg.store(in_row(dgp, at.c));
+    dx.template store_if<LAST>(in_row(dxp, at.c));
+    dr.template store_if<LAST>(in_row(drp, at.c));
+    dg.template store_if<LAST>(in_row(dgp, at.c));
     dxp -= p.sdx;
     drp -= p.sdr;
     dgp -= p.sdg;
@@ -495,7 +498,7 @@ __device__ __forceinline__ void bwd_grads(const GatedBwdProblem& p, const Place<
 // keeps its steps in registers, finds its entering state and adjoint as the
 // forward does, and writes its steps' gradients. parts: one row of dA per span
 // and batch row.
-template <class IO, int V>
+template <class IO, int V, bool LAST>
 __global__ __launch_bounds__(kBwdThreads, 2) void gated_bwd_kernel(GatedBwdProblem p, Order o, unsigned* counter,
                                                                    u64* words, float* parts) {
   __shared__ Shared<V, kBwdWaves> sh;            // A and B of the adjoint
@@ -515,9 +518,9 @@ __global__ __launch_bounds__(kBwdThreads, 2) void gated_bwd_kernel(GatedBwdProbl
   const uint32_t resets = reset_bits(p.reset, at.row, at.steps);
   const bool plain = at.steps == kBwdSteps && resets == 0;
   if (plain)
-    bwd_maps<true>(p, at, resets, rate, s, A1, B1, M1);
+    bwd_maps<true, LAST>(p, at, resets, rate, s, A1, B1, M1);
   else if (at.steps > 0)
-    bwd_maps<false>(p, at, resets, rate, s, A1, B1, M1);
+    bwd_maps<false, LAST>(p, at, resets, rate, s, A1, B1, M1);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     sh.A[wave][v][lane] = A1[v];
@@ -549,9 +552,9 @@ __global__ __launch_bounds__(kBwdThreads, 2) void gated_bwd_kernel(GatedBwdProbl
 #pragma unroll
     for (int v = 0; v < V; ++v) m[v] = through(sh.A[k][v][lane], sh.B[k][v][lane], m[v]);
   if (plain)
-    bwd_grads<true>(p, at, resets, rate, s, m, dA);
+    bwd_grads<true, LAST>(p, at, resets, rate, s, m, dA);
   else if (at.steps > 0)
-    bwd_grads<false>(p, at, resets, rate, s, m, dA);
+    bwd_grads<false, LAST>(p, at, resets, rate, s, m, dA);
   // the waves' parts of dA, added in their order (mapB is read no more)
 #pragma unroll
   for (int v = 0; v < V; ++v) mapB[wave][v][lane] = dA[v];
@@ -586,9 +589,9 @@ __global__ __launch_bounds__(kLanes) void gated_update_kernel(GatedUpdateProblem
     for (int i = 0; i < kTokenRows; ++i) {
       const int64_t b = b0 + i < p.batch ? b0 + i : p.batch - 1;  // past the end: not used
       h[i] = p.state[b * p.dim + c];
-      x[i].load(static_cast<const raw*>(p.x) + b * p.sx + c);
-      r[i].load(static_cast<const raw*>(p.r) + b * p.sr + c);
-      g[i].load(static_cast<const raw*>(p.g) + b * p.sg + c);
+      x[i].load_last(static_cast<const raw*>(p.x) + b * p.sx + c);
+      r[i].load_last(static_cast<const raw*>(p.r) + b * p.sr + c);
+      g[i].load_last(static_cast<const raw*>(p.g) + b * p.sg + c);
     }
 #pragma unroll
     for (int i = 0; i < kTokenRows; ++i) {
@@ -639,8 +642,10 @@ hipError_t launch_fwd(const GatedProblem& p, void* workspace, hipStream_t stream
   }
   unsigned* counter = bytes ? static_cast<unsigned*>(workspace) : nullptr;
   u64* words = bytes ? reinterpret_cast<u64*>(static_cast<char*>(workspace) + kHeader) : nullptr;
-  hipLaunchKernelGGL((gated_fwd_kernel<IO, V>), grid_of(o), dim3(kFwdThreads), 0,
-                     stream, p, o, counter, words);
+  const auto kernel = streams(4 * p.batch * p.seqlen * p.dim * static_cast<int64_t>(sizeof(typename IO::raw)))
+                          ? gated_fwd_kernel<IO, V, true>
+                          : gated_fwd_kernel<IO, V, false>;
+  hipLaunchKernelGGL(kernel, grid_of(o), dim3(kFwdThreads), 0, stream, p, o, counter, words);
   return hipGetLastError();
 }
 
@@ -656,8 +661,10 @@ hipError_t launch_bwd(const GatedBwdProblem& p, void* workspace, hipStream_t str
   unsigned* counter = bytes ? reinterpret_cast<unsigned*>(ws) : nullptr;
   u64* words = bytes ? reinterpret_cast<u64*>(ws + kHeader) : nullptr;
   float* parts = reinterpret_cast<float*>(ws + bytes);
-  hipLaunchKernelGGL((gated_bwd_kernel<IO, V>), grid_of(o), dim3(kBwdThreads), 0,
-                     stream, p, o, counter, words, parts);
+  const auto kernel = streams(7 * p.batch * p.seqlen * p.dim * static_cast<int64_t>(sizeof(typename IO::raw)))
+                          ? gated_bwd_kernel<IO, V, true>
+                          : gated_bwd_kernel<IO, V, false>;
+  hipLaunchKernelGGL(kernel, grid_of(o), dim3(kBwdThreads), 0, stream, p, o, counter, words, parts);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   return launch_colsum(parts, p.batch * o.spans, p.dim, StoreFlat{p.dA}, stream);

@@ -39,6 +39,16 @@ __device__ __forceinline__ void load8(Row8<IO>& to, const typename IO::raw* row,
     to.load_some(row + d, dim - d);
 }
 
+// the same for what is not read again (the backward's loads: a training step of
+// 16384 x 2560 bf16 130 us instead of 134; the forward's measured no better with it)
+template <class IO>
+__device__ __forceinline__ void load8_last(Row8<IO>& to, const typename IO::raw* row, int d, int dim) {
+  if (d + kPiece <= dim)
+    to.load_last(row + d);
+  else
+    to.load_some(row + d, dim - d);
+}
+
 template <class IO>
 __device__ __forceinline__ void store8(const Row8<IO>& from, typename IO::raw* row, int d, int dim) {
   if (d + kPiece <= dim)
@@ -286,9 +296,9 @@ __global__ __launch_bounds__(1024, 5) void norm_bwd_kernel(NormBwdProblem p, flo
   Row8<RES> s, ds;
   Row8<IO> dy;
   const auto load = [&](int64_t row) {
-    load8(s, static_cast<const res_raw*>(p.sum) + row * p.ssum, d, dim);
-    load8(dy, static_cast<const raw*>(p.dout) + row * p.so, d, dim);
-    if (p.dsum) load8(ds, static_cast<const res_raw*>(p.dsum) + row * p.sdsum, d, dim);
+    load8_last(s, static_cast<const res_raw*>(p.sum) + row * p.ssum, d, dim);
+    load8_last(dy, static_cast<const raw*>(p.dout) + row * p.so, d, dim);
+    if (p.dsum) load8_last(ds, static_cast<const res_raw*>(p.dsum) + row * p.sdsum, d, dim);
   };
   load(blockIdx.x);
   int turn = 0;
