@@ -9,11 +9,11 @@
 // One pass: every input is read once and every output written once.
 //
 // Measured on an MI355X, where a plain copy moves 5.3 TB/s: the forward of
-// 8 x 2048 x 5120 bf16 takes 130 us (671 MB, 5.2 TB/s), of 1 x 131072 x 5120
-// 1007 us (5.37 GB, 5.3 TB/s). It is bound by HBM, with the vector ALUs close
+// 8 x 2048 x 5120 bf16 takes 132 us (671 MB, 5.1 TB/s), of 1 x 131072 x 5120
+// 990 us (5.37 GB, 5.4 TB/s). It is bound by HBM, with the vector ALUs close
 // behind (37 instructions per element and step, 6 of them transcendental: about
-// 80 % of their issue slots). The backward of the first takes 250 us (1.17 GB,
-// 4.7 TB/s; 66 instructions): its tile fills the registers at two waves per
+// 80 % of their issue slots). The backward of the first takes 240 us (1.17 GB,
+// 4.9 TB/s; 66 instructions): its tile fills the registers at two waves per
 // SIMD, too few to cover every load and wait.
 #include "block.h"
 #include "block_math.h"
@@ -372,8 +372,8 @@ __global__ __launch_bounds__(256) void gated_no_steps_kernel(const float* from, 
 
 // A tile of the backward, 16 steps in each of 4 waves. bf16 takes two channels
 // per lane: 256 registers, two waves per SIMD, 440 us for a training step of
-// 8 x 2048 x 5120 against 478 with one channel (163 registers, three waves) and
-// 534 with 8 steps in each of 8 waves. With fp32, whose pieces take twice the
+// 8 x 2048 x 5120 (380 since) against 478 with one channel (163 registers, three
+// waves) and 534 with 8 steps in each of 8 waves. With fp32, whose pieces take twice the
 // room, two channels do not fit, so it takes one.
 constexpr int kBwdSteps = 16, kBwdWaves = 4;
 constexpr int kBwdThreads = kLanes * kBwdWaves;
@@ -572,9 +572,10 @@ __global__ __launch_bounds__(kBwdThreads, 2) void gated_bwd_kernel(GatedBwdProbl
 constexpr int kTokenRows = 4;   // batch rows per thread, loaded together
 
 // One decode token: a channel of kTokenRows batch rows per thread. Bound by
-// HBM: state in and out, three inputs, one output. 4096 x 5120 bf16: 58.6 us,
-// 5.7 TB/s; with two channels per thread 61.2, four 71, eight 87 us; with one,
-// two or eight rows 88, 62 and 62 us.
+// HBM: state in and out, three inputs, one output. 4096 x 5120 bf16: 63 us,
+// 5.3 TB/s. One output buffer for all calls, plain loads: 58.6 us, with two
+// channels per thread 61.2, four 71, eight 87; with one, two or eight rows 88, 62
+// and 62.
 template <class IO>
 __global__ __launch_bounds__(kLanes) void gated_update_kernel(GatedUpdateProblem p) {
   using raw = typename IO::raw;

@@ -11,9 +11,9 @@
 // pieces).
 //
 // Measured on an MI355X (a plain copy moves 5.3 TB/s): 16384 x 2560, bf16 with
-// an fp32 stream, to 8 bits 82 us (461 MB, 5.6 TB/s); bf16 with a bf16 stream 56 us
-// (336 MB, 6.0 TB/s), its backward 78 us and 5 for dweight (336 MB and 8 MB of
-// parts, 4.4 TB/s: three workgroups per compute unit, each with one row ahead).
+// an fp32 stream, to 8 bits 83 us (461 MB, 5.5 TB/s); bf16 with a bf16 stream 60 us
+// (336 MB, 5.6 TB/s), its backward 64 us and 5 for dweight (336 MB and 8 MB of
+// parts, 5.4 TB/s).
 #include "block.h"
 #include "block_math.h"
 #include "colsum.h"
