@@ -17,7 +17,8 @@
  *
  * Non-finite inputs propagate within their row: a NaN makes the row NaN; an
  * infinity makes rstd 0, so its own outputs NaN and the row's others 0. NaN
- * values do not take part in a scale's maximum.
+ * values do not take part in a scale's maximum. With eps 0 a row of zeros has
+ * no norm and is NaN.
  *
  * Conventions as in mamba_scan.h. x, out, dout and dx have the io dtype;
  * residual, sum, dsum and dresidual the residual dtype, which is the io dtype
