@@ -13,7 +13,9 @@
  * The 8-bit form gives q = e4m3(y / scale), rounded to nearest even, with one
  * float32 scale per row (group 0) or per run of `group` channels (the last
  * run may be shorter): scale = max(max |y|, 2^-100) / 448, 448 being e4m3's
- * largest finite value. y is not rounded in between. Rows of zeros give q = 0.
+ * largest finite value. y is a float32 value, not rounded to the io dtype in
+ * between, and y / scale its float32 quotient by the scale as it is stored.
+ * Rows of zeros give q = 0.
  *
  * Non-finite inputs propagate within their row: a NaN makes the row NaN; an
  * infinity makes rstd 0, so its own outputs NaN and the row's others 0. NaN
