@@ -17,9 +17,12 @@
  *
  * A must be finite and <= 0 (A = -c softplus(lambda), or c log of the decay of
  * an open gate); A = 0 holds the state (a = 1, weight 0). A > 0 makes the
- * square root NaN. r = -inf holds the state too; r = +inf, g = +-inf are the
- * gates' limits. The weight's derivative with respect to a gate that holds
- * the state exactly (1 - a^2 = 0) is taken as 0.
+ * square root NaN, and the gradients with it. r = -inf holds the state too;
+ * r = +inf, g = +-inf are the gates' limits. The weight's derivative with
+ * respect to a gate that holds the state exactly (1 - a^2 = 0) is taken as 0.
+ * Where sigmoid(r) is below float32's normal range (2^-126) it counts as 0; in
+ * the forward and the decode token a weight below 2^-63 does too, in the
+ * gradients it keeps its value.
  *
  * Conventions as in mamba_scan.h: device pointers of the current device owned
  * by the caller, asynchronous on `stream`, validation before any HIP call,

@@ -126,22 +126,47 @@ struct Piece<Bf16Io, 8> : BfPiece<8> {};
 // 1 / (1 + e^-v): 0 and 1 at the infinities
 __device__ __forceinline__ float sigmoid_f(float v) { return hw_rcp(1.0f + hw_exp2(-v * kLog2e)); }
 
-// Decay a = e^v and 1 - a^2 of one step, v = A sigmoid(r) <= 0, from v2 = v log2(e).
-// 1 - a^2 = 1 - e^-u with u = -2v: for u < 1/4, where 1 - a^2 would cancel, six
-// terms of its series u - u^2/2 + u^3/6 - ... (the next is u^6 / 5040 < 5e-8 of
-// the sum), as a polynomial in v2; above, a's rounding of 2^-24 is at most 3e-7
-// of 1 - a^2 >= 0.22.
-__device__ __forceinline__ float decay_gap(float v2, float& a) {
-  constexpr float k = 2.0f * kLn2;  // u = -k v2
-  constexpr float c1 = -k, c2 = c1 * k / 2.0f, c3 = c2 * k / 3.0f, c4 = c3 * k / 4.0f, c5 = c4 * k / 5.0f,
-                  c6 = c5 * k / 6.0f;
+// Decay a = e^v of one step, v = A s with the gate's sigmoid s, and 1 - a^2, from
+// rate = A log2(e). With u = -2v and v2 = v log2(e): for u < 1/4 (`near`), where
+// 1 - a^2 = 1 - e^-u would cancel, six terms of its series u - u^2/2 + u^3/6 - ...
+// (the next is u^6 / 5040 < 5e-8 of the sum), as v2 times a polynomial in v2;
+// above, a's rounding of 2^-24 is at most 3e-7 of 1 - a^2 >= 0.22. With SPLIT the
+// series leaves out the factor |A|: s times a polynomial, which stays in float32's
+// range where |A| s does not.
+template <bool SPLIT>
+__device__ __forceinline__ float decay_gap(float rate, float s, float& a, bool& near) {
+  constexpr float k = 2.0f * kLn2;  // u = -k v2 = 2 |A| s
+  constexpr float c1 = SPLIT ? 2.0f : -k, c2 = c1 * k / 2.0f, c3 = c2 * k / 3.0f, c4 = c3 * k / 4.0f,
+                  c5 = c4 * k / 5.0f, c6 = c5 * k / 6.0f;
+  const float v2 = rate * s;
   a = hw_exp2(v2);
   float p = fmaf(v2, c6, c5);
   p = fmaf(v2, p, c4);
   p = fmaf(v2, p, c3);
   p = fmaf(v2, p, c2);
   p = fmaf(v2, p, c1);
-  return v2 > -0.25f / k ? v2 * p : fmaf(-a, a, 1.0f);
+  near = v2 > -0.25f / k;
+  return near ? (SPLIT ? s : v2) * p : fmaf(-a, a, 1.0f);
 }
+
+// a and w = sqrt(1 - a^2). The hardware's root takes numbers below its normal
+// range as 0, so a weight below 2^-63 is 0. (Kept in range as the backward keeps it
+// costs the forward 1.6 to 2 %: 129 -> 131.5 us for 8 x 2048 x 5120 bf16.)
+__device__ __forceinline__ float decay_weight(float rate, float s, float& a) {
+  bool near;
+  return __builtin_amdgcn_sqrtf(decay_gap<false>(rate, s, a, near));
+}
+
+// What the weight's slope needs of a channel's A: sqrt(-A) and its reciprocal,
+// NaN for A > 0; 0 both for A = 0, which holds the state.
+struct RateRoot {
+  float root, inv;
+  __device__ __forceinline__ explicit RateRoot(float A) {
+    const bool low = -A < 0x1p-100f;  // lifted: the hardware's roots take subnormal numbers as 0
+    const float m = low ? -A * 0x1p64f : -A;
+    root = __builtin_amdgcn_sqrtf(m) * (low ? 0x1p-32f : 1.0f);
+    inv = A == 0.0f ? 0.0f : __builtin_amdgcn_rsqf(m) * (low ? 0x1p32f : 1.0f);
+  }
+};
 
 }  // namespace mscan

@@ -259,7 +259,7 @@ __device__ __forceinline__ void steps_to_maps(const GatedProblem& p, const Place
   for (int i = 0; i < kFwdSteps; ++i)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float w = __builtin_amdgcn_sqrtf(decay_gap(rate[v] * sigmoid_f(r[i].get(v)), a[i][v]));
+      float w = decay_weight(rate[v], sigmoid_f(r[i].get(v)), a[i][v]);
       const bool on = !PLAIN && (resets >> i & 1), past = !PLAIN && i >= at.steps;
       if (on) w = 1.0f;
       u[i][v] = w * (sigmoid_f(g[i].get(v)) * x[i].get(v));
@@ -380,8 +380,9 @@ constexpr int kBwdThreads = kLanes * kBwdWaves;
 static_assert(kBwdSteps * kBwdWaves == kGatedCheckpoint, "a tile starts at a checkpoint");
 
 // What the backward keeps of a wave's steps: the decay a, the input gate sg and
-// its product with the weight p = w sg, the recurrence gate sr, and d, the
-// slope of h_t along log a: first a^2 / w sg x, then a h_{t-1} minus that.
+// its product with the weight p = w sg, the recurrence gate sr, and d, sr times
+// the slope of h_t along log a: first sr a^2 / w sg x, then sr a h_{t-1} minus that.
+// (sr / w stays in range where 1 / w need not.)
 template <class IO, int V>
 struct Steps {
   float a[kBwdSteps][V], p[kBwdSteps][V], sg[kBwdSteps][V], sr[kBwdSteps][V], d[kBwdSteps][V];
@@ -406,9 +407,15 @@ __device__ __forceinline__ void bwd_maps(const GatedBwdProblem& p, const Place<V
       const bool on = !PLAIN && (resets >> i & 1), past = !PLAIN && i >= at.steps;
       const float sr = sigmoid_f(r[i].get(v)), sg = sigmoid_f(g[i].get(v)), xv = s.x[i].get(v);
       float a;
-      const float gap = decay_gap(rate[v] * kLog2e * sr, a);
-      const float inv = gap > 0.0f ? __builtin_amdgcn_rsqf(gap) : 0.0f;  // 1 / w; no slope where the state is held
-      float w = gap * inv;
+      bool near;
+      const RateRoot A(rate[v]);
+      const float gap = decay_gap<true>(rate[v] * kLog2e, sr, a, near);
+      const float inv = gap >= 0x1p-126f ? __builtin_amdgcn_rsqf(gap) : 0.0f;  // no slope where the state is held
+      float w = gap * inv, slope = inv * sr;  // w and sr / w
+      if (near) {
+        w *= A.root;
+        slope *= A.inv;
+      }
       if (on) w = 1.0f;
       if (past) {
         a = 1.0f;
@@ -419,7 +426,7 @@ __device__ __forceinline__ void bwd_maps(const GatedBwdProblem& p, const Place<V
       s.p[i][v] = pg;
       s.sg[i][v] = sg;
       s.sr[i][v] = sr;
-      s.d[i][v] = a * a * inv * (sg * xv);
+      s.d[i][v] = a * a * slope * (sg * xv);
       B1[v] = on ? u : fmaf(a, B1[v], u);
       A1[v] = on || (!PLAIN && A1[v] == 0.0f) ? 0.0f : PLAIN ? A1[v] * a : joined(A1[v], a);
     }
@@ -445,7 +452,7 @@ __device__ __forceinline__ void bwd_states(int steps, uint32_t resets, float (&h
       if (!PLAIN && i >= steps) continue;
       const float u = s.p[i][v] * s.x[i].get(v), kept = s.a[i][v] * h[v];
       const bool on = !PLAIN && (resets >> i & 1);
-      s.d[i][v] = on ? 0.0f : kept - s.d[i][v];
+      s.d[i][v] = on ? 0.0f : fmaf(kept, s.sr[i][v], -s.d[i][v]);
       h[v] = on ? u : kept + u;
     }
 }
@@ -471,7 +478,7 @@ __device__ __forceinline__ void bwd_grads(const GatedBwdProblem& p, const Place<
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float lam = s.dy[i].get(v) + m[v], lp = lam * s.p[i][v];
-      const float dvr = on ? 0.0f : lam * s.d[i][v] * s.sr[i][v];
+      const float dvr = on ? 0.0f : lam * s.d[i][v];
       m[v] = on ? 0.0f : s.a[i][v] * lam;
       dA[v] += dvr;
       xs[v] = lp;
@@ -599,7 +606,7 @@ __global__ __launch_bounds__(kLanes) void gated_update_kernel(GatedUpdateProblem
       const int64_t b = b0 + i;
       if (b >= p.batch) break;
       float a;
-      const float w = __builtin_amdgcn_sqrtf(decay_gap(rate * sigmoid_f(r[i].get(0)), a));
+      const float w = decay_weight(rate, sigmoid_f(r[i].get(0)), a);
       const float next = fmaf(a, h[i], w * (sigmoid_f(g[i].get(0)) * x[i].get(0)));
       p.state[b * p.dim + c] = next;
       static_cast<raw*>(p.out)[b * p.so + c] = IO::from_f32(next);

@@ -1,11 +1,15 @@
 """GPU tests of the block operators where single values decide: 8-bit values at
-the borders of their roundings."""
+the borders of their roundings, gates that are nearly closed."""
 import pytest
 import torch
 
-from selective_state_space_56_amd import rmsnorm_fwd, rmsnorm_quant_fwd
+import block_ref as ref
+from block_ref import assert_within, rounded
+from selective_state_space_56_amd import (gated_scan_bwd, gated_scan_fwd, gated_update, rmsnorm_fwd,
+                                          rmsnorm_quant_fwd)
 
 pytestmark = pytest.mark.gpu
+IO = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 
 @pytest.fixture(scope="module")
@@ -87,3 +91,94 @@ def test_8_bit_values_of_an_infinite_maximum(dev, group):
     run = f[:, :group or 300]
     assert int(run.isnan().sum()) == 2 and float(run.nan_to_num(0.0).abs().max()) == 0.0
     assert bool(f[:, 128:].isfinite().all())
+
+
+CLOSED = [-1.0, -0.3, -0.1, -0.008, -1e-6, -1e-20, -1e-30, -1e-38]
+
+
+def _closed_gates(dev, io, mixed, seed):
+    """Recurrence gates from -70 to -105 in half steps, in every channel of
+    CLOSED; mixed: every other step has an ordinary gate."""
+    g = torch.Generator().manual_seed(seed)
+    A = torch.tensor(CLOSED).repeat(3)
+    dim, sweep = A.numel(), -70.0 - 0.5 * torch.arange(71)
+    L = 142
+    r = sweep.repeat(2)[:, None].repeat(1, dim)[None].repeat(2, 1, 1)
+    if mixed:
+        r[:, 1::2] = torch.randn((2, L // 2, dim), generator=g)
+        r[:, 0::2] = sweep[None, :, None]
+    rest = [torch.randn((2, L, dim), generator=g) for _ in range(3)]
+    x, gate, dout = (t.to(io).to(dev) for t in rest)
+    return x, r.to(io).to(dev), gate, A.to(dev), dout
+
+
+def _closed_slack(x, r, A, dout, dlast, want):
+    """What numbers below float32's normal range, taken as 0, add to the bounds.
+
+    With S = 2^-126: a sigmoid below it moves w = sqrt(1 - a^2), whose square has a
+    slope of at most 2 |A|, by at most dw = sqrt(2 |A| S), and sigmoid / w by at
+    most sqrt(S / (2 |A|)). a^2 / w |A| sigmoid comes to w / 2 and moves by dw at
+    most. The forward, which also takes 1 - a^2 below S as 0, loses weights of at
+    most sqrt(S) (a factor of 2 for the borders), so its states move by the
+    sum of those times |x| at most."""
+    x, r, A = ref.d64(x).abs(), ref.d64(r), ref.d64(A).abs()
+    s, S = torch.sigmoid(r), 2.0 ** -126
+    dw = torch.where(s < 2 * S, (2 * A * S).sqrt(), torch.zeros_like(x))
+    slope = torch.where(s < 2 * S, (S / (2 * A)).sqrt(), torch.zeros_like(x))
+    lost = torch.where((2 * A * s < 2 * S) | (s < 2 * S), torch.full_like(x, (2 * S) ** 0.5), torch.zeros_like(x))
+    state = (torch.maximum(dw, lost) * x).sum(1, keepdim=True)
+    lam = ref.d64(dout).abs().flip(1).cumsum(1).flip(1)
+    if dlast is not None:
+        lam = lam + ref.d64(dlast).abs()[:, None]
+    h = want["before"][0].abs()
+    closed = S * h + s * state
+    return {"out": state.expand_as(x), "last_state": state[:, 0], "dx": lam * dw, "dg": lam * x * dw,
+            "dr": lam * (A * closed + x * dw), "dA": (lam * (closed + x * slope)).sum((0, 1)), "dh0": 0.0}
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("mixed,with_h0", [(False, True), (False, False), (True, True)])
+def test_nearly_closed_recurrence_gates(dev, io, mixed, with_h0):
+    """1 - a^2 down to and past float32's smallest numbers is the definition's
+    value, in every output and gradient, and spoils nothing around it."""
+    x, r, gate, A, dout = _closed_gates(dev, IO[io], mixed, 11)
+    h0 = torch.randn((2, A.numel()), device=dev) if with_h0 else None
+    dlast = torch.randn((2, A.numel()), device=dev) if with_h0 else None
+    out, last, marks = gated_scan_fwd(x, r, gate, A, h0=h0, return_checkpoints=True)
+    d = gated_scan_bwd(x, r, gate, A, dout, marks, dlast=dlast)
+    torch.cuda.synchronize()
+    want = ref.gated(x, r, gate, A, h0, None, dout, dlast)
+    more = _closed_slack(x, r, A, dout, dlast, want)
+    got = {"out": out, "last_state": last, **d}
+    for name, t in got.items():
+        v, e = want[name]
+        assert_within(name, t, rounded((v, e + more[name]), t.dtype))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_nearly_closed_recurrence_gates_of_a_token(dev, io):
+    x, r, gate, A, dout = _closed_gates(dev, IO[io], True, 12)
+    state = torch.zeros((2, A.numel()), device=dev)
+    for t in range(6):
+        before = state.clone()
+        cut = [v[:, t:t + 1].contiguous() for v in (x, r, gate)]
+        out = gated_update(state, *(v[:, 0] for v in cut), A)
+        torch.cuda.synchronize()
+        want = ref.gated(*cut, A, before, None, dout[:, t:t + 1])
+        more = _closed_slack(cut[0], cut[1], A, dout[:, t:t + 1], None, want)["last_state"]
+        v, e = want["last_state"]
+        assert_within("out", out, rounded((v, e + more), IO[io]))
+        assert_within("state", state, rounded((v, e + more), torch.float32))
+
+
+def test_a_positive_rate_is_nan_in_the_gradients_too(dev):
+    """A must not be above 0: its square root is NaN, in its own channel only."""
+    g = torch.Generator().manual_seed(3)
+    x, r, gate, dout = (torch.randn((1, 70, 6), generator=g).to(dev) for _ in range(4))
+    A = torch.tensor([-0.5, 0.25, -0.1, 1e-6, -1.0, 2.0], device=dev)
+    out, _, marks = gated_scan_fwd(x, r, gate, A, return_checkpoints=True)
+    d = gated_scan_bwd(x, r, gate, A, dout, marks)
+    torch.cuda.synchronize()
+    for t in (out, d["dx"], d["dr"], d["dg"]):
+        assert bool(t[..., [1, 3, 5]].isnan().all()) and bool(t[..., [0, 2, 4]].isfinite().all())
+    assert d["dA"].isnan().tolist() == [False, True, False, True, False, True]
