@@ -37,7 +37,7 @@ size_t mamba_conv1d_bwd_workspace_size(const mamba_conv_desc *desc);
 
 /*
  *   xin, weight, bias, state_in : as given to mamba_conv1d_fwd (bias and
- *                state_in may be NULL).
+ *                state_in may be NULL; weight is read for empty sequences too).
  *   dout       : (batch, seqlen, dim) io dtype.
  *   dstate_out : (batch, dim, width-1) float32 or NULL (zero).
  *   dxin       : (batch, seqlen, dim) io dtype, written.

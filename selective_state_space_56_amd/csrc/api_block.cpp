@@ -508,8 +508,8 @@ mamba_status mamba_conv1d_bwd(const mamba_conv_desc* d, const void* xin, const f
   const int64_t rows = d->batch * d->dim, elems = rows * d->seqlen, W = d->width;
   if (d->dim == 0) return ok();
   if ((st = check_present(who, {{"dweight", dweight, 0}})) != MAMBA_OK) return st;
-  if (elems > 0 && (st = check_present(who, {{"xin", xin, 0}, {"weight", weight, 0}, {"dout", dout, 0},
-                                             {"dxin", dxin, 0}})) != MAMBA_OK)
+  if (rows > 0 && (st = check_present(who, {{"weight", weight, 0}})) != MAMBA_OK) return st;  // also of no tokens
+  if (elems > 0 && (st = check_present(who, {{"xin", xin, 0}, {"dout", dout, 0}, {"dxin", dxin, 0}})) != MAMBA_OK)
     return st;
   const size_t need = mamba_conv1d_bwd_workspace_size(d);
   if ((st = check_workspace(who, workspace, workspace_bytes, need)) != MAMBA_OK) return st;
