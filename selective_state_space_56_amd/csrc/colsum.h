@@ -12,6 +12,11 @@ constexpr int kColsumCols = 32;    // columns per workgroup: one 128-byte piece 
 constexpr int kColsumRuns = 32;    // threads per column, each with its own rows
 constexpr int kColsumAhead = 8;    // loads in flight per thread
 
+// Workgroups of a launch at most; each takes every kColsumGroups-th group of
+// columns. A launch holds fewer than 2^32 threads, and a convolution's backward may
+// have 5 x 2^31 columns of sums.
+constexpr int64_t kColsumGroups = int64_t(1) << 20;
+
 // parts (rows, cols) -> out[column]; Store(column, sum) places it. Thread k of a
 // column adds rows k, k + 32, ... in that order and one thread adds the 32 sums
 // in order, so the result does not depend on how the waves run.
@@ -20,27 +25,31 @@ __global__ __launch_bounds__(kColsumCols* kColsumRuns) void colsum_kernel(const 
                                                                           int64_t cols, Store store) {
   __shared__ float sums[kColsumRuns][kColsumCols + 1];
   const int col = threadIdx.x % kColsumCols, run = threadIdx.x / kColsumCols;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kColsumCols + col;
-  float s = 0.0f;
-  if (c < cols) {
-    const float* p = parts + c;
-    int64_t r = run;
-    for (; r + (kColsumAhead - 1) * kColsumRuns < rows; r += kColsumAhead * kColsumRuns) {
-      float v[kColsumAhead];
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kColsumCols; first < cols;
+       first += static_cast<int64_t>(gridDim.x) * kColsumCols) {
+    const int64_t c = first + col;
+    float s = 0.0f;
+    if (c < cols) {
+      const float* p = parts + c;
+      int64_t r = run;
+      for (; r + (kColsumAhead - 1) * kColsumRuns < rows; r += kColsumAhead * kColsumRuns) {
+        float v[kColsumAhead];
 #pragma unroll
-      for (int k = 0; k < kColsumAhead; ++k) v[k] = p[(r + k * kColsumRuns) * cols];
+        for (int k = 0; k < kColsumAhead; ++k) v[k] = p[(r + k * kColsumRuns) * cols];
 #pragma unroll
-      for (int k = 0; k < kColsumAhead; ++k) s += v[k];
+        for (int k = 0; k < kColsumAhead; ++k) s += v[k];
+      }
+      for (; r < rows; r += kColsumRuns) s += p[r * cols];
     }
-    for (; r < rows; r += kColsumRuns) s += p[r * cols];
-  }
-  sums[run][col] = s;
-  __syncthreads();
-  if (run == 0 && c < cols) {
-    float t = 0.0f;
+    sums[run][col] = s;
+    __syncthreads();
+    if (run == 0 && c < cols) {
+      float t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kColsumRuns; ++k) t += sums[k][col];
-    store(c, t);
+      for (int k = 0; k < kColsumRuns; ++k) t += sums[k][col];
+      store(c, t);
+    }
+    __syncthreads();  // the next columns' sums take these places
   }
 }
 
@@ -51,7 +60,8 @@ struct StoreFlat {
 
 template <class Store>
 hipError_t launch_colsum(const float* parts, int64_t rows, int64_t cols, Store store, hipStream_t stream) {
-  hipLaunchKernelGGL((colsum_kernel<Store>), dim3(static_cast<unsigned>((cols + kColsumCols - 1) / kColsumCols)),
+  const int64_t groups = (cols + kColsumCols - 1) / kColsumCols;
+  hipLaunchKernelGGL((colsum_kernel<Store>), dim3(static_cast<unsigned>(groups < kColsumGroups ? groups : kColsumGroups)),
                      dim3(kColsumCols * kColsumRuns), 0, stream, parts, rows, cols, store);
   return hipGetLastError();
 }

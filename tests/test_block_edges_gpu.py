@@ -5,7 +5,7 @@ import torch
 
 import block_ref as ref
 from block_ref import assert_within, rounded
-from selective_state_space_56_amd import (gated_scan_bwd, gated_scan_fwd, gated_update, rmsnorm_fwd,
+from selective_state_space_56_amd import (conv1d_bwd, gated_scan_bwd, gated_scan_fwd, gated_update, rmsnorm_fwd,
                                           rmsnorm_quant_fwd)
 
 pytestmark = pytest.mark.gpu
@@ -182,3 +182,27 @@ def test_a_positive_rate_is_nan_in_the_gradients_too(dev):
     for t in (out, d["dx"], d["dr"], d["dg"]):
         assert bool(t[..., [1, 3, 5]].isnan().all()) and bool(t[..., [0, 2, 4]].isfinite().all())
     assert d["dA"].isnan().tolist() == [False, True, False, True, False, True]
+
+
+def test_conv_bwd_of_the_most_channels(dev):
+    """More columns of sums than 32 threads each fit into one launch (2^27)."""
+    dim, W, L, io = 27_000_001, 4, 2, torch.bfloat16
+    assert (W + 1) * dim > 2 ** 27
+    g = torch.Generator(device=dev).manual_seed(5)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device=dev)
+
+    x, dout = normal(1, L, dim).to(io), normal(1, L, dim).to(io)
+    w, b = normal(dim, W) * 0.5, normal(dim) * 0.5
+    d = conv1d_bwd(x, w, dout, b)
+    torch.cuda.synchronize()
+    # every channel is its own: the first, the last, and those on both sides of each turn of the sums
+    turn = (1 << 20) * 32
+    edges = [c for j in range(W + 1) for k in range(6) for c in range(k * turn - j * dim - 3, k * turn - j * dim + 3)]
+    at = torch.tensor(sorted({c for c in edges if 0 <= c < dim} | set(range(70)) | set(range(dim - 70, dim))), device=dev)
+    want = ref.conv_bwd(x[..., at], w[at], dout[..., at], b[at])
+    assert_within("dxin", d["dxin"][..., at], rounded(want["dxin"], io))
+    assert_within("dweight", d["dweight"][at], rounded(want["dweight"], torch.float32))
+    assert_within("dbias", d["dbias"][at], rounded(want["dbias"], torch.float32))
+    assert bool(d["dweight"].isfinite().all()) and bool((d["dbias"] != 0).float().mean() > 0.99)
