@@ -13,7 +13,10 @@
  *
  * With reset[b,t] nonzero, step t starts a new sequence: a_t = 0, so that
  * h_t = sigmoid(g) x and nothing of the state before it remains (not even a
- * non-finite one); r gets no gradient there.
+ * non-finite one); r gets no gradient there. last_state is the state after the
+ * last step, so of several sequences in one row the last one's. (The
+ * convolution of mamba_conv.h in front of the recurrence has no resets: it sees
+ * the width - 1 inputs before a step whatever sequence they belong to.)
  *
  * A must be finite and <= 0 (A = -c softplus(lambda), or c log of the decay of
  * an open gate); A = 0 holds the state (a = 1, weight 0). A > 0 makes the

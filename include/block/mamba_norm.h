@@ -20,7 +20,11 @@
  * Non-finite inputs propagate within their row: a NaN makes the row NaN; an
  * infinity makes rstd 0, so its own outputs NaN and the row's others 0. NaN
  * values do not take part in a scale's maximum. With eps 0 a row of zeros has
- * no norm and is NaN.
+ * no norm and is NaN. Squares and their sum are float32 numbers: a row whose sum
+ * of squares is above their range (values of 1e19 and more) has rstd 0 as an
+ * infinite one has, and with eps 0 one whose squares are all below it (values
+ * of 1e-23 and less) an infinite rstd. In the backward a row of the stream with a
+ * non-finite value has a NaN ds.
  *
  * Conventions as in mamba_scan.h. x, out, dout and dx have the io dtype;
  * residual, sum, dsum and dresidual the residual dtype, which is the io dtype

@@ -5,7 +5,7 @@ import torch
 
 import block_ref as ref
 from block_ref import assert_within, rounded
-from selective_state_space_56_amd import (conv1d_bwd, gated_scan_bwd, gated_scan_fwd, gated_update, rmsnorm_fwd,
+from selective_state_space_56_amd import (conv1d_bwd, gated_scan_bwd, gated_scan_fwd, gated_update, rmsnorm_bwd, rmsnorm_fwd,
                                           rmsnorm_quant_fwd)
 
 pytestmark = pytest.mark.gpu
@@ -206,3 +206,41 @@ def test_conv_bwd_of_the_most_channels(dev):
     assert_within("dweight", d["dweight"][at], rounded(want["dweight"], torch.float32))
     assert_within("dbias", d["dbias"][at], rounded(want["dbias"], torch.float32))
     assert bool(d["dweight"].isfinite().all()) and bool((d["dbias"] != 0).float().mean() > 0.99)
+
+
+def test_norm_at_the_ends_of_the_range(dev):
+    """Rows whose squares leave float32's range, as the header states them."""
+    x = torch.ones((5, 200), device=dev)
+    x[0] *= 1e20
+    x[1] *= 1e-24
+    x[2] *= 1e18
+    x[3] *= 1e-18
+    x[4, 9] = float("inf")
+    w = torch.ones(200, device=dev)
+    y, _ = rmsnorm_fwd(x, w, eps=0.0)
+    d = rmsnorm_bwd(x, w, torch.ones_like(x), eps=0.0)
+    torch.cuda.synchronize()
+    assert float(y[0].abs().max()) == 0.0 and bool(y[1].isinf().all())
+    assert_within("in range", y[2:4], rounded(ref.norm(x[2:4], w, None, 0.0)["out"], torch.float32))
+    assert bool(d["dx"][4].isnan().all()) and bool(d["dx"][2:4].isfinite().all())
+
+
+def test_gated_one_step_slices_of_a_longer_sequence(dev):
+    """Single steps taken out of a sequence as views: batch rows are a whole
+    sequence apart."""
+    g = torch.Generator().manual_seed(8)
+    x, r, gate = (torch.randn((3, 5, 34), generator=g).to(dev) for _ in range(3))
+    A = (-0.1 - torch.rand(34, generator=g)).to(dev)
+    whole, last = gated_scan_fwd(x, r, gate, A)
+    state, h = torch.zeros((3, 34), device=dev), None
+    for t in range(5):
+        cut = [v[:, t:t + 1] for v in (x, r, gate)]
+        out, h = gated_scan_fwd(*cut, A, h0=h)
+        tok = gated_update(state, *(v[:, 0] for v in cut), A)
+        torch.cuda.synchronize()
+        want = ref.gated(x[:, :t + 1], r[:, :t + 1], gate[:, :t + 1], A)
+        v, e = want["last_state"]
+        assert_within("step", out[:, 0], rounded((v, e), torch.float32))
+        assert_within("token", tok, rounded((v, e), torch.float32))
+        assert torch.equal(state, tok)
+    assert_within("last", last, rounded(want["last_state"], torch.float32))
