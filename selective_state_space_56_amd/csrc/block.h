@@ -61,11 +61,14 @@ struct GatedUpdateProblem {
 
 constexpr int64_t kGatedCheckpoint = 64;
 
-// Workgroups of a sequence call: kGatedCheckpoint steps of 128 channels each.
+// At least half the workgroups of a sequence call, counted as tiles of
+// kGatedCheckpoint steps and 128 channels. The forward's tiles have twice the
+// steps and 512 threads (64 channels only where there is one), the backward's 256
+// threads and in fp32 64 channels, twice as many tiles: at most 2^24 - 2 of them.
 inline int64_t gated_tiles(int64_t batch, int64_t seqlen, int64_t dim) {
   return batch * ((dim + 127) / 128) * ((seqlen + kGatedCheckpoint - 1) / kGatedCheckpoint);
 }
-constexpr int64_t kGatedMaxTiles = (int64_t(1) << 23) - 1;  // of 512 threads: a launch holds fewer than 2^32
+constexpr int64_t kGatedMaxTiles = (int64_t(1) << 23) - 1;  // a launch holds fewer than 2^32 threads
 
 size_t gated_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
 size_t gated_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);

@@ -62,8 +62,10 @@ __device__ __forceinline__ u64 heard(const u64* p) {
 // state already, so the result does not depend on who was first. A word not
 // there yet is waited for: its tile started earlier than this one. One word
 // is asked for at first, mostly a state already, then four together (four at
-// once from the start: 138 against 134 us for 8 x 2048 x 5120 bf16). With 16 maps
-// held instead of 32, 1 x 131072 x 256 takes 108 us instead of 87, with 2 360.
+// once from the start: 134 against 127 us for 8 x 2048 x 5120 bf16, 86 against 87
+// for 1 x 131072 x 256). With 16 maps held instead of 32, 1 x 131072 x 256 takes
+// 108 us instead of 87, with 2 402; a copy of its 268 MB would take 51: in so narrow
+// a sequence what takes the time is the state's way through the tiles.
 __device__ __forceinline__ float state_before(const u64* from, int64_t step, int before, u64 (&held)[kHeld][kLanes]) {
   const int lane = threadIdx.x % kLanes;
   int n = 0;  // maps held: the words of the nearest n tiles
@@ -235,9 +237,9 @@ __device__ __forceinline__ uint32_t reset_bits(const uint8_t* reset, int64_t row
 // A tile: steps per wave, waves. Its fixed costs (a tile's ticket, two barriers,
 // the words) want it large, the registers and the number of tiles small. On
 // 8 x 2048 x 5120 and 1 x 131072 x 5120 bf16, two channels per lane: 16 x 8 steps
-// 148 and 1097 us, 8 x 8 188 and 1479, 8 x 16 200 and 1573, 16 x 4 160 and 1191,
-// 32 x 8 166 and 1230, 16 x 16 158 and 1170; one channel per lane (8 x 8) 264 and
-// 2023 (all before the look-back was shortened).
+// 127 and 971 us, 8 x 8 156 and 1167, 8 x 16 174 and 1330, 16 x 4 158 and 1154,
+// 16 x 16 150 and 1075, 32 x 4 135 and 975, 32 x 8 160 and 1134; 16 x 8 with one
+// channel per lane 155 and 1117.
 constexpr int kFwdSteps = 16, kFwdWaves = 8;
 constexpr int kFwdSpan = kFwdSteps * kFwdWaves, kFwdThreads = kLanes * kFwdWaves;
 static_assert(kGatedCheckpoint % kFwdSteps == 0, "a checkpoint is where a wave's steps start");
@@ -580,9 +582,12 @@ constexpr int kTokenRows = 4;   // batch rows per thread, loaded together
 
 // One decode token: a channel of kTokenRows batch rows per thread. Bound by
 // HBM: state in and out, three inputs, one output. 4096 x 5120 bf16: 63 us,
-// 5.3 TB/s. One output buffer for all calls, plain loads: 58.6 us, with two
-// channels per thread 61.2, four 71, eight 87; with one, two or eight rows 88, 62
-// and 62.
+// 5.3 TB/s; with one, two or eight rows per thread 87, 62 and 64.5, and 1024 x 5120
+// 24.1, 17.1 and 15.5 against 15.6. (Two channels per thread instead of one were
+// 4 % slower, four 21 %: with plain loads and one output buffer for all calls.)
+// The inputs carry the non-temporal hint at every size: 4096 x 5120 bf16 62.5 us
+// against 66.2, 2048 rows 29.2 against 30.6, 1024 rows 15.6 against 14.0, 512 and
+// fewer the same.
 template <class IO>
 __global__ __launch_bounds__(kLanes) void gated_update_kernel(GatedUpdateProblem p) {
   using raw = typename IO::raw;

@@ -39,8 +39,10 @@ __device__ __forceinline__ void load8(Row8<IO>& to, const typename IO::raw* row,
     to.load_some(row + d, dim - d);
 }
 
-// the same for what is not read again (the backward's loads: a training step of
-// 16384 x 2560 bf16 130 us instead of 134; the forward's measured no better with it)
+// The same for what is not read again: the backward's loads. A training step of
+// 16384 x 2560 bf16 takes 130 us instead of 133.5, of 8192 rows 71.3 against 70.7, of
+// 4096 38.6 against 41.4, of 2048 and fewer the same; of 16384 x 2560 fp32 273.5
+// against 266.8. The forward's measured no better with it.
 template <class IO>
 __device__ __forceinline__ void load8_last(Row8<IO>& to, const typename IO::raw* row, int d, int dim) {
   if (d + kPiece <= dim)
