@@ -80,9 +80,9 @@ hipError_t launch_gated_update(const GatedUpdateProblem& p, hipStream_t stream);
 // that the last-level cache holds, so that nothing of it would be found there
 // by the next call. Such calls carry the non-temporal hint on their large
 // tensors. With it the recurrence's training step of 8 x 2048 x 5120 bf16 (671 MB
-// and more per call) takes 379 us instead of 399 and the convolution's backward
-// 114 instead of 119; 3 x 1021 x 771 fp32 (38 MB), whose backward finds the forward's
-// inputs in the cache, would take 51 us instead of 47.
+// and more per call) takes 386 us instead of 404 and the convolution's backward
+// 114.6 instead of 119.5; 3 x 1021 x 771 fp32 (38 MB), whose backward finds the
+// forward's inputs in the cache, would take 51 us instead of 48.
 inline bool streams(int64_t bytes) { return bytes > (int64_t(256) << 20); }
 
 // RMS norm over rows, with the residual's addition and either an io output or

@@ -1,6 +1,9 @@
 // Sums over the rows of a float32 matrix, one per column: the last step of the
 // gradients that are shared by every token (decay, norm weight, convolution
-// taps), whose per-workgroup parts are rows of a workspace.
+// taps), whose per-workgroup parts are rows of a workspace. A workgroup takes 32
+// columns and all rows: 4 to 7 us for 1500 columns and more; with few columns
+// long rows of work fall to few workgroups (8192 x 320 of a convolution's backward
+// over 4 x 131072 x 64: 14 us beside 79 of its main pass).
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -3,7 +3,7 @@
 //   dx_t = sum_j w_j dv_{t+(W-1)-j},  dw_j = sum_t dv_t x_{t-(W-1)+j},  dbias = sum_t dv_t.
 //
 // Streaming and bound by HBM: x and dout in, dx out (503 MB for 8 x 2048 x 5120
-// bf16), and 11 % on top for the W - 1 steps that neighbouring spans both read
+// bf16), and 9 % on top for the W - 1 steps that neighbouring spans both read
 // and for the parts of dw. That takes 108 us and 6 for the sums of dw on an
 // MI355X, 5.1 TB/s of what is moved; a plain copy reaches 5.3.
 #include "block.h"

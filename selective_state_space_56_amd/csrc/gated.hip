@@ -10,11 +10,11 @@
 //
 // Measured on an MI355X, where a plain copy moves 5.3 TB/s: the forward of
 // 8 x 2048 x 5120 bf16 takes 132 us (671 MB, 5.1 TB/s), of 1 x 131072 x 5120
-// 990 us (5.37 GB, 5.4 TB/s). It is bound by HBM, with the vector ALUs close
-// behind (37 instructions per element and step, 6 of them transcendental: about
-// 80 % of their issue slots). The backward of the first takes 240 us (1.17 GB,
-// 4.9 TB/s; 66 instructions): its tile fills the registers at two waves per
-// SIMD, too few to cover every load and wait.
+// 990 us (5.37 GB, 5.4 TB/s). It is bound by HBM, with the vector ALUs behind
+// (37 instructions per element and step, 6 of them transcendental: they issue in
+// 70 % of the kernel's cycles). The backward of the first takes 250 us (1.17 GB,
+// 4.7 TB/s; 70 instructions, 67 % of the cycles): its tile fills the registers
+// at two waves per SIMD, too few to cover every load and wait.
 #include "block.h"
 #include "block_math.h"
 #include "colsum.h"
@@ -374,7 +374,7 @@ __global__ __launch_bounds__(256) void gated_no_steps_kernel(const float* from, 
 
 // A tile of the backward, 16 steps in each of 4 waves. bf16 takes two channels
 // per lane: 256 registers, two waves per SIMD, 440 us for a training step of
-// 8 x 2048 x 5120 (380 since) against 478 with one channel (163 registers, three
+// 8 x 2048 x 5120 (385 since) against 478 with one channel (163 registers, three
 // waves) and 534 with 8 steps in each of 8 waves. With fp32, whose pieces take twice the
 // room, two channels do not fit, so it takes one.
 constexpr int kBwdSteps = 16, kBwdWaves = 4;
@@ -461,8 +461,8 @@ __device__ __forceinline__ void bwd_states(int steps, uint32_t resets, float (&h
 
 // A wave's gradients, from the adjoint m that enters its last step. Their stores
 // take the non-temporal hint too where the call streams (a training step of
-// 8 x 2048 x 5120 bf16 391 -> 377 us); the forward's output does not (1 x 131072 x
-// 5120 982 us without, 1005 with it).
+// 8 x 2048 x 5120 bf16 395 us without, 386 with it); the forward's output does not
+// (1 x 131072 x 5120 996 us without, 1010 with it; 8 x 2048 x 5120 132 and 129).
 template <bool PLAIN, bool LAST, class IO, int V>
 __device__ __forceinline__ void bwd_grads(const GatedBwdProblem& p, const Place<V, kBwdSteps, kBwdWaves>& at,
                                           uint32_t resets, const float (&rate)[V], const Steps<IO, V>& s,

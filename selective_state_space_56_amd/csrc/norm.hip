@@ -11,9 +11,12 @@
 // pieces).
 //
 // Measured on an MI355X (a plain copy moves 5.3 TB/s): 16384 x 2560, bf16 with
-// an fp32 stream, to 8 bits 83 us (461 MB, 5.5 TB/s); bf16 with a bf16 stream 60 us
+// an fp32 stream, to 8 bits 85 us (461 MB, 5.4 TB/s); bf16 with a bf16 stream 60 us
 // (336 MB, 5.6 TB/s), its backward 64 us and 5 for dweight (336 MB and 8 MB of
-// parts, 5.4 TB/s).
+// parts, 5.4 TB/s). Away from such rows: up to 512 channels a launch of 16384 rows
+// takes about 10 us whatever their number (a row takes a whole wave), and
+// 4096 x 20000 bf16 155 us to 8 bits in groups and 461 a training step, where a copy of
+// the same bytes takes 109 and 247 (each use of a wide row reads it again).
 #include "block.h"
 #include "block_math.h"
 #include "colsum.h"
