@@ -1,0 +1,157 @@
+// What the kernels of linear attention share: a call's parts ("roles"), where
+// sequences and their pieces lie, and the decays inside one chunk of steps.
+//
+// One map does all the work: per sequence and head, with a state S of K x V,
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t
+// over chunks of C steps. With ell_t the running sum of g inside the chunk,
+//   o_t   = e^{ell_t} S_in^T q_t + sum_{s <= t} e^{ell_t - ell_s} (k_s . q_t) v_s
+//   S_out = e^{ell_C} S_in + sum_s e^{ell_C - ell_s} k_s v_s^T
+// so a chunk is four matrix products, and S stays in registers from the first
+// chunk of a segment to its last. The gradients are the same map with other
+// operands (dq: queries dout, keys v, values k, state S^T) and, for dk and dv,
+// with time reversed; a reversed step's decay lies behind it, so there ell is
+// the running sum before the step.
+#pragma once
+
+#include "block_math.h"
+#include "mamba_scan.h"
+#include "mixer.h"
+
+namespace mscan {
+
+constexpr float kNoDecay = -104.0f;  // e^g is 0 in float32 from here on: what was before is dropped
+
+// One run of the map. Operands are rows of `heads / div` heads; e is what the
+// sums for the decays' gradients take beside them.
+struct MixRole {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* e;         // or null: no sums
+  void* o;               // io rows, or null
+  float* part;           // float32 rows (contiguous) in the place of o, or null
+  int64_t sq, sk, sv, se, so;
+  int qdiv, kdiv, vdiv, ediv;  // heads that share the operand's head
+  int K, V;
+  const float* s0;       // the state that enters a sequence, (batch, heads, K, V), or null
+  const float* enter;    // the states that enter later segments, (slots, heads, K, V), or null
+  float* last;           // (batch, heads, K, V) or null
+  float* marks;          // states at every `mark` chunks, (slots, heads, K, V), or null
+  float* sums;           // (value tiles, heads, rows) or null
+  float* local;          // a segment's own state, (slots, heads, K, V), instead of outputs; or null
+  float* gone;           // with it: the segment's whole decay, (slots, heads)
+  bool s0_turned;        // s0 is (.., V, K)
+  bool reverse;
+  bool pairs;            // the sums take what the chunk's own pairs give too
+  float score, from, to; // factors of the chunk's scores, of what S_in gives, of what a step adds to S
+};
+
+struct MixCall {
+  MixRole role[3];
+  const int64_t* offsets;  // or null: sequences of seqlen steps
+  const float* g;
+  int64_t g_step;          // between steps: heads, or 0 with one decay per head
+  int64_t seqlen, rows;
+  int64_t slots;           // segments at most, over all sequences
+  int batch, heads, roles, tiles;
+  int per;                 // chunks of a segment
+  int mark;                // chunks between two marks
+};
+
+// Where a sequence lies. Offsets are read as they are found on the device, held
+// to 0 .. rows.
+struct Sequence {
+  int64_t begin, len;
+};
+__device__ __forceinline__ int64_t offset_of(const int64_t* offsets, int64_t i, int64_t seqlen, int64_t rows) {
+  if (!offsets) return i * seqlen;
+  const int64_t v = offsets[i];
+  return v < 0 ? 0 : v > rows ? rows : v;
+}
+__device__ __forceinline__ Sequence sequence_of(const int64_t* offsets, int64_t i, int64_t seqlen, int64_t rows) {
+  const int64_t a = offset_of(offsets, i, seqlen, rows), b = offset_of(offsets, i + 1, seqlen, rows);
+  return {a, b > a ? b - a : 0};
+}
+
+// Pieces of `steps` steps are counted through all sequences: piece p of sequence
+// i has slot offset_i / steps + i + p, which leaves room for each sequence's last
+// piece. The sequence of a slot is the last one that starts at or before it.
+__device__ __forceinline__ int64_t first_slot(int64_t begin, int64_t i, int64_t steps) { return begin / steps + i; }
+inline int64_t slots_of(int64_t rows, int64_t batch, int64_t steps) { return rows / steps + batch; }
+
+__device__ __forceinline__ int sequence_at(const int64_t* offsets, int batch, int64_t seqlen, int64_t rows, int64_t steps,
+                                           int64_t slot) {
+  int lo = 0, hi = batch;  // lo: starts at or before the slot; hi: does not
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first_slot(offset_of(offsets, mid, seqlen, rows), mid, steps) <= slot)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// The decays of one chunk of C <= 64 steps, by one wave, a step per lane. Sums
+// are float64: among large decays the differences of float32 sums would lose the
+// small ones (at 6400, half a step is 2^-12). A decay of 0 is no summand but cuts:
+// step t sees steps s >= from[t] only. Steps past the chunk's end add nothing.
+template <int C>
+struct Decays {
+  double ell[C];
+  float in[C];     // of S_in in o_t; 0 where a cut lies between
+  float end[C];    // of a step in S_out; 0 where a cut lies between
+  int from[C];
+  float all;       // of S_in in S_out; 0 with a cut
+  int cut;         // whether there is one
+  double total;    // the sum of the others
+};
+
+__device__ __forceinline__ float exp_of(double v) { return hw_exp2(static_cast<float>(v) * kLog2e); }
+
+// Returns `all`.
+template <int C>
+__device__ __forceinline__ float chunk_decays(Decays<C>& d, float g, int n, bool reverse) {
+  const int i = threadIdx.x & 63;
+  const bool live = i < n, cut = live && g <= kNoDecay;
+  const double own = live && !cut ? static_cast<double>(g) : 0.0;
+  double sum = own;
+  int last = cut ? i : -1;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const double u = __shfl_up(sum, off);
+    const int w = __shfl_up(last, off);
+    if (i >= off) {
+      sum += u;
+      last = last > w ? last : w;
+    }
+  }
+  const double total = __shfl(sum, 63);
+  const int cuts = __shfl(last, 63);
+  const float all = cuts < 0 ? exp_of(total) : 0.0f;
+  double ell = sum;
+  int seen = last;
+  if (reverse) {
+    // not sum - own: the sums in the order in which they are made
+    ell = __shfl_up(sum, 1);
+    seen = __shfl_up(last, 1);
+    if (i == 0) {
+      ell = 0.0;
+      seen = -1;
+    }
+  }
+  if (i < C) {
+    d.ell[i] = ell;
+    d.in[i] = seen < 0 ? exp_of(ell) : 0.0f;
+    d.from[i] = seen < 0 ? 0 : reverse ? seen + 1 : seen;
+    d.end[i] = live && (reverse ? i > cuts : i >= cuts) ? exp_of(total - ell) : 0.0f;
+    if (i == 0) {
+      d.all = all;
+      d.cut = cuts >= 0;
+      d.total = total;
+    }
+  }
+  return all;
+}
+
+}  // namespace mscan

@@ -1,0 +1,549 @@
+// Linear attention with a decay for each head: how a call is cut into roles and
+// segments, and the small kernels around the map's own (linattn.h).
+#include "colsum.h"
+#include "linattn_walk.h"
+
+namespace mscan {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Segments. The state that enters segment p + 1 of a sequence is
+// gone_p enter_p + local_p, of which local and gone are known by then; enter takes
+// local's place. A thread takes four elements of one (sequence, head).
+constexpr int kJoinThreads = 256;
+
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk, int64_t blocks) {
+  const MixRole& r = w.role[blockIdx.y];
+  const int64_t size = static_cast<int64_t>(r.K) * r.V;
+  const int64_t e = ((blockIdx.x % blocks) * kJoinThreads + threadIdx.x) * 4;
+  const int64_t sh = blockIdx.x / blocks;
+  const int head = static_cast<int>(sh % w.heads);
+  const int64_t seq = sh / w.heads;
+  if (e >= size) return;
+  const int64_t steps = static_cast<int64_t>(w.per) * chunk;
+  const Sequence s = sequence_of(w.offsets, seq, w.seqlen, w.rows);
+  const int64_t chunks = (s.len + chunk - 1) / chunk, base = first_slot(s.begin, seq, steps);
+  const int64_t segs = chunks > w.per ? (chunks + w.per - 1) / w.per : 1;
+  float cur[4] = {};
+  if (r.s0) {
+    const float* from = r.s0 + sh * size;
+    for (int k = 0; k < 4; ++k)
+      cur[k] = r.s0_turned ? from[(e + k) % r.V * r.K + (e + k) / r.V] : from[e + k];
+  }
+  for (int64_t p = 0; p < segs; ++p) {
+    const int64_t at = (base + (r.reverse ? segs - 1 - p : p)) * w.heads + head;
+    float* to = r.local + at * size + e;
+    float own[4] = {}, gone = 0.0f;
+    if (p + 1 < segs) {
+      Piece<F32Io, 4> piece;
+      piece.load(to);
+      for (int k = 0; k < 4; ++k) own[k] = piece.get(k);
+      gone = r.gone[at];
+    }
+    for (int k = 0; k < 4; ++k) {
+      to[k] = cur[k];
+      cur[k] = gone != 0.0f ? fmaf(gone, cur[k], own[k]) : own[k];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients of the decays. For step t of a chunk, with what the two runs' sums
+// hold (a_s = end_s k_s . (dS_out v_s), b_u = in_u scale q_u . (S_in dout_u) and the
+// chunk's own pairs (u, s), added at u and taken off at s):
+//   dg_t = e^{ell_C} <S_in, dS_out> + sum_{s < t} a_s + sum_{u >= t} b_u
+// Every term is of the size of the result: the difference of q . dq and k . dk
+// summed from the sequence's end, which is the same, would lose what strong decays
+// leave. The first term goes from chunk to chunk, <S_out, dS_out> - sum a + sum b,
+// and is formed anew from the states at every mark. One workgroup per stretch between
+// marks and head.
+constexpr int kDecayThreads = 256;
+
+struct DecayGrad {
+  MixCall w;                 // sequences; per is not used
+  const float* a;            // (atiles, heads, rows)
+  const float* b;            // (btiles, heads, rows)
+  const float* marks;        // (slots, heads, V, K): states
+  const float* dmarks;       // (slots, heads, K, V): their gradients
+  const float* last;         // (batch, heads, V, K) or null
+  const float* dlast;        // (batch, heads, K, V) or null
+  float* dg;                 // (rows, heads), or null:
+  float* parts;              // (slots, heads): sums over the stretch
+  int atiles, btiles, K, V;
+};
+
+template <int C>
+__global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) {
+  const MixCall& w = p.w;
+  __shared__ double s_sum[kDecayThreads / 64];
+  __shared__ Decays<C> dec;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int head = blockIdx.x % w.heads;
+  const int64_t slot = blockIdx.x / w.heads;
+  const int64_t steps = static_cast<int64_t>(w.mark) * C;
+  const int seq = sequence_at(w.offsets, w.batch, w.seqlen, w.rows, steps, slot);
+  const Sequence s = sequence_of(w.offsets, seq, w.seqlen, w.rows);
+  const int64_t chunks = (s.len + C - 1) / C, m = slot - first_slot(s.begin, seq, steps), begin = m * w.mark;
+  if (m < 0 || begin >= chunks) {  // (nothing of a sequence of no steps)
+    if (p.parts && tid == 0) p.parts[slot * w.heads + head] = 0.0f;
+    return;
+  }
+  const int64_t end = begin + w.mark < chunks ? begin + w.mark : chunks;
+  // <S, dS> at the stretch's end
+  const int64_t size = static_cast<int64_t>(p.K) * p.V;
+  const float* S = p.marks + ((slot + 1) * w.heads + head) * size;
+  const float* dS = p.dmarks + ((slot + 1) * w.heads + head) * size;
+  if (end == chunks) {
+    S = p.last ? p.last + (static_cast<int64_t>(seq) * w.heads + head) * size : nullptr;
+    dS = p.dlast ? p.dlast + (static_cast<int64_t>(seq) * w.heads + head) * size : nullptr;
+  }
+  double dot = 0.0;
+  if (S && dS)
+    for (int64_t e = tid; e < size; e += kDecayThreads)
+      dot += static_cast<double>(dS[e]) * S[e % p.V * p.K + e / p.V];
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) dot += __shfl_xor(dot, off);
+  if (lane == 0) s_sum[tid >> 6] = dot;
+  __syncthreads();
+  if (tid >= 64) return;
+  double X = 0.0, all = 0.0;
+  for (int k = 0; k < kDecayThreads / 64; ++k) X += s_sum[k];
+  for (int64_t c = end - 1; c >= begin; --c) {
+    const int64_t c0 = c * C, row = s.begin + c0 + lane;
+    const int n = s.len - c0 < C ? static_cast<int>(s.len - c0) : C;
+    const bool live = lane < n;
+    const float g = live ? w.g[row * w.g_step + head] : 0.0f;
+    const float kept = chunk_decays<C>(dec, g, n, false);
+    double a = 0.0, b = 0.0;
+    if (live) {
+      for (int k = 0; k < p.atiles; ++k) a += p.a[(static_cast<int64_t>(k) * w.heads + head) * w.rows + row];
+      for (int k = 0; k < p.btiles; ++k) b += p.b[(static_cast<int64_t>(k) * w.heads + head) * w.rows + row];
+    }
+    double pre = a, post = b;  // sums up to here, and from here on
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double u = __shfl_up(pre, off), v = __shfl_down(post, off);
+      if (lane >= off) pre += u;
+      if (lane + off < 64) post += v;
+    }
+    const double sum_a = __shfl(pre, 63), sum_b = __shfl(post, 0);
+    pre = __shfl_up(pre, 1);
+    if (lane == 0) pre = 0.0;
+    const double through = kept != 0.0f ? X - sum_a : 0.0;
+    const double grad = live && !(g <= kNoDecay) ? through + pre + post : 0.0;
+    if (p.dg && live) p.dg[row * w.heads + head] = static_cast<float>(grad);
+    all += grad;
+    X = through + sum_b;
+  }
+  if (!p.parts) return;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) all += __shfl_xor(all, off);
+  if (lane == 0) p.parts[slot * w.heads + head] = static_cast<float>(all);
+}
+
+// ---------------------------------------------------------------------------
+// Gradients of shared queries and keys: the sum over a group's heads, in order, of
+// the float32 rows that the heads have written, 8 values per thread.
+struct GroupSum {
+  const float* part[2];      // (rows, heads, K)
+  void* to[2];
+  int64_t stride[2];
+  const int64_t* offsets;
+  int64_t rows, pieces;      // pieces: 8-value pieces of a row of `to`
+  int heads, groups, K, batch;
+};
+
+template <class IO>
+__global__ __launch_bounds__(256) void group_sum_kernel(GroupSum p) {
+  const int64_t begin = p.offsets ? offset_of(p.offsets, 0, 0, p.rows) : 0;
+  const int64_t end = p.offsets ? offset_of(p.offsets, p.batch, 0, p.rows) : p.rows;
+  const int per = p.heads / p.groups;
+  for (int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; id < p.rows * p.pieces;
+       id += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = id / p.pieces;
+    if (row < begin || row >= end) continue;
+    const int x = static_cast<int>(id % p.pieces) * 8, group = x / p.K, c = x % p.K;
+    const float* from = (blockIdx.y ? p.part[1] : p.part[0]) + (row * p.heads + static_cast<int64_t>(group) * per) * p.K + c;
+    float sum[8] = {};
+    for (int h = 0; h < per; ++h, from += p.K) {
+      Piece<F32Io, 8> v;
+      v.load(from);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += v.get(k);
+    }
+    Piece<IO, 8> out;
+    out.set(sum);
+    out.store(static_cast<typename IO::raw*>(blockIdx.y ? p.to[1] : p.to[0]) +
+              row * (blockIdx.y ? p.stride[1] : p.stride[0]) + x);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Zeros in the rows before the first and behind the last of packed sequences.
+struct RestRows {
+  void* to[4];
+  int64_t stride[4], bytes[4];  // in bytes; bytes: of a row, 0 for no tensor
+  const int64_t* offsets;
+  int64_t rows;
+  int batch;
+};
+
+__global__ __launch_bounds__(256) void zero_rest_kernel(RestRows p) {
+  const int64_t a = offset_of(p.offsets, 0, 0, p.rows);
+  int64_t b = offset_of(p.offsets, p.batch, 0, p.rows);
+  if (b < a) b = a;
+  const int64_t rest = a + p.rows - b;
+  for (int64_t i = blockIdx.x; i < rest; i += gridDim.x) {
+    const int64_t row = i < a ? i : i - a + b;
+    for (int k = 0; k < 4; ++k)
+      for (int64_t x = 2 * threadIdx.x; x < p.bytes[k]; x += 512)
+        *reinterpret_cast<uint16_t*>(static_cast<char*>(p.to[k]) + row * p.stride[k] + x) = 0;
+  }
+}
+
+// ---------------------------------------------------------------------------
+
+size_t r256(size_t v) { return (v + 255) / 256 * 256; }
+
+int64_t compute_units() {
+  int dev = 0, n = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
+    n = 256;
+  return n;
+}
+
+int chunk_of(const LinattnSizes& n) { return (n.K > n.V ? n.K : n.V) > 128 ? 32 : 64; }
+int64_t chunks_of(const LinattnSizes& n) { return (n.rows + chunk_of(n) - 1) / chunk_of(n); }
+
+// Chunks of a segment, when `walks` workgroups walk each sequence. One segment per
+// sequence reads everything once; more let a few long sequences fill the machine, at
+// the price of reading keys and values twice. Of packed sequences the lengths are not
+// known here: they are cut as one would be, unless there are very many.
+constexpr int64_t kLeastPer = 8;
+int per_of(const LinattnSizes& n, int64_t walks) {
+  const int64_t chunks = chunks_of(n), want = 2 * compute_units();
+  const int64_t whole = chunks + 1;
+  const int64_t units = n.batch * walks;
+  if (units >= (n.packed ? 16 * want : want / 2)) return static_cast<int>(whole);
+  int64_t per = (chunks * walks + want - 1) / want;
+  if (per < kLeastPer) per = kLeastPer;
+  return static_cast<int>(per < whole ? per : whole);
+}
+bool split(const LinattnSizes& n, int per) { return per <= (n.packed ? chunks_of(n) : (n.seqlen - 1) / chunk_of(n)); }
+
+MixCall call_of(const LinattnProblem& p) {
+  MixCall w{};
+  w.offsets = p.offsets;
+  w.g = p.g;
+  w.g_step = p.head_decay ? 0 : p.n.heads;
+  w.seqlen = p.n.seqlen;
+  w.rows = p.n.rows;
+  w.batch = static_cast<int>(p.n.batch);
+  w.heads = static_cast<int>(p.n.heads);
+  w.mark = 1024 / chunk_of(p.n);
+  return w;
+}
+
+void set_segments(MixCall& w, const LinattnSizes& n, int per) {
+  w.per = per;
+  w.slots = slots_of(n.rows, n.batch, static_cast<int64_t>(per) * chunk_of(n));
+}
+
+// What a run's segments need of the workspace: their states and decays.
+struct SegmentBytes {
+  size_t states, gone;
+  size_t total() const { return states + gone; }
+};
+SegmentBytes segment_bytes(const LinattnSizes& n, int per) {
+  if (!split(n, per)) return {0, 0};
+  const size_t at = static_cast<size_t>(slots_of(n.rows, n.batch, static_cast<int64_t>(per) * chunk_of(n))) * n.heads;
+  return {r256(at * n.K * n.V * 4), r256(at * 4)};
+}
+
+void give_segments(MixRole& r, const SegmentBytes& s, char*& at) {
+  r.local = reinterpret_cast<float*>(at);
+  r.gone = reinterpret_cast<float*>(at + s.states);
+  at += s.total();
+}
+
+hipError_t walk(const MixCall& w, int io, int chunk, hipStream_t stream) {
+  return launch_walk_f32(w, io, chunk, stream);
+}
+
+// The runs of w: with segments, first what each leaves, then what enters each.
+hipError_t run(MixCall w, const LinattnSizes& n, bool cut, hipStream_t stream) {
+  const int chunk = chunk_of(n);
+  w.tiles = value_tiles(w.role[0].K, w.role[0].V);
+  if (cut) {
+    hipError_t e = walk(w, n.io, chunk, stream);
+    if (e != hipSuccess) return e;
+    const int64_t blocks = (n.K * n.V / 4 + kJoinThreads - 1) / kJoinThreads;
+    hipLaunchKernelGGL(join_kernel, dim3(static_cast<unsigned>(n.batch * n.heads * blocks), w.roles), dim3(kJoinThreads),
+                       0, stream, w, chunk, blocks);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  for (int k = 0; k < w.roles; ++k) {
+    w.role[k].enter = w.role[k].local;
+    w.role[k].local = nullptr;
+  }
+  return walk(w, n.io, chunk, stream);
+}
+
+hipError_t zero_rest(const RestRows& z, hipStream_t stream) {
+  hipLaunchKernelGGL(zero_rest_kernel, dim3(static_cast<unsigned>(z.rows < 2048 ? z.rows : 2048)), dim3(256), 0, stream, z);
+  return hipGetLastError();
+}
+
+// Workgroups of the backward's three runs for each sequence.
+int64_t bwd_walks(const LinattnSizes& n) { return n.heads * (value_tiles(n.K, n.V) + 2 * value_tiles(n.V, n.K)); }
+
+// The backward's workspace.
+struct BwdBytes {
+  SegmentBytes seg;
+  size_t marks, a, b, last, part, parts;
+  int64_t mark_slots;
+  size_t total() const { return 3 * seg.total() + 2 * marks + a + b + last + 2 * part + parts; }
+};
+BwdBytes bwd_bytes(const LinattnSizes& n, bool head_decay) {
+  BwdBytes s;
+  s.seg = segment_bytes(n, per_of(n, bwd_walks(n)));
+  s.mark_slots = slots_of(n.rows, n.batch, 1024);
+  s.marks = r256(static_cast<size_t>(s.mark_slots) * n.heads * n.K * n.V * 4);
+  s.a = r256(static_cast<size_t>(value_tiles(n.K, n.V)) * n.heads * n.rows * 4);
+  s.b = r256(static_cast<size_t>(value_tiles(n.V, n.K)) * n.heads * n.rows * 4);
+  s.last = r256(static_cast<size_t>(n.batch) * n.heads * n.K * n.V * 4);
+  s.part = n.heads == n.groups ? 0 : r256(static_cast<size_t>(n.rows) * n.heads * n.K * 4);
+  s.parts = head_decay ? r256(static_cast<size_t>(s.mark_slots) * n.heads * 4) : 0;
+  return s;
+}
+
+}  // namespace
+
+size_t linattn_fwd_workspace_bytes(const LinattnSizes& n) {
+  if (n.rows == 0 || n.heads == 0 || n.batch == 0) return 0;
+  return segment_bytes(n, per_of(n, n.heads * value_tiles(n.K, n.V))).total();
+}
+
+size_t linattn_bwd_workspace_bytes(const LinattnSizes& n, bool head_decay) {
+  if (n.rows == 0 || n.heads == 0 || n.batch == 0) return 0;
+  return bwd_bytes(n, head_decay).total();
+}
+
+hipError_t launch_linattn_fwd(const LinattnProblem& p, void* workspace, hipStream_t stream) {
+  const LinattnSizes& n = p.n;
+  const int eb = n.io == MAMBA_BF16 ? 2 : 4;
+  if (p.zero_rest && n.rows > 0) {
+    RestRows z{};
+    z.to[0] = p.out;
+    z.stride[0] = p.so * eb;
+    z.bytes[0] = n.heads * n.V * eb;
+    z.offsets = p.offsets;
+    z.rows = n.rows;
+    z.batch = static_cast<int>(n.batch);
+    const hipError_t e = zero_rest(z, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (n.batch == 0) return hipSuccess;
+  MixCall w = call_of(p);
+  const int per = per_of(n, n.heads * value_tiles(n.K, n.V));
+  set_segments(w, n, per);
+  w.roles = 1;
+  MixRole& r = w.role[0];
+  r.q = p.q;
+  r.k = p.k;
+  r.v = p.v;
+  r.o = p.out;
+  r.sq = p.sq;
+  r.sk = p.sk;
+  r.sv = p.sv;
+  r.so = p.so;
+  r.qdiv = r.kdiv = static_cast<int>(n.heads / n.groups);
+  r.vdiv = r.ediv = 1;
+  r.K = static_cast<int>(n.K);
+  r.V = static_cast<int>(n.V);
+  r.s0 = p.h0;
+  r.last = p.last_state;
+  r.score = r.from = p.scale;
+  r.to = 1.0f;
+  const bool cut = n.rows > 0 && split(n, per);
+  char* at = static_cast<char*>(workspace);
+  if (cut) give_segments(r, segment_bytes(n, per), at);
+  return run(w, n, cut, stream);
+}
+
+hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipStream_t stream) {
+  const LinattnProblem& f = p.f;
+  const LinattnSizes& n = f.n;
+  const int64_t eb = n.io == MAMBA_BF16 ? 2 : 4;
+  hipError_t e;
+  if (f.zero_rest && n.rows > 0) {
+    RestRows z{};
+    void* to[4] = {p.dq, p.dk, p.dv, f.head_decay ? nullptr : p.dg};
+    const int64_t stride[4] = {p.sdq * eb, p.sdk * eb, p.sdv * eb, n.heads * 4};
+    const int64_t bytes[4] = {n.groups * n.K * eb, n.groups * n.K * eb, n.heads * n.V * eb, n.heads * 4};
+    for (int k = 0; k < 4; ++k) {
+      z.to[k] = to[k];
+      z.stride[k] = stride[k];
+      z.bytes[k] = to[k] ? bytes[k] : 0;
+    }
+    z.offsets = f.offsets;
+    z.rows = n.rows;
+    z.batch = static_cast<int>(n.batch);
+    if ((e = zero_rest(z, stream)) != hipSuccess) return e;
+  }
+  const bool work = n.batch > 0 && n.rows > 0;
+  const BwdBytes s = work ? bwd_bytes(n, f.head_decay) : BwdBytes{};
+  char* at = static_cast<char*>(workspace);
+  auto take = [&at](size_t bytes) {
+    float* v = reinterpret_cast<float*>(at);
+    at += bytes;
+    return v;
+  };
+  if (n.batch > 0) {
+    MixCall w = call_of(f);
+    const int per = per_of(n, bwd_walks(n));
+    set_segments(w, n, per);
+    const bool cut = work && split(n, per);
+    const int share = static_cast<int>(n.heads / n.groups), K = static_cast<int>(n.K), V = static_cast<int>(n.V);
+    // dv: queries k, keys q, values dout, in reverse; the state is dS (K x V)
+    MixRole dv{};
+    dv.q = f.k;
+    dv.sq = f.sk;
+    dv.k = f.q;
+    dv.sk = f.sq;
+    dv.v = p.dout;
+    dv.sv = f.so;
+    dv.qdiv = dv.kdiv = share;
+    dv.vdiv = dv.ediv = 1;
+    dv.o = p.dv;
+    dv.so = p.sdv;
+    dv.K = K;
+    dv.V = V;
+    dv.s0 = p.dlast;
+    dv.last = p.dh0;
+    dv.reverse = true;
+    dv.score = dv.to = f.scale;
+    dv.from = 1.0f;
+    // dk: queries v, keys dout, values q, in reverse; dS^T (V x K)
+    MixRole dk{};
+    dk.q = f.v;
+    dk.sq = f.sv;
+    dk.k = p.dout;
+    dk.sk = f.so;
+    dk.v = f.q;
+    dk.sv = f.sq;
+    dk.qdiv = dk.kdiv = 1;
+    dk.vdiv = dk.ediv = share;
+    dk.o = p.dk;
+    dk.so = p.sdk;
+    dk.K = V;
+    dk.V = K;
+    dk.s0 = p.dlast;
+    dk.s0_turned = true;
+    dk.reverse = true;
+    dk.score = dk.to = f.scale;
+    dk.from = 1.0f;
+    // dq: queries dout, keys v, values k; S^T (V x K)
+    MixRole dq = dk;
+    dq.q = p.dout;
+    dq.sq = f.so;
+    dq.k = f.v;
+    dq.sk = f.sv;
+    dq.v = f.k;
+    dq.sv = f.sk;
+    dq.o = p.dq;
+    dq.so = p.sdq;
+    dq.s0 = f.h0;
+    dq.reverse = false;
+    dq.score = dq.from = f.scale;
+    dq.to = 1.0f;
+    if (cut)
+      for (MixRole* r : {&dv, &dk, &dq}) give_segments(*r, s.seg, at);
+    DecayGrad d{};
+    if (work && p.dg) {
+      dv.e = f.v;
+      dv.se = f.sv;
+      dv.marks = take(s.marks);
+      dv.sums = take(s.a);
+      dq.e = f.q;
+      dq.se = f.sq;
+      dq.marks = take(s.marks);
+      dq.sums = take(s.b);
+      dq.pairs = true;
+      if (p.dlast) dq.last = take(s.last);
+      d.w = w;
+      d.a = dv.sums;
+      d.b = dq.sums;
+      d.marks = dq.marks;
+      d.dmarks = dv.marks;
+      d.last = dq.last;
+      d.dlast = p.dlast;
+      d.dg = f.head_decay ? nullptr : p.dg;
+      d.parts = f.head_decay ? take(s.parts) : nullptr;
+      d.atiles = value_tiles(K, V);
+      d.btiles = value_tiles(V, K);
+      d.K = K;
+      d.V = V;
+    }
+    if (work && share > 1) {
+      dq.part = take(s.part);
+      dk.part = take(s.part);
+    }
+    // roles of the same shape go in one launch: their operands are the same rows
+    const bool same = key_tiles(K) == key_tiles(V) && value_waves(K, V) == value_waves(V, K) &&
+                      value_tiles(K, V) == value_tiles(V, K);
+    w.role[0] = dv;
+    w.roles = 1;
+    if (same) {
+      w.role[1] = dk;
+      w.role[2] = dq;
+      w.roles = 3;
+    }
+    if ((e = run(w, n, cut, stream)) != hipSuccess) return e;
+    if (!same) {
+      w.role[0] = dk;
+      w.role[1] = dq;
+      w.roles = 2;
+      if ((e = run(w, n, cut, stream)) != hipSuccess) return e;
+    }
+    if (work && share > 1) {
+      GroupSum gs{};
+      gs.part[0] = dq.part;
+      gs.part[1] = dk.part;
+      gs.to[0] = p.dq;
+      gs.to[1] = p.dk;
+      gs.stride[0] = p.sdq;
+      gs.stride[1] = p.sdk;
+      gs.offsets = f.offsets;
+      gs.rows = n.rows;
+      gs.pieces = n.groups * n.K / 8;
+      gs.heads = static_cast<int>(n.heads);
+      gs.groups = static_cast<int>(n.groups);
+      gs.K = K;
+      gs.batch = static_cast<int>(n.batch);
+      const int64_t groups = (n.rows * gs.pieces + 255) / 256;
+      const dim3 grid(static_cast<unsigned>(groups < (1 << 20) ? groups : 1 << 20), 2);
+      if (n.io == MAMBA_BF16)
+        hipLaunchKernelGGL((group_sum_kernel<Bf16Io>), grid, dim3(256), 0, stream, gs);
+      else
+        hipLaunchKernelGGL((group_sum_kernel<F32Io>), grid, dim3(256), 0, stream, gs);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (work && p.dg) {
+      const dim3 grid(static_cast<unsigned>(s.mark_slots * n.heads));
+      if (chunk_of(n) == 64)
+        hipLaunchKernelGGL((decay_grad_kernel<64>), grid, dim3(kDecayThreads), 0, stream, d);
+      else
+        hipLaunchKernelGGL((decay_grad_kernel<32>), grid, dim3(kDecayThreads), 0, stream, d);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      if (f.head_decay) return launch_colsum(d.parts, s.mark_slots, n.heads, StoreFlat{p.dg}, stream);
+    }
+  }
+  // no tokens: a decay that every token shares has the gradient 0
+  if (!work && p.dg && f.head_decay) return launch_colsum(nullptr, 0, n.heads, StoreFlat{p.dg}, stream);
+  return hipSuccess;
+}
+
+}  // namespace mscan
