@@ -23,15 +23,15 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmamba_scan.so")
 ARCH = "gfx950"
 
-SOURCES = ["api.cpp", "api_block.cpp", "api_mixer.cpp", "linattn_f32.hip", "linattn.hip", "linattn_update.hip", "qknorm.hip",
-           "scan_fwd.hip", "scan_split.hip", "scan_bwd.hip", "state_update.hip",
+SOURCES = ["api.cpp", "api_block.cpp", "api_mixer.cpp", "linattn_bf16.hip", "linattn_f32.hip", "linattn.hip",
+           "linattn_update.hip", "qknorm.hip", "scan_fwd.hip", "scan_split.hip", "scan_bwd.hip", "state_update.hip",
            "conv1d.hip", "ssd.hip", "gated.hip", "norm.hip", "conv_bwd.hip"]
 
 # A build of the gated recurrence's backward that spilled vector registers gave
 # wrong gradients where the same source with room gave right ones. Why is not
 # known, so such a build is not linked, whichever compiler made it.
-NO_SPILLS = ("gated.hip", "norm.hip", "conv_bwd.hip", "linattn.hip", "linattn_f32.hip", "linattn_update.hip",
-             "qknorm.hip")
+NO_SPILLS = ("gated.hip", "norm.hip", "conv_bwd.hip", "linattn.hip", "linattn_f32.hip", "linattn_bf16.hip",
+             "linattn_update.hip", "qknorm.hip")
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-I", CSRC]
 DEVICE = ["-x", "hip", "--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang",

@@ -99,8 +99,8 @@ __device__ __forceinline__ int sequence_at(const int64_t* offsets, int batch, in
 template <int C>
 struct Decays {
   double ell[C];
-  float in[C];     // of S_in in o_t; 0 where a cut lies between
-  float end[C];    // of a step in S_out; 0 where a cut lies between
+  float in[C];     // of S_in in o_t, times `from`; 0 where a cut lies between
+  float end[C];    // of a step in S_out, times `to`; 0 where a cut lies between
   int from[C];
   float all;       // of S_in in S_out; 0 with a cut
   int cut;         // whether there is one
@@ -111,7 +111,7 @@ __device__ __forceinline__ float exp_of(double v) { return hw_exp2(static_cast<f
 
 // Returns `all`.
 template <int C>
-__device__ __forceinline__ float chunk_decays(Decays<C>& d, float g, int n, bool reverse) {
+__device__ __forceinline__ float chunk_decays(Decays<C>& d, float g, int n, bool reverse, float from, float to) {
   const int i = threadIdx.x & 63;
   const bool live = i < n, cut = live && g <= kNoDecay;
   const double own = live && !cut ? static_cast<double>(g) : 0.0;
@@ -142,9 +142,9 @@ __device__ __forceinline__ float chunk_decays(Decays<C>& d, float g, int n, bool
   }
   if (i < C) {
     d.ell[i] = ell;
-    d.in[i] = seen < 0 ? exp_of(ell) : 0.0f;
+    d.in[i] = seen < 0 ? exp_of(ell) * from : 0.0f;
     d.from[i] = seen < 0 ? 0 : reverse ? seen + 1 : seen;
-    d.end[i] = live && (reverse ? i > cuts : i >= cuts) ? exp_of(total - ell) : 0.0f;
+    d.end[i] = live && (reverse ? i > cuts : i >= cuts) ? exp_of(total - ell) * to : 0.0f;
     if (i == 0) {
       d.all = all;
       d.cut = cuts >= 0;

@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) 
     const int n = s.len - c0 < C ? static_cast<int>(s.len - c0) : C;
     const bool live = lane < n;
     const float g = live ? w.g[row * w.g_step + head] : 0.0f;
-    const float kept = chunk_decays<C>(dec, g, n, false);
+    const float kept = chunk_decays<C>(dec, g, n, false, 1.0f, 1.0f);
     double a = 0.0, b = 0.0;
     if (live) {
       for (int k = 0; k < p.atiles; ++k) a += p.a[(static_cast<int64_t>(k) * w.heads + head) * w.rows + row];
@@ -269,7 +269,7 @@ void give_segments(MixRole& r, const SegmentBytes& s, char*& at) {
 }
 
 hipError_t walk(const MixCall& w, int io, int chunk, hipStream_t stream) {
-  return launch_walk_f32(w, io, chunk, stream);
+  return io == MAMBA_BF16 ? launch_walk_bf16(w, chunk, stream) : launch_walk_f32(w, chunk, stream);
 }
 
 // The runs of w: with segments, first what each leaves, then what enters each.

@@ -24,11 +24,10 @@ __device__ __forceinline__ f32x16 mfma(float a, float b, f32x16 c) {
 
 // KT: 32-row tiles of the state; NW: waves, 32 value channels each; CT: 32-step
 // tiles of a chunk.
-template <class IO, int KT, int NW, int CT>
+template <int KT, int NW, int CT>
 __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
   constexpr int C = 32 * CT, kK = 32 * KT, kV = 32 * NW, kThreads = 64 * NW;
   constexpr int ldk = kK + 4, ldv = kV + 4, ldp = C + 4;
-  using raw = typename IO::raw;
   __shared__ Decays<C> dec;
   __shared__ __align__(16) float s_q[C][ldk], s_k[C][ldk], s_v[C][ldv], s_e[C][ldv], s_p[C][ldp];
   __shared__ float s_red[NW][C], s_row[CT][C], s_col[CT][C];
@@ -50,8 +49,8 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
       const int row = id / per, x = 8 * (id % per);
       f32x4 a = {}, b = {};
       if (row < n && x < have) {
-        Piece<IO, 8> p;
-        p.load(static_cast<const raw*>(from) + (at.begin + at.token(row, c0, n)) * stride + first_col + x);
+        Piece<F32Io, 8> p;
+        p.load(static_cast<const float*>(from) + (at.begin + at.token(row, c0, n)) * stride + first_col + x);
         a = f32x4{p.get(0), p.get(1), p.get(2), p.get(3)};
         b = f32x4{p.get(4), p.get(5), p.get(6), p.get(7)};
       }
@@ -66,7 +65,7 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
     const int n = at.len - c0 < C ? static_cast<int>(at.len - c0) : C;
     if (wv == 0) {
       const float g = lane < n ? w.g[(at.begin + at.token(lane, c0, n)) * w.g_step + at.head] : 0.0f;
-      chunk_decays<C>(dec, g, n, r.reverse);
+      chunk_decays<C>(dec, g, n, r.reverse, r.from, r.to);
     }
     if (!r.local) stage(&s_q[0][0], ldk, kK, r.q, r.sq, (at.head / r.qdiv) * r.K, r.K, c0, n);
     stage(&s_k[0][0], ldk, kK, r.k, r.sk, (at.head / r.kdiv) * r.K, r.K, c0, n);
@@ -94,7 +93,8 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int s = 32 * si + 8 * (i >> 2) + 4 * hi + (i & 3);
-            p[i] = s <= t && s >= from ? p[i] * (exp_of(ell - dec.ell[s]) * r.score) : 0.0f;
+            const float f = exp_of(ell - dec.ell[s]) * r.score;
+            p[i] = where((s <= t) & (s >= from), p[i] * f);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -113,7 +113,7 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int s = 32 * si + 8 * (i >> 2) + 4 * hi + (i & 3);
-              u[i] = s < t && s >= from ? u[i] * p[i] : 0.0f;
+              u[i] = where((s < t) & (s >= from), u[i] * p[i]);
               sum += u[i];
               const float all = over_32(u[i]);
               if (lo == 0) s_col[ti][s] = all;
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
         for (int i = 0; i < 16; ++i) {
           const int t = 32 * ti + 8 * (i >> 2) + 4 * hi + (i & 3);
           const float f = dec.in[t];
-          acc[i] = f != 0.0f ? acc[i] * (f * r.from) : 0.0f;
+          acc[i] = where(f != 0.0f, acc[i] * f);
           if (r.sums) {
             const float all = over_32(acc[i] * s_e[t][32 * wv + lo]);
             if (lo == 0) s_red[wv][t] = all;
@@ -153,21 +153,22 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
           }
         // a score of 0 times a value that is not finite is NaN: where an output is not
         // finite, its steps are added one by one, those that it sees only
-        bool bad = false;
+        float worst = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) bad |= !(fabsf(acc[i]) <= 3.4028234e38f);
-        if (__any(bad)) {
+        for (int i = 0; i < 16; ++i) worst = fmaf(acc[i], 0.0f, worst);
+        if (__any(worst != 0.0f)) {
           acc = before;
           for (int s = 0; s < 32 * (ti + 1); ++s) {
             const float v = s_v[s][32 * wv + lo];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int t = 32 * ti + 8 * (i >> 2) + 4 * hi + (i & 3);
-              if (s <= t && s >= dec.from[t]) acc[i] = fmaf(s_p[t][s], v, acc[i]);
+              const float more = fmaf(s_p[t][s], v, acc[i]);
+              acc[i] = ((s <= t) & (s >= dec.from[t])) ? more : acc[i];
             }
           }
         }
-        at.store<IO>(w, r, acc, 32 * ti, c0, n, col, hi);
+        at.store<F32Io>(w, r, acc, 32 * ti, c0, n, col, hi);
       }
       if (r.sums) {
         __syncthreads();
@@ -187,16 +188,17 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) S[kt][i] = all != 0.0f ? S[kt][i] * all : 0.0f;
+      for (int i = 0; i < 16; ++i) S[kt][i] = where(all != 0.0f, S[kt][i] * all);
     }
     for (int s0 = 0; s0 < C; s0 += 8)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int s = s0 + 4 * hi + e;
         const float f = dec.end[s];
-        const float b = f != 0.0f ? s_v[s][32 * wv + lo] * (f * r.to) : 0.0f;
+        const bool on = f != 0.0f;
+        const float b = where(on, s_v[s][32 * wv + lo] * f);
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) S[kt] = mfma(f != 0.0f ? s_k[s][32 * kt + lo] : 0.0f, b, S[kt]);
+        for (int kt = 0; kt < KT; ++kt) S[kt] = mfma(where(on, s_k[s][32 * kt + lo]), b, S[kt]);
       }
     gone.add(dec.cut, dec.total);
     __syncthreads();  // the next chunk's rows take these places
@@ -204,29 +206,24 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
   at.leave_state<KT>(w, r, S, gone, col, hi);
 }
 
-template <class IO, int KT, int NW, int CT>
+template <int KT, int NW, int CT>
 hipError_t launch(const MixCall& w, hipStream_t stream) {
-  hipLaunchKernelGGL((walk_f32_kernel<IO, KT, NW, CT>), dim3(static_cast<unsigned>(walk_units(w))), dim3(64 * NW), 0,
+  hipLaunchKernelGGL((walk_f32_kernel<KT, NW, CT>), dim3(static_cast<unsigned>(walk_units(w))), dim3(64 * NW), 0,
                      stream, w);
   return hipGetLastError();
 }
 
-template <class IO>
-hipError_t by_shape(const MixCall& w, int chunk, hipStream_t stream) {
-  const int kt = key_tiles(w.role[0].K), nw = value_waves(w.role[0].K, w.role[0].V);
-  if (kt == 8) return launch<IO, 8, 2, 1>(w, stream);
-  if (chunk == 32) {
-    if (kt == 2) return nw == 2 ? launch<IO, 2, 2, 1>(w, stream) : launch<IO, 2, 4, 1>(w, stream);
-    return nw == 2 ? launch<IO, 4, 2, 1>(w, stream) : launch<IO, 4, 4, 1>(w, stream);
-  }
-  if (kt == 2) return nw == 2 ? launch<IO, 2, 2, 2>(w, stream) : launch<IO, 2, 4, 2>(w, stream);
-  return nw == 2 ? launch<IO, 4, 2, 2>(w, stream) : launch<IO, 4, 4, 2>(w, stream);
-}
-
 }  // namespace
 
-hipError_t launch_walk_f32(const MixCall& w, int io, int chunk, hipStream_t stream) {
-  return io == MAMBA_BF16 ? by_shape<Bf16Io>(w, chunk, stream) : by_shape<F32Io>(w, chunk, stream);
+hipError_t launch_walk_f32(const MixCall& w, int chunk, hipStream_t stream) {
+  const int kt = key_tiles(w.role[0].K), nw = value_waves(w.role[0].K, w.role[0].V);
+  if (kt == 8) return launch<8, 2, 1>(w, stream);
+  if (chunk == 32) {
+    if (kt == 2) return nw == 2 ? launch<2, 2, 1>(w, stream) : launch<2, 4, 1>(w, stream);
+    return nw == 2 ? launch<4, 2, 1>(w, stream) : launch<4, 4, 1>(w, stream);
+  }
+  if (kt == 2) return nw == 2 ? launch<2, 2, 2>(w, stream) : launch<2, 4, 2>(w, stream);
+  return nw == 2 ? launch<4, 2, 2>(w, stream) : launch<4, 4, 2>(w, stream);
 }
 
 }  // namespace mscan

@@ -23,6 +23,16 @@ __device__ __forceinline__ float over_32(float v) {
   return v;
 }
 
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t a = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t b = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(b) << 32 | a);
+}
+
+// v where `on`, else 0. The value is formed either way: written as a condition around
+// its expression, the compiler branches around each one.
+__device__ __forceinline__ float where(bool on, float v) { return on ? v : 0.0f; }
+
 // A segment's whole decay.
 struct Gone {
   double sum = 0.0;
@@ -49,10 +59,11 @@ struct Walk {
     head = static_cast<int>(u % w.heads);
     slot = u / w.heads;
     const int64_t steps = static_cast<int64_t>(w.per) * C;
-    seq = sequence_at(w.offsets, w.batch, w.seqlen, w.rows, steps, slot);
+    // (the same in every lane, which the compiler cannot see of values read from memory)
+    seq = __builtin_amdgcn_readfirstlane(sequence_at(w.offsets, w.batch, w.seqlen, w.rows, steps, slot));
     const Sequence s = sequence_of(w.offsets, seq, w.seqlen, w.rows);
-    begin = s.begin;
-    len = s.len;
+    begin = uniform(s.begin);
+    len = uniform(s.len);
     chunks = (len + C - 1) / C;
     const int64_t segs = chunks > w.per ? (chunks + w.per - 1) / w.per : 1;
     const int64_t seg = slot - first_slot(begin, seq, steps);
@@ -73,60 +84,80 @@ struct Walk {
     return c0 + (reverse ? n - 1 - row : row);
   }
 
-  // Register i of tile kt holds S[32 kt + 8 (i / 4) + 4 hi + i % 4][col].
-  static __device__ __forceinline__ int row_of(int kt, int i, int hi) { return 32 * kt + 8 * (i >> 2) + 4 * hi + (i & 3); }
+  // Register i of tile kt holds S[32 kt + 8 (i / 4) + 4 hi + i % 4][col], or with EIGHT
+  // S[32 kt + 16 (i / 8) + 8 hi + i % 8][col].
+  template <bool EIGHT = false>
+  static __device__ __forceinline__ int row_of(int kt, int i, int hi) {
+    return EIGHT ? 32 * kt + 16 * (i >> 3) + 8 * hi + (i & 7) : 32 * kt + 8 * (i >> 2) + 4 * hi + (i & 3);
+  }
 
-  template <int KT, class Tile>
+  // The part of row_of that lanes do not differ in, and the lane's own.
+  template <bool EIGHT>
+  static constexpr int row_base(int kt, int i) { return EIGHT ? row_eight(kt, i) : 32 * kt + 8 * (i >> 2) + (i & 3); }
+  static constexpr int row_eight(int kt, int i) { return 32 * kt + 16 * (i >> 3) + (i & 7); }
+
+  // States are reached through a buffer resource, so that a register's address is a
+  // scalar beside the lane's own; what lies past the state is out of its range.
+  template <int KT, bool EIGHT = false, class Tile>
   __device__ __forceinline__ void write(const MixRole& r, float* to, const Tile (&S)[KT], int col, int hi) const {
-    if (col >= r.V) return;
+    const auto rs = make_rsrc(to, static_cast<uint32_t>(r.K * r.V * 4));
+    const int first = (EIGHT ? 8 : 4) * hi;  // the lane's first row
+    const uint32_t lane = col < r.V ? static_cast<uint32_t>((first * r.V + col) * 4) : kOffNone;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int row = row_of(kt, i, hi);
-        if (row < r.K) to[static_cast<int64_t>(row) * r.V + col] = S[kt][i];
+        const int base = row_base<EIGHT>(kt, i);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[kt][i]), rs, first + base < r.K ? lane : kOffNone,
+                                              base * r.V * 4, 0);
       }
   }
 
-  template <int KT, class Tile>
+  template <int KT, bool EIGHT = false, class Tile>
   __device__ __forceinline__ void enter_state(const MixCall& w, const MixRole& r, Tile (&S)[KT], int col, int hi) const {
-    const int64_t size = static_cast<int64_t>(r.K) * r.V;
-    const float* from = entry ? r.s0 : r.enter;
-    if (r.local) from = nullptr;
-    if (from) from += ((entry ? seq : slot) * w.heads + head) * size;
+    const float* from = r.local ? nullptr : entry ? r.s0 : r.enter;
+    if (!from) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) S[kt] = Tile{};
+      return;
+    }
+    from += ((entry ? static_cast<int64_t>(seq) : slot) * w.heads + head) * r.K * r.V;
+    const auto rs = make_rsrc(from, static_cast<uint32_t>(r.K * r.V * 4));
     const bool turned = entry && r.s0_turned;
+    const int first = (EIGHT ? 8 : 4) * hi;
+    const uint32_t lane = static_cast<uint32_t>((turned ? col * r.K + first : first * r.V + col) * 4);
+    const int row_step = turned ? 4 : r.V * 4;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int row = row_of(kt, i, hi);
-        S[kt][i] = from && row < r.K && col < r.V ? from[turned ? static_cast<int64_t>(col) * r.K + row
-                                                                : static_cast<int64_t>(row) * r.V + col]
-                                                  : 0.0f;
+        const int base = row_base<EIGHT>(kt, i);
+        const uint32_t at = col < r.V && first + base < r.K ? lane : kOffNone;
+        S[kt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, base * row_step, 0));
       }
   }
 
   // The state between chunks, for the gradients of the decays: with time running
   // forward what enters chunk c, in reverse what enters it from behind.
-  template <int KT, class Tile>
+  template <int KT, bool EIGHT = false, class Tile>
   __device__ __forceinline__ void leave_mark(const MixCall& w, const MixRole& r, const Tile (&S)[KT], int64_t c, int64_t C,
                                              int col, int hi) const {
     if (!r.marks) return;
     const int64_t between = reverse ? c + 1 : c;
     if (between == 0 || between >= chunks || between % w.mark) return;
     const int64_t at = first_slot(begin, seq, w.mark * C) + between / w.mark;
-    write<KT>(r, r.marks + (at * w.heads + head) * r.K * r.V, S, col, hi);
+    write<KT, EIGHT>(r, r.marks + (at * w.heads + head) * r.K * r.V, S, col, hi);
   }
 
-  template <int KT, class Tile>
+  template <int KT, bool EIGHT = false, class Tile>
   __device__ __forceinline__ void leave_state(const MixCall& w, const MixRole& r, const Tile (&S)[KT], const Gone& gone,
                                               int col, int hi) const {
     const int64_t size = static_cast<int64_t>(r.K) * r.V;
     if (r.local) {
-      write<KT>(r, r.local + (slot * w.heads + head) * size, S, col, hi);
+      write<KT, EIGHT>(r, r.local + (slot * w.heads + head) * size, S, col, hi);
       if (threadIdx.x == 0 && tile == 0) r.gone[slot * w.heads + head] = gone.cut ? 0.0f : exp_of(gone.sum);
     } else if (r.last && exit) {
-      write<KT>(r, r.last + (static_cast<int64_t>(seq) * w.heads + head) * size, S, col, hi);
+      write<KT, EIGHT>(r, r.last + (static_cast<int64_t>(seq) * w.heads + head) * size, S, col, hi);
     }
   }
 
@@ -134,20 +165,22 @@ struct Walk {
   template <class IO, class Tile>
   __device__ __forceinline__ void store(const MixCall& w, const MixRole& r, const Tile& o, int t0, int64_t c0, int n,
                                         int col, int hi) const {
+    using raw = typename IO::raw;
+    const int64_t stride = r.part ? static_cast<int64_t>(w.heads) * r.V : r.so, step = reverse ? -stride : stride;
+    const int64_t at = (begin + token(0, c0, n)) * stride + static_cast<int64_t>(head) * r.V + col + (t0 + 4 * hi) * step;
     if (col >= r.V) return;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int t = t0 + row_of(0, i, hi);
-      if (t >= n) continue;
-      const int64_t row = begin + token(t, c0, n), at = static_cast<int64_t>(head) * r.V + col;
+      if (t0 + row_of(0, i, hi) >= n) continue;
       if (r.part)
-        r.part[row * w.heads * r.V + at] = o[i];
+        r.part[at + row_base<false>(0, i) * step] = o[i];
       else
-        static_cast<typename IO::raw*>(r.o)[row * r.so + at] = IO::from_f32(o[i]);
+        static_cast<raw*>(r.o)[at + row_base<false>(0, i) * step] = IO::from_f32(o[i]);
     }
   }
 };
 
-hipError_t launch_walk_f32(const MixCall& w, int io, int chunk, hipStream_t stream);
+hipError_t launch_walk_f32(const MixCall& w, int chunk, hipStream_t stream);
+hipError_t launch_walk_bf16(const MixCall& w, int chunk, hipStream_t stream);
 
 }  // namespace mscan

@@ -232,13 +232,15 @@ def test_strong_and_growing_decays(io):
 
 
 def test_gradients_are_optional():
+    # without dg the state goes into the products in two parts instead of three: the same
+    # values to the bound that holds for two (2^-17 of each term), not the same bits
     s = make(22, (2, 130), 4, 2, 64, 64, BF, states=2)
-    args = (s["q"], s["k"], s["v"], s["g"], s["dout"])
-    full = linear_attn_bwd(*args, h0=s["h0"], dlast=s["dlast"])
-    some = linear_attn_bwd(*args, h0=s["h0"], dlast=s["dlast"], want_dg=False, want_dh0=False)
+    some = linear_attn_bwd(s["q"], s["k"], s["v"], s["g"], s["dout"], h0=s["h0"], dlast=s["dlast"], want_dg=False,
+                           want_dh0=False)
     assert some["dg"] is None and some["dh0"] is None
+    ref = R.linattn(s["q"], s["k"], s["v"], s["g"], 64 ** -0.5, s["h0"], None, s["dout"], s["dlast"])
     for n in ("dq", "dk", "dv"):
-        assert torch.equal(some[n], full[n])
+        assert_within(n, some[n], rounded(ref[n], BF))
 
 
 def test_gradients_into_one_buffer():
