@@ -73,7 +73,7 @@ typedef struct mamba_linattn_desc {
  * be column slices of one projection's rows and their gradients of one
  * gradient's; 0 = contiguous (heads * head size). Elements within a row stay
  * contiguous. `out` is out's, or dout's in the backward. Below a row's length:
- * MAMBA_ERR_INVALID_ARG; above 2^26: MAMBA_ERR_UNSUPPORTED. A NULL struct means
+ * MAMBA_ERR_INVALID_ARG; above 2^23 (a row's length too): MAMBA_ERR_UNSUPPORTED. A NULL struct means
  * all contiguous. Any two inputs may interleave, and so may dq, dk and dv.
  */
 typedef struct mamba_linattn_strides {

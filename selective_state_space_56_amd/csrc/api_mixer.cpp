@@ -91,6 +91,9 @@ mamba_status resolve_linattn(const char* who, const mscan::LinattnSizes& n, cons
   const mamba_linattn_strides none = {0, 0, 0, 0, 0, 0, 0};
   const mamba_linattn_strides& v = s ? *s : none;
   const int64_t qk = n.groups * n.K, hv = n.heads * n.V;
+  for (int64_t given : {qk, hv, v.q, v.k, v.v, v.out, v.dq, v.dk, v.dv})
+    if (given > mscan::kMixMaxStride)
+      return fail(MAMBA_ERR_UNSUPPORTED, "%s: rows of %lld elements are too far apart", who, (long long)given);
   return resolve_all(who, n.rows,
                      {{"q", v.q, qk, &to->q}, {"k", v.k, qk, &to->k}, {"v", v.v, hv, &to->v}, {"out", v.out, hv, &to->out},
                       {"dq", v.dq, qk, &to->dq}, {"dk", v.dk, qk, &to->dk}, {"dv", v.dv, hv, &to->dv}});

@@ -36,7 +36,7 @@ struct MixRole {
   const float* s0;       // the state that enters a sequence, (batch, heads, K, V), or null
   const float* enter;    // the states that enter later segments, (slots, heads, K, V), or null
   float* last;           // (batch, heads, K, V) or null
-  float* marks;          // states at every `mark` chunks, (slots, heads, K, V), or null
+  float* marks;          // states at every kMarkSteps steps, (slots, heads, K, V), or null
   float* sums;           // (value tiles, heads, rows) or null
   float* local;          // a segment's own state, (slots, heads, K, V), instead of outputs; or null
   float* gone;           // with it: the segment's whole decay, (slots, heads)
@@ -55,8 +55,10 @@ struct MixCall {
   int64_t slots;           // segments at most, over all sequences
   int batch, heads, roles, tiles;
   int per;                 // chunks of a segment
-  int mark;                // chunks between two marks
 };
+
+// Steps between two marks: where the gradients of the decays start anew.
+constexpr int kMarkSteps = 1024;
 
 // Where a sequence lies. Offsets are read as they are found on the device, held
 // to 0 .. rows.
@@ -76,10 +78,13 @@ __device__ __forceinline__ Sequence sequence_of(const int64_t* offsets, int64_t 
 // Pieces of `steps` steps are counted through all sequences: piece p of sequence
 // i has slot offset_i / steps + i + p, which leaves room for each sequence's last
 // piece. The sequence of a slot is the last one that starts at or before it.
-__device__ __forceinline__ int64_t first_slot(int64_t begin, int64_t i, int64_t steps) { return begin / steps + i; }
+// (Rows are counted in 31 bits, and a segment has at most a chunk or two more.)
+__device__ __forceinline__ int64_t first_slot(int64_t begin, int64_t i, uint32_t steps) {
+  return static_cast<uint32_t>(begin) / steps + i;
+}
 inline int64_t slots_of(int64_t rows, int64_t batch, int64_t steps) { return rows / steps + batch; }
 
-__device__ __forceinline__ int sequence_at(const int64_t* offsets, int batch, int64_t seqlen, int64_t rows, int64_t steps,
+__device__ __forceinline__ int sequence_at(const int64_t* offsets, int batch, int64_t seqlen, int64_t rows, uint32_t steps,
                                            int64_t slot) {
   int lo = 0, hi = batch;  // lo: starts at or before the slot; hi: does not
   while (hi - lo > 1) {

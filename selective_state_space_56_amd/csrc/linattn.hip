@@ -21,17 +21,16 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk
   const int head = static_cast<int>(sh % w.heads);
   const int64_t seq = sh / w.heads;
   if (e >= size) return;
-  const int64_t steps = static_cast<int64_t>(w.per) * chunk;
   const Sequence s = sequence_of(w.offsets, seq, w.seqlen, w.rows);
-  const int64_t chunks = (s.len + chunk - 1) / chunk, base = first_slot(s.begin, seq, steps);
-  const int64_t segs = chunks > w.per ? (chunks + w.per - 1) / w.per : 1;
+  const int64_t base = first_slot(s.begin, seq, static_cast<uint32_t>(w.per) * chunk);
+  const int segs = segments_of(static_cast<int>((s.len + chunk - 1) / chunk), w.per);
   float cur[4] = {};
   if (r.s0) {
     const float* from = r.s0 + sh * size;
     for (int k = 0; k < 4; ++k)
       cur[k] = r.s0_turned ? from[(e + k) % r.V * r.K + (e + k) / r.V] : from[e + k];
   }
-  for (int64_t p = 0; p < segs; ++p) {
+  for (int p = 0; p < segs; ++p) {
     const int64_t at = (base + (r.reverse ? segs - 1 - p : p)) * w.heads + head;
     float* to = r.local + at * size + e;
     float own[4] = {}, gone = 0.0f;
@@ -81,15 +80,15 @@ __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) 
   const int tid = threadIdx.x, lane = tid & 63;
   const int head = blockIdx.x % w.heads;
   const int64_t slot = blockIdx.x / w.heads;
-  const int64_t steps = static_cast<int64_t>(w.mark) * C;
-  const int seq = sequence_at(w.offsets, w.batch, w.seqlen, w.rows, steps, slot);
+  constexpr int kMark = kMarkSteps / C;
+  const int seq = sequence_at(w.offsets, w.batch, w.seqlen, w.rows, kMarkSteps, slot);
   const Sequence s = sequence_of(w.offsets, seq, w.seqlen, w.rows);
-  const int64_t chunks = (s.len + C - 1) / C, m = slot - first_slot(s.begin, seq, steps), begin = m * w.mark;
+  const int64_t chunks = (s.len + C - 1) / C, m = slot - first_slot(s.begin, seq, kMarkSteps), begin = m * kMark;
   if (m < 0 || begin >= chunks) {  // (nothing of a sequence of no steps)
     if (p.parts && tid == 0) p.parts[slot * w.heads + head] = 0.0f;
     return;
   }
-  const int64_t end = begin + w.mark < chunks ? begin + w.mark : chunks;
+  const int64_t end = begin + kMark < chunks ? begin + kMark : chunks;
   // <S, dS> at the stretch's end
   const int64_t size = static_cast<int64_t>(p.K) * p.V;
   const float* S = p.marks + ((slot + 1) * w.heads + head) * size;
@@ -242,7 +241,6 @@ MixCall call_of(const LinattnProblem& p) {
   w.rows = p.n.rows;
   w.batch = static_cast<int>(p.n.batch);
   w.heads = static_cast<int>(p.n.heads);
-  w.mark = 1024 / chunk_of(p.n);
   return w;
 }
 
@@ -309,7 +307,7 @@ struct BwdBytes {
 BwdBytes bwd_bytes(const LinattnSizes& n, bool head_decay) {
   BwdBytes s;
   s.seg = segment_bytes(n, per_of(n, bwd_walks(n)));
-  s.mark_slots = slots_of(n.rows, n.batch, 1024);
+  s.mark_slots = slots_of(n.rows, n.batch, kMarkSteps);
   s.marks = r256(static_cast<size_t>(s.mark_slots) * n.heads * n.K * n.V * 4);
   s.a = r256(static_cast<size_t>(value_tiles(n.K, n.V)) * n.heads * n.rows * 4);
   s.b = r256(static_cast<size_t>(value_tiles(n.V, n.K)) * n.heads * n.rows * 4);

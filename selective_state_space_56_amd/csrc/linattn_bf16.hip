@@ -95,33 +95,37 @@ __device__ __forceinline__ float over_32_of_two(float a, float b) {
 }
 
 // One operand's rows of a chunk, 16 bytes at a time: W values per row (0 from `have`
-// on), N pieces per thread.
+// on), N pieces per thread. A chunk's rows are one buffer resource that ends with its
+// last row, so that rows past it read 0 and are not written without a condition (in
+// reverse they lie before its first row, which as an offset is out of range too).
+// Offsets stay below 2^31: rows are at most kMixMaxStride elements apart.
 template <int W, int C, int THREADS>
 struct Rows {
   static constexpr int kPer = W / 8, N = C * kPer / THREADS, kStep = THREADS / kPer;
   static_assert(C * kPer % THREADS == 0 && THREADS % kPer == 0, "whole rows of pieces");
   const uint16_t* base;
-  int64_t stride, lane;   // of rows; this lane's offset
-  int row, x;
-  bool has, back;
+  int stride;             // of rows, in bytes
+  uint32_t lane;          // this lane's offset
+  int row, x, width;      // width: of a row, in bytes
+  bool back;
 
   __device__ __forceinline__ Rows(const void* p, int64_t first_row, int64_t stride_, int64_t first_col, int have, bool reverse)
-      : base(static_cast<const uint16_t*>(p) + first_row * stride_ + first_col), stride(stride_), back(reverse) {
+      : base(static_cast<const uint16_t*>(p) + first_row * stride_ + first_col), stride(static_cast<int>(2 * stride_)),
+        width(2 * (have < W ? have : W)), back(reverse) {
     row = threadIdx.x / kPer;
     x = 8 * (threadIdx.x % kPer);
-    has = x < have;
-    lane = (reverse ? -row : row) * stride + x;
+    lane = x < have ? static_cast<uint32_t>((reverse ? -row : row) * stride + 2 * x) : kOffNone;
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk(int64_t c0, int n) const {
+    return make_rsrc(base + c0 * (stride / 2), static_cast<uint32_t>((n - 1) * stride + width));
   }
   // rows of a chunk that starts c0 steps into the sequence and has n
   __device__ __forceinline__ void load(u32x4 (&to)[N], int64_t c0, int n) const {
-    const uint16_t* p = base + (c0 + (back ? n - 1 : 0)) * stride;
-    const int64_t step = (back ? -kStep : kStep) * stride;
+    const auto rs = chunk(c0, n);
+    const int first = back ? (n - 1) * stride : 0, step = (back ? -kStep : kStep) * stride;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      Words<uint32_t, 4, 2> v = {};
-      if (has && row + i * kStep < n) v = *reinterpret_cast<const Words<uint32_t, 4, 2>*>(p + i * step + lane);
-      to[i] = u32x4{v[0], v[1], v[2], v[3]};
-    }
+    for (int i = 0; i < N; ++i)
+      to[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, lane + (first + i * step), 0, 0));
   }
   __device__ __forceinline__ void keep(const u32x4 (&from)[N], uint16_t* tile, int ld) const {
 #pragma unroll
@@ -129,32 +133,34 @@ struct Rows {
   }
 };
 
-// KT: 32-row tiles of the state; NW: waves; CT: 32-step tiles of a chunk; SUMS: with
+// KT: 32-row tiles of a wave's state; KH: waves that share the state's rows, KT tiles
+// each; NV: waves that share the value channels; CT: 32-step tiles of a chunk; SUMS: with
 // the sums for the decays' gradients.
-template <int KT, int NW, int CT, bool SUMS>
-__global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_kernel(MixCall w) {
-  constexpr int C = 32 * CT, kK = 32 * KT, kV = 32 * NW, kThreads = 64 * NW;
+template <int KT, int KH, int NV, int CT, bool SUMS>
+__global__ __launch_bounds__(64 * NV * KH, NV == 4 && !SUMS ? 2 : 1) void walk_bf16_kernel(MixCall w) {
+  constexpr int NW = NV * KH, C = 32 * CT, kK = 32 * KT * KH, kV = 32 * NV, kThreads = 64 * NW;
   constexpr int kW = kK > kV ? kK : kV;  // widest rows that the queries' tile holds
   // row strides of the tiles: rows read along, 16 bytes per lane, start 4 banks apart;
   // rows read by the transposing load 16 (values) or 20 (keys, which are read both
   // ways) banks apart
   constexpr int ldq = kW + 8, ldk = kK + (kK == 64 ? 24 : 40), ldv = kV + 32, ldp = C + 8;
   constexpr int kParts = SUMS ? 3 : 2;
-  constexpr bool kAhead = KT < 8;  // the next chunk's loads in flight, where there are registers for them
   __shared__ Decays<C> s_dec[2];
   __shared__ __align__(16) uint16_t s_q[C][ldq], s_k[C][ldk], s_v[C][ldv], s_p[2][C][ldp];
-  __shared__ float s_red[SUMS ? NW : 1][C], s_row[CT][C], s_col[CT][C];
+  __shared__ float s_red[SUMS ? NV : 1][C], s_row[CT][C], s_col[CT][C];
+  __shared__ float s_half[KH > 1 ? NV : 1][KH > 1 ? CT * 16 : 1][64];
   Walk at;
   if (!at.find(w, C)) return;
   const MixRole& r = w.role[at.role];
   const int tid = threadIdx.x, lane = tid & 63, lo = lane & 31, hi = lane >> 5;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col = at.tile * kV + 32 * wv + lo;  // this lane's value channel
+  const int vv = wv % NV, kh = wv / NV, k0 = 32 * KT * kh;  // this wave's channels and rows of the state
+  const int col = at.tile * kV + 32 * vv + lo;             // this lane's value channel
   const int vw = r.V - at.tile * kV;
   const bool outputs = r.local == nullptr, sums = SUMS && r.sums;
 
   f32x16 S[KT];
-  at.enter_state<KT, true>(w, r, S, col, hi);
+  at.enter_state<KT, true>(w, r, S, col, hi, k0);
 
   const Rows<kK, C, kThreads> rq(r.q, at.begin, r.sq, static_cast<int64_t>(at.head / r.qdiv) * r.K, r.K, at.reverse);
   const Rows<kK, C, kThreads> rk(r.k, at.begin, r.sk, static_cast<int64_t>(at.head / r.kdiv) * r.K, r.K, at.reverse);
@@ -180,10 +186,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_k
   int turn = 0;
   float g = 0.0f;
   if (at.first != at.stop) {
-    if (kAhead) {
-      fetch(at.first);
-      if (outputs) rq.load(q, static_cast<int64_t>(at.first) * C, tokens(at.first));
-    }
+    fetch(at.first);
+    if (outputs) rq.load(q, static_cast<int64_t>(at.first) * C, tokens(at.first));
     // the last wave, which has no scores to make, forms each chunk's decays one chunk ahead
     if (wv == NW - 1) {
       chunk_decays<C>(s_dec[0], gate(at.first), tokens(at.first), r.reverse, r.from, r.to);
@@ -194,14 +198,10 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_k
     const int64_t c0 = static_cast<int64_t>(c) * C;
     const int n = tokens(c), next = c + at.step;
     const Decays<C>& dec = s_dec[turn];
-    if (!kAhead) {
-      fetch(c);
-      if (outputs) rq.load(q, c0, n);
-    }
     rk.keep(k, &s_k[0][0], ldk);
     rv.keep(v, &s_v[0][0], ldv);
     if (outputs) rq.keep(q, &s_q[0][0], ldq);
-    if (kAhead && next != at.stop) fetch(next);
+    if (next != at.stop) fetch(next);
     if (sums) re.load(x, c0, n);
     __syncthreads();
     if (wv == NW - 1 && next != at.stop) {
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_k
     }
     f32x16 acc[CT];
     if (outputs) {
-      if (sums) at.leave_mark<KT, true>(w, r, S, c, C, col, hi);
+      if (sums) at.leave_mark<KT, true>(w, r, S, c, C, col, hi, k0);
       // scores, transposed (earlier steps s as rows, steps t as columns)
       f32x16 p = {};
       constexpr int kTiles = CT * (CT + 1) / 2;
@@ -284,21 +284,35 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_k
           }
 #pragma unroll
           for (int t = 0; t < CT; ++t) {
-            const u32x4 a = row8(&s_q[32 * t + lo][32 * kt + 16 * j + 8 * hi]);
+            const u32x4 a = row8(&s_q[32 * t + lo][k0 + 32 * kt + 16 * j + 8 * hi]);
 #pragma unroll
             for (int m = 0; m < kParts; ++m) acc[t] = mfma(a, part[m], acc[t]);
           }
         }
+      // (not with the others: registers)
+      if (next != at.stop) rq.load(q, static_cast<int64_t>(next) * C, tokens(next));
+      static_assert(KH <= 2, "one wave adds one other's");
+      if (KH > 1 && kh) {
+#pragma unroll
+        for (int i = 0; i < 16 * CT; ++i) s_half[vv][i][lane] = acc[i / 16][i % 16];
+      }
+      __syncthreads();
+      if (KH > 1 && !kh) {
+#pragma unroll
+        for (int i = 0; i < 16 * CT; ++i) acc[i / 16][i % 16] += s_half[vv][i][lane];
+      }
+      const bool cut = __builtin_amdgcn_readfirstlane(dec.cut);
 #pragma unroll
       for (int t = 0; t < CT; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float f = dec.in[32 * t + 8 * (i >> 2) + 4 * hi + (i & 3)];
-          acc[t][i] = where(f != 0.0f, acc[t][i] * f);
-        }
-      // (not with the others: registers)
-      if (kAhead && next != at.stop) rq.load(q, static_cast<int64_t>(next) * C, tokens(next));
-      __syncthreads();
+        for (int i = 0; i < 16; ++i) acc[t][i] *= dec.in[32 * t + 8 * (i >> 2) + 4 * hi + (i & 3)];
+      if (cut) {  // what a cut drops may be anything
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            acc[t][i] = where(dec.in[32 * t + 8 * (i >> 2) + 4 * hi + (i & 3)] != 0.0f, acc[t][i]);
+      }
       if (sums) {
         re.keep(x, &s_q[0][0], ldq);  // the queries are done with
         __syncthreads();
@@ -310,19 +324,19 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_k
           if (wv < kTiles) pairs(ti, si);
         }
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
+        for (int t = 0; t < CT && !kh; ++t)
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const int row = 32 * t + 8 * (i >> 2) + 4 * hi + (i & 3);
-            const float two = over_32_of_two(acc[t][i] * Bf16Io::to_f32(s_q[row][32 * wv + lo]),
-                                             acc[t][i + 1] * Bf16Io::to_f32(s_q[row + 1][32 * wv + lo]));
-            if ((lo & 15) == 0) s_red[wv][row + (lo >> 4)] = two;
+            const float two = over_32_of_two(acc[t][i] * Bf16Io::to_f32(s_q[row][32 * vv + lo]),
+                                             acc[t][i + 1] * Bf16Io::to_f32(s_q[row + 1][32 * vv + lo]));
+            if ((lo & 15) == 0) s_red[vv][row + (lo >> 4)] = two;
           }
         __syncthreads();  // the outputs take the rows' place
         if (tid < n) {
           float sum = 0.0f;
 #pragma unroll
-          for (int i = 0; i < NW; ++i) sum += s_red[i][tid];
+          for (int i = 0; i < NV; ++i) sum += s_red[i][tid];
           if (r.pairs) {
             for (int i = 0; i <= tid / 32; ++i) sum += s_row[i][tid];
             for (int i = tid / 32; i < CT; ++i) sum -= s_col[i][tid];
@@ -330,13 +344,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_k
           r.sums[(static_cast<int64_t>(at.tile) * w.heads + at.head) * w.rows + at.begin + at.token(tid, c0, n)] = sum;
         }
       }
+      if (!kh) {
       // A score of 0 times a value that is not finite is NaN: with such a value among this
       // wave's, steps are added one by one, to the outputs that see them only (whose score
       // is not -0).
       u16x2 most = {};
 #pragma unroll
       for (int j = 0; j < 2 * CT; ++j) {
-        const u32x4 b = column8<false>(&s_v[16 * j][32 * wv], ldv, lane);
+        const u32x4 b = column8<false>(&s_v[16 * j][32 * vv], ldv, lane);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, b[e] & 0x7fff7fffu));
@@ -344,7 +359,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_k
       if (!__any((most[0] >= 0x7f80) | (most[1] >= 0x7f80))) {
 #pragma unroll
         for (int j = 0; j < 2 * CT; ++j) {
-          const u32x4 b = column8<false>(&s_v[16 * j][32 * wv], ldv, lane);
+          const u32x4 b = column8<false>(&s_v[16 * j][32 * vv], ldv, lane);
 #pragma unroll
           for (int t = j / 2; t < CT; ++t) {
             acc[t] = mfma(row8(&s_p[0][32 * t + lo][16 * j + 8 * hi]), b, acc[t]);
@@ -354,7 +369,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_k
       } else {
 #pragma unroll 1
         for (int s = 0; s < n; ++s) {
-          const float value = Bf16Io::to_f32(s_v[s][32 * wv + lo]);
+          const float value = Bf16Io::to_f32(s_v[s][32 * vv + lo]);
 #pragma unroll
           for (int t = 0; t < CT; ++t)
 #pragma unroll
@@ -371,36 +386,42 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_k
         for (int t = 0; t < CT; ++t) at.store<Bf16Io>(w, r, acc[t], 32 * t, c0, n, col, hi);
       } else {
         // through the queries' place (this wave's columns of it), as pieces of rows
-        uint16_t* to = &s_q[0][32 * wv];
+        uint16_t* to = &s_q[0][32 * vv];
 #pragma unroll
         for (int t = 0; t < CT; ++t)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            to[(32 * t + 8 * (i >> 2) + 4 * hi + (i & 3)) * ldq + lo] = Bf16Io::from_f32(acc[t][i]);
-        __builtin_amdgcn_wave_barrier();
-        const int piece = 8 * (lane & 3);
-        uint16_t* out = static_cast<uint16_t*>(r.o) + (at.begin + c0 + (at.reverse ? n - 1 : 0)) * r.so +
-                        static_cast<int64_t>(at.head) * r.V + at.tile * kV + 32 * wv + piece;
-        if (32 * wv + piece < vw) {
-#pragma unroll
-          for (int i = 0; i < C / 16; ++i) {
-            const int row = 16 * i + (lane >> 2);
-            if (row < n) {
-              const u32x4 o = row8(to + row * ldq + piece);
-              *reinterpret_cast<Words<uint32_t, 4, 2>*>(out + (at.reverse ? -row : row) * r.so) =
-                  Words<uint32_t, 4, 2>{o[0], o[1], o[2], o[3]};
-            }
+          for (int i = 0; i < 16; i += 2) {
+            const uint32_t two = pack(acc[t][i], acc[t][i + 1]);
+            const int row = 32 * t + 8 * (i >> 2) + 4 * hi + (i & 3);
+            to[row * ldq + lo] = static_cast<uint16_t>(two);
+            to[(row + 1) * ldq + lo] = static_cast<uint16_t>(two >> 16);
           }
-        }
+        __builtin_amdgcn_wave_barrier();
+        const int piece = 8 * (lane & 3), stride = static_cast<int>(2 * r.so);
+        const auto rs = make_rsrc(static_cast<uint16_t*>(r.o) + (at.begin + c0) * r.so + static_cast<int64_t>(at.head) * r.V +
+                                      at.tile * kV + 32 * vv,
+                                  static_cast<uint32_t>((n - 1) * stride + 2 * (vw - 32 * vv < 32 ? vw - 32 * vv : 32)));
+        const uint32_t own =
+            32 * vv + piece < vw ? static_cast<uint32_t>((at.reverse ? n - 1 - (lane >> 2) : lane >> 2) * stride + 2 * piece)
+                                 : kOffNone;
+#pragma unroll
+        for (int i = 0; i < C / 16; ++i)
+          __builtin_amdgcn_raw_buffer_store_b128(row8(to + (16 * i + (lane >> 2)) * ldq + piece), rs,
+                                                 own + (at.reverse ? -16 : 16) * i * stride, 0, 0);
         __builtin_amdgcn_wave_barrier();
       }
+      }
     }
-    if (dec.cut) {
-      // steps that a later one cuts off: their keys too, which may be anything
-      if (!outputs) __syncthreads();
+    if (__builtin_amdgcn_readfirstlane(dec.cut)) {
+      // the rows of steps that a later one cuts off, which may be anything, become 0
+      __syncthreads();
       for (int id = tid; id < C * kK / 2; id += kThreads) {
         const int s = id / (kK / 2);
         if (dec.end[s] == 0.0f) *reinterpret_cast<uint32_t*>(&s_k[s][2 * (id % (kK / 2))]) = 0;
+      }
+      for (int id = tid; id < C * kV / 2; id += kThreads) {
+        const int s = id / (kV / 2);
+        if (dec.end[s] == 0.0f) *reinterpret_cast<uint32_t*>(&s_v[s][2 * (id % (kV / 2))]) = 0;
       }
       __syncthreads();
     }
@@ -414,7 +435,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_k
     }
 #pragma unroll
     for (int j = 0; j < 2 * CT; ++j) {
-      const u32x4 b = column8<false>(&s_v[16 * j][32 * wv], ldv, lane);
+      const u32x4 b = column8<false>(&s_v[16 * j][32 * vv], ldv, lane);
       const f32x4 f0 = *reinterpret_cast<const f32x4*>(&dec.end[16 * j + 8 * hi]);
       const f32x4 f1 = *reinterpret_cast<const f32x4*>(&dec.end[16 * j + 8 * hi + 4]);
       u32x4 part[3];
@@ -422,13 +443,13 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_k
       for (int e = 0; e < 4; ++e) {
         const float a = e < 2 ? f0[2 * e] : f1[2 * e - 4], z = e < 2 ? f0[2 * e + 1] : f1[2 * e - 3];
         uint32_t words[3];
-        split<3>(where(a != 0.0f, low(b[e]) * a), where(z != 0.0f, high(b[e]) * z), words);
+        split<3>(low(b[e]) * a, high(b[e]) * z, words);
 #pragma unroll
         for (int m = 0; m < 3; ++m) part[m][e] = words[m];
       }
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        const u32x4 a = column8<true>(&s_k[16 * j][32 * kt], ldk, lane);
+        const u32x4 a = column8<true>(&s_k[16 * j][k0 + 32 * kt], ldk, lane);
 #pragma unroll
         for (int m = 0; m < 3; ++m) S[kt] = mfma(a, part[m], S[kt]);
       }
@@ -436,18 +457,18 @@ __global__ __launch_bounds__(64 * NW, NW == 4 && !SUMS ? 2 : 1) void walk_bf16_k
     gone.add(dec.cut, dec.total);
     __syncthreads();  // the next chunk's rows take these places
   }
-  at.leave_state<KT, true>(w, r, S, gone, col, hi);
+  at.leave_state<KT, true>(w, r, S, gone, col, hi, k0);
 }
 
-template <int KT, int NW, int CT>
+template <int KT, int KH, int NV, int CT>
 hipError_t launch(const MixCall& w, hipStream_t stream) {
   bool sums = false;
   for (int k = 0; k < w.roles; ++k) sums |= w.role[k].sums != nullptr && !w.role[k].local;
   const dim3 grid(static_cast<unsigned>(walk_units(w)));
   if (sums)
-    hipLaunchKernelGGL((walk_bf16_kernel<KT, NW, CT, true>), grid, dim3(64 * NW), 0, stream, w);
+    hipLaunchKernelGGL((walk_bf16_kernel<KT, KH, NV, CT, true>), grid, dim3(64 * NV * KH), 0, stream, w);
   else
-    hipLaunchKernelGGL((walk_bf16_kernel<KT, NW, CT, false>), grid, dim3(64 * NW), 0, stream, w);
+    hipLaunchKernelGGL((walk_bf16_kernel<KT, KH, NV, CT, false>), grid, dim3(64 * NV * KH), 0, stream, w);
   return hipGetLastError();
 }
 
@@ -459,13 +480,13 @@ template __global__ void walk_bf16_kernel<ONLY, false>(MixCall);
 }  // namespace
 hipError_t launch_walk_bf16(const MixCall& w, int chunk, hipStream_t stream) {
   const int kt = key_tiles(w.role[0].K), nw = value_waves(w.role[0].K, w.role[0].V);
-  if (kt == 8) return launch<8, 2, 1>(w, stream);
+  if (kt == 8) return launch<4, 2, 2, 1>(w, stream);
   if (chunk == 32) {
-    if (kt == 2) return nw == 2 ? launch<2, 2, 1>(w, stream) : launch<2, 4, 1>(w, stream);
-    return nw == 2 ? launch<4, 2, 1>(w, stream) : launch<4, 4, 1>(w, stream);
+    if (kt == 2) return nw == 2 ? launch<2, 1, 2, 1>(w, stream) : launch<2, 1, 4, 1>(w, stream);
+    return nw == 2 ? launch<4, 1, 2, 1>(w, stream) : launch<4, 1, 4, 1>(w, stream);
   }
-  if (kt == 2) return nw == 2 ? launch<2, 2, 2>(w, stream) : launch<2, 4, 2>(w, stream);
-  return nw == 2 ? launch<4, 2, 2>(w, stream) : launch<4, 4, 2>(w, stream);
+  if (kt == 2) return nw == 2 ? launch<2, 1, 2, 2>(w, stream) : launch<2, 1, 4, 2>(w, stream);
+  return nw == 2 ? launch<4, 1, 2, 2>(w, stream) : launch<4, 1, 4, 2>(w, stream);
 }
 #endif
 

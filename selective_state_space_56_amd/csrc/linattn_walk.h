@@ -6,8 +6,9 @@
 
 namespace mscan {
 
-// 32-row tiles of a workgroup's state, and its waves, each with 32 value channels. (With
-// 8 tiles, 128 registers of state, four waves' kernel would need more than there are.)
+// 32-row tiles of a workgroup's state, and its waves of 32 value channels each. (With 8
+// tiles, 128 registers of state, the float32 kernel has registers for two waves only; the
+// bfloat16 one shares the rows among two pairs of waves.)
 inline int key_tiles(int64_t K) { return K <= 64 ? 2 : K <= 128 ? 4 : 8; }
 inline int value_waves(int64_t K, int64_t V) { return V <= 64 || key_tiles(K) == 8 ? 2 : 4; }
 inline int value_tiles(int64_t K, int64_t V) {
@@ -22,6 +23,8 @@ __device__ __forceinline__ float over_32(float v) {
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor(v, off);
   return v;
 }
+
+__device__ __forceinline__ int segments_of(int chunks, int per) { return chunks > per ? (chunks + per - 1) / per : 1; }
 
 __device__ __forceinline__ int64_t uniform(int64_t v) {
   const uint32_t a = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
@@ -45,36 +48,37 @@ struct Gone {
 
 struct Walk {
   int role, tile, head, seq;
-  int64_t slot, begin, len, chunks;
+  int64_t slot, begin, len;
+  int chunks;
   int first, stop, step;      // chunks: first, first + step, ... before stop
   bool entry, exit, reverse;  // whether the segment is its sequence's first or last on the way
 
   // False for a workgroup that has nothing to do.
   __device__ __forceinline__ bool find(const MixCall& w, int C) {
-    int64_t u = blockIdx.x;
-    role = static_cast<int>(u % w.roles);
+    uint32_t u = blockIdx.x;
+    role = u % w.roles;
     u /= w.roles;
-    tile = static_cast<int>(u % w.tiles);
+    tile = u % w.tiles;
     u /= w.tiles;
-    head = static_cast<int>(u % w.heads);
+    head = u % w.heads;
     slot = u / w.heads;
-    const int64_t steps = static_cast<int64_t>(w.per) * C;
+    const uint32_t steps = static_cast<uint32_t>(w.per) * C;
     // (the same in every lane, which the compiler cannot see of values read from memory)
     seq = __builtin_amdgcn_readfirstlane(sequence_at(w.offsets, w.batch, w.seqlen, w.rows, steps, slot));
     const Sequence s = sequence_of(w.offsets, seq, w.seqlen, w.rows);
     begin = uniform(s.begin);
     len = uniform(s.len);
-    chunks = (len + C - 1) / C;
-    const int64_t segs = chunks > w.per ? (chunks + w.per - 1) / w.per : 1;
-    const int64_t seg = slot - first_slot(begin, seq, steps);
+    chunks = static_cast<int>((len + C - 1) / C);
+    const int segs = segments_of(chunks, w.per);
+    const int seg = static_cast<int>(slot - first_slot(begin, seq, steps));
     if (seg < 0 || seg >= segs) return false;
     reverse = w.role[role].reverse;
     entry = seg == (reverse ? segs - 1 : 0);
     exit = seg == (reverse ? 0 : segs - 1);
     if (w.role[role].local && exit) return false;  // nobody enters with what it leaves
-    const int64_t a = seg * w.per, b = a + w.per < chunks ? a + w.per : chunks;
-    first = static_cast<int>(reverse ? b - 1 : a);
-    stop = static_cast<int>(reverse ? a - 1 : b);
+    const int a = seg * w.per, b = a + w.per < chunks ? a + w.per : chunks;
+    first = reverse ? b - 1 : a;
+    stop = reverse ? a - 1 : b;
     step = reverse ? -1 : 1;
     return true;
   }
@@ -99,22 +103,28 @@ struct Walk {
   // States are reached through a buffer resource, so that a register's address is a
   // scalar beside the lane's own; what lies past the state is out of its range.
   template <int KT, bool EIGHT = false, class Tile>
-  __device__ __forceinline__ void write(const MixRole& r, float* to, const Tile (&S)[KT], int col, int hi) const {
+  __device__ __forceinline__ void write(const MixRole& r, float* to, const Tile (&S)[KT], int col, int hi,
+                                        int row0 = 0) const {
     const auto rs = make_rsrc(to, static_cast<uint32_t>(r.K * r.V * 4));
-    const int first = (EIGHT ? 8 : 4) * hi;  // the lane's first row
+    const int first = row0 + (EIGHT ? 8 : 4) * hi;  // the lane's first row
     const uint32_t lane = col < r.V ? static_cast<uint32_t>((first * r.V + col) * 4) : kOffNone;
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+    for (int kt = 0; kt < KT; ++kt) {
+      int row_step = r.V * 4;
+      asm volatile("" : "+s"(row_step));  // formed here, not kept for every register from the kernel's start on
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int base = row_base<EIGHT>(kt, i);
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[kt][i]), rs, first + base < r.K ? lane : kOffNone,
-                                              base * r.V * 4, 0);
+                                              base * row_step, 0);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 
   template <int KT, bool EIGHT = false, class Tile>
-  __device__ __forceinline__ void enter_state(const MixCall& w, const MixRole& r, Tile (&S)[KT], int col, int hi) const {
+  __device__ __forceinline__ void enter_state(const MixCall& w, const MixRole& r, Tile (&S)[KT], int col, int hi,
+                                              int row0 = 0) const {
     const float* from = r.local ? nullptr : entry ? r.s0 : r.enter;
     if (!from) {
 #pragma unroll
@@ -124,40 +134,42 @@ struct Walk {
     from += ((entry ? static_cast<int64_t>(seq) : slot) * w.heads + head) * r.K * r.V;
     const auto rs = make_rsrc(from, static_cast<uint32_t>(r.K * r.V * 4));
     const bool turned = entry && r.s0_turned;
-    const int first = (EIGHT ? 8 : 4) * hi;
+    const int first = row0 + (EIGHT ? 8 : 4) * hi;
     const uint32_t lane = static_cast<uint32_t>((turned ? col * r.K + first : first * r.V + col) * 4);
-    const int row_step = turned ? 4 : r.V * 4;
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+    for (int kt = 0; kt < KT; ++kt) {
+      int row_step = turned ? 4 : r.V * 4;
+      asm volatile("" : "+s"(row_step));
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int base = row_base<EIGHT>(kt, i);
         const uint32_t at = col < r.V && first + base < r.K ? lane : kOffNone;
         S[kt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, base * row_step, 0));
       }
+      __builtin_amdgcn_sched_barrier(0);  // (a tile's addresses at a time)
+    }
   }
 
   // The state between chunks, for the gradients of the decays: with time running
   // forward what enters chunk c, in reverse what enters it from behind.
   template <int KT, bool EIGHT = false, class Tile>
-  __device__ __forceinline__ void leave_mark(const MixCall& w, const MixRole& r, const Tile (&S)[KT], int64_t c, int64_t C,
-                                             int col, int hi) const {
-    if (!r.marks) return;
-    const int64_t between = reverse ? c + 1 : c;
-    if (between == 0 || between >= chunks || between % w.mark) return;
-    const int64_t at = first_slot(begin, seq, w.mark * C) + between / w.mark;
-    write<KT, EIGHT>(r, r.marks + (at * w.heads + head) * r.K * r.V, S, col, hi);
+  __device__ __forceinline__ void leave_mark(const MixCall& w, const MixRole& r, const Tile (&S)[KT], int c, int C, int col,
+                                             int hi, int row0 = 0) const {
+    const int between = reverse ? c + 1 : c, mark = kMarkSteps / C;
+    if (!r.marks || between == 0 || between >= chunks || between % mark) return;
+    const int64_t at = first_slot(begin, seq, kMarkSteps) + between / mark;
+    write<KT, EIGHT>(r, r.marks + (at * w.heads + head) * r.K * r.V, S, col, hi, row0);
   }
 
   template <int KT, bool EIGHT = false, class Tile>
   __device__ __forceinline__ void leave_state(const MixCall& w, const MixRole& r, const Tile (&S)[KT], const Gone& gone,
-                                              int col, int hi) const {
+                                              int col, int hi, int row0 = 0) const {
     const int64_t size = static_cast<int64_t>(r.K) * r.V;
     if (r.local) {
-      write<KT, EIGHT>(r, r.local + (slot * w.heads + head) * size, S, col, hi);
+      write<KT, EIGHT>(r, r.local + (slot * w.heads + head) * size, S, col, hi, row0);
       if (threadIdx.x == 0 && tile == 0) r.gone[slot * w.heads + head] = gone.cut ? 0.0f : exp_of(gone.sum);
     } else if (r.last && exit) {
-      write<KT, EIGHT>(r, r.last + (static_cast<int64_t>(seq) * w.heads + head) * size, S, col, hi);
+      write<KT, EIGHT>(r, r.last + (static_cast<int64_t>(seq) * w.heads + head) * size, S, col, hi, row0);
     }
   }
 

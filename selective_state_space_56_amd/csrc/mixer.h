@@ -59,6 +59,9 @@ struct LinattnUpdateProblem {
   int64_t sq, sk, sv, so;
 };
 
+// Elements between two token rows at most: 64 rows are addressed in 31 bits.
+constexpr int64_t kMixMaxStride = int64_t(1) << 23;
+
 // Token rows times heads, and states, of one call at most: what the kernels
 // count in 31 bits.
 constexpr int64_t kLinattnMaxRowHeads = (int64_t(1) << 31) - 1;
