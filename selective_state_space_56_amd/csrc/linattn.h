@@ -37,12 +37,12 @@ struct MixRole {
   const float* enter;    // the states that enter later segments, (slots, heads, K, V), or null
   float* last;           // (batch, heads, K, V) or null
   float* marks;          // states at every kMarkSteps steps, (slots, heads, K, V), or null
-  float* sums;           // (value tiles, heads, rows) or null
+  float* sums;           // (2, value tiles, heads, rows) or null: for each step t, e_t . what S_in gives
+                         // of o_t, and sum_{s < t} of score (s, t) times e_t . v_s
   float* local;          // a segment's own state, (slots, heads, K, V), instead of outputs; or null
   float* gone;           // with it: the segment's whole decay, (slots, heads)
   bool s0_turned;        // s0 is (.., V, K)
   bool reverse;
-  bool pairs;            // the sums take what the chunk's own pairs give too
   float score, from, to; // factors of the chunk's scores, of what S_in gives, of what a step adds to S
 };
 
@@ -107,16 +107,27 @@ struct Decays {
   float in[C];     // of S_in in o_t, times `from`; 0 where a cut lies between
   float end[C];    // of a step in S_out, times `to`; 0 where a cut lies between
   int from[C];
+  // Scores' factors e^{ell_t - ell_s} as up[t] down[s] (times `score`), where that is safe:
+  // `flat` without a cut, with no g above 0 and 100 of decay at most.
+  float up[C], down[C];
+  int flat;
   float all;       // of S_in in S_out; 0 with a cut
   int cut;         // whether there is one
   double total;    // the sum of the others
 };
 
+// e^v for the difference of two sums; the float32 argument is off by 2^-24 of |v|
 __device__ __forceinline__ float exp_of(double v) { return hw_exp2(static_cast<float>(v) * kLog2e); }
+// e^v to float32 whatever |v|: the whole part of log2 of it taken apart
+__device__ __forceinline__ float exp_exactly(double v) {
+  const double v2 = v * 1.44269504088896340736;
+  const double whole = rint(v2 < -400.0 ? -400.0 : v2 > 400.0 ? 400.0 : v2);
+  return ldexpf(hw_exp2(static_cast<float>(v2 - whole)), static_cast<int>(whole));
+}
 
 // Returns `all`.
 template <int C>
-__device__ __forceinline__ float chunk_decays(Decays<C>& d, float g, int n, bool reverse, float from, float to) {
+__device__ __forceinline__ float chunk_decays(Decays<C>& d, float g, int n, bool reverse, float from, float to, float score) {
   const int i = threadIdx.x & 63;
   const bool live = i < n, cut = live && g <= kNoDecay;
   const double own = live && !cut ? static_cast<double>(g) : 0.0;
@@ -133,7 +144,8 @@ __device__ __forceinline__ float chunk_decays(Decays<C>& d, float g, int n, bool
   }
   const double total = __shfl(sum, 63);
   const int cuts = __shfl(last, 63);
-  const float all = cuts < 0 ? exp_of(total) : 0.0f;
+  const float all = cuts < 0 ? exp_exactly(total) : 0.0f;
+  const bool flat = cuts < 0 && total > -100.0 && !__any(live && !(g <= 0.0f));
   double ell = sum;
   int seen = last;
   if (reverse) {
@@ -147,11 +159,14 @@ __device__ __forceinline__ float chunk_decays(Decays<C>& d, float g, int n, bool
   }
   if (i < C) {
     d.ell[i] = ell;
-    d.in[i] = seen < 0 ? exp_of(ell) * from : 0.0f;
+    d.in[i] = seen < 0 ? exp_exactly(ell) * from : 0.0f;
+    d.up[i] = exp_exactly(ell - 0.5 * total) * score;
+    d.down[i] = exp_exactly(0.5 * total - ell);
     d.from[i] = seen < 0 ? 0 : reverse ? seen + 1 : seen;
-    d.end[i] = live && (reverse ? i > cuts : i >= cuts) ? exp_of(total - ell) * to : 0.0f;
+    d.end[i] = live && (reverse ? i > cuts : i >= cuts) ? exp_exactly(total - ell) * to : 0.0f;
     if (i == 0) {
       d.all = all;
+      d.flat = flat;
       d.cut = cuts >= 0;
       d.total = total;
     }

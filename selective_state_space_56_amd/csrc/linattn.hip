@@ -49,9 +49,10 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk
 
 // ---------------------------------------------------------------------------
 // Gradients of the decays. For step t of a chunk, with what the two runs' sums
-// hold (a_s = end_s k_s . (dS_out v_s), b_u = in_u scale q_u . (S_in dout_u) and the
-// chunk's own pairs (u, s), added at u and taken off at s):
-//   dg_t = e^{ell_C} <S_in, dS_out> + sum_{s < t} a_s + sum_{u >= t} b_u
+// hold (a_s = end_s k_s . (dS_out v_s), b_u = in_u scale q_u . (S_in dout_u), and of the
+// chunk's own pairs c_s, those that later steps make with s, and d_u, those that u makes
+// with earlier ones):
+//   dg_t = e^{ell_C} <S_in, dS_out> + sum_{s < t} a_s + sum_{u >= t} (b_u + d_u - c_u)
 // Every term is of the size of the result: the difference of q . dq and k . dk
 // summed from the sequence's end, which is the same, would lose what strong decays
 // leave. The first term goes from chunk to chunk, <S_out, dS_out> - sum a + sum b,
@@ -61,8 +62,8 @@ constexpr int kDecayThreads = 256;
 
 struct DecayGrad {
   MixCall w;                 // sequences; per is not used
-  const float* a;            // (atiles, heads, rows)
-  const float* b;            // (btiles, heads, rows)
+  const float* a;            // (2, atiles, heads, rows): a, c
+  const float* b;            // (2, btiles, heads, rows): b, d
   const float* marks;        // (slots, heads, V, K): states
   const float* dmarks;       // (slots, heads, K, V): their gradients
   const float* last;         // (batch, heads, V, K) or null
@@ -113,11 +114,19 @@ __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) 
     const int n = s.len - c0 < C ? static_cast<int>(s.len - c0) : C;
     const bool live = lane < n;
     const float g = live ? w.g[row * w.g_step + head] : 0.0f;
-    const float kept = chunk_decays<C>(dec, g, n, false, 1.0f, 1.0f);
+    const float kept = chunk_decays<C>(dec, g, n, false, 1.0f, 1.0f, 1.0f);
     double a = 0.0, b = 0.0;
     if (live) {
-      for (int k = 0; k < p.atiles; ++k) a += p.a[(static_cast<int64_t>(k) * w.heads + head) * w.rows + row];
-      for (int k = 0; k < p.btiles; ++k) b += p.b[(static_cast<int64_t>(k) * w.heads + head) * w.rows + row];
+      for (int k = 0; k < p.atiles; ++k) {
+        const float* from = p.a + (static_cast<int64_t>(k) * w.heads + head) * w.rows + row;
+        a += from[0];
+        b -= from[static_cast<int64_t>(p.atiles) * w.heads * w.rows];
+      }
+      for (int k = 0; k < p.btiles; ++k) {
+        const float* from = p.b + (static_cast<int64_t>(k) * w.heads + head) * w.rows + row;
+        b += from[0];
+        b += from[static_cast<int64_t>(p.btiles) * w.heads * w.rows];
+      }
     }
     double pre = a, post = b;  // sums up to here, and from here on
 #pragma unroll
@@ -213,7 +222,8 @@ int64_t compute_units() {
   return n;
 }
 
-int chunk_of(const LinattnSizes& n) { return (n.K > n.V ? n.K : n.V) > 128 ? 32 : 64; }
+// Steps of a chunk: what the kernels' tiles hold.
+int chunk_of(const LinattnSizes& n) { return n.io == MAMBA_F32 && (n.K > n.V ? n.K : n.V) > 128 ? 32 : 64; }
 int64_t chunks_of(const LinattnSizes& n) { return (n.rows + chunk_of(n) - 1) / chunk_of(n); }
 
 // Chunks of a segment, when `walks` workgroups walk each sequence. One segment per
@@ -267,13 +277,13 @@ void give_segments(MixRole& r, const SegmentBytes& s, char*& at) {
 }
 
 hipError_t walk(const MixCall& w, int io, int chunk, hipStream_t stream) {
-  return io == MAMBA_BF16 ? launch_walk_bf16(w, chunk, stream) : launch_walk_f32(w, chunk, stream);
+  return io == MAMBA_BF16 ? launch_walk_bf16(w, stream) : launch_walk_f32(w, chunk, stream);
 }
 
 // The runs of w: with segments, first what each leaves, then what enters each.
 hipError_t run(MixCall w, const LinattnSizes& n, bool cut, hipStream_t stream) {
   const int chunk = chunk_of(n);
-  w.tiles = value_tiles(w.role[0].K, w.role[0].V);
+  w.tiles = value_tiles(n.io, w.role[0].K, w.role[0].V);
   if (cut) {
     hipError_t e = walk(w, n.io, chunk, stream);
     if (e != hipSuccess) return e;
@@ -295,7 +305,7 @@ hipError_t zero_rest(const RestRows& z, hipStream_t stream) {
 }
 
 // Workgroups of the backward's three runs for each sequence.
-int64_t bwd_walks(const LinattnSizes& n) { return n.heads * (value_tiles(n.K, n.V) + 2 * value_tiles(n.V, n.K)); }
+int64_t bwd_walks(const LinattnSizes& n) { return n.heads * (value_tiles(n.io, n.K, n.V) + 2 * value_tiles(n.io, n.V, n.K)); }
 
 // The backward's workspace.
 struct BwdBytes {
@@ -309,8 +319,8 @@ BwdBytes bwd_bytes(const LinattnSizes& n, bool head_decay) {
   s.seg = segment_bytes(n, per_of(n, bwd_walks(n)));
   s.mark_slots = slots_of(n.rows, n.batch, kMarkSteps);
   s.marks = r256(static_cast<size_t>(s.mark_slots) * n.heads * n.K * n.V * 4);
-  s.a = r256(static_cast<size_t>(value_tiles(n.K, n.V)) * n.heads * n.rows * 4);
-  s.b = r256(static_cast<size_t>(value_tiles(n.V, n.K)) * n.heads * n.rows * 4);
+  s.a = r256(static_cast<size_t>(2 * value_tiles(n.io, n.K, n.V)) * n.heads * n.rows * 4);
+  s.b = r256(static_cast<size_t>(2 * value_tiles(n.io, n.V, n.K)) * n.heads * n.rows * 4);
   s.last = r256(static_cast<size_t>(n.batch) * n.heads * n.K * n.V * 4);
   s.part = n.heads == n.groups ? 0 : r256(static_cast<size_t>(n.rows) * n.heads * n.K * 4);
   s.parts = head_decay ? r256(static_cast<size_t>(s.mark_slots) * n.heads * 4) : 0;
@@ -321,7 +331,7 @@ BwdBytes bwd_bytes(const LinattnSizes& n, bool head_decay) {
 
 size_t linattn_fwd_workspace_bytes(const LinattnSizes& n) {
   if (n.rows == 0 || n.heads == 0 || n.batch == 0) return 0;
-  return segment_bytes(n, per_of(n, n.heads * value_tiles(n.K, n.V))).total();
+  return segment_bytes(n, per_of(n, n.heads * value_tiles(n.io, n.K, n.V))).total();
 }
 
 size_t linattn_bwd_workspace_bytes(const LinattnSizes& n, bool head_decay) {
@@ -345,7 +355,7 @@ hipError_t launch_linattn_fwd(const LinattnProblem& p, void* workspace, hipStrea
   }
   if (n.batch == 0) return hipSuccess;
   MixCall w = call_of(p);
-  const int per = per_of(n, n.heads * value_tiles(n.K, n.V));
+  const int per = per_of(n, n.heads * value_tiles(n.io, n.K, n.V));
   set_segments(w, n, per);
   w.roles = 1;
   MixRole& r = w.role[0];
@@ -469,7 +479,6 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
       dq.se = f.sq;
       dq.marks = take(s.marks);
       dq.sums = take(s.b);
-      dq.pairs = true;
       if (p.dlast) dq.last = take(s.last);
       d.w = w;
       d.a = dv.sums;
@@ -480,8 +489,8 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
       d.dlast = p.dlast;
       d.dg = f.head_decay ? nullptr : p.dg;
       d.parts = f.head_decay ? take(s.parts) : nullptr;
-      d.atiles = value_tiles(K, V);
-      d.btiles = value_tiles(V, K);
+      d.atiles = value_tiles(n.io, K, V);
+      d.btiles = value_tiles(n.io, V, K);
       d.K = K;
       d.V = V;
     }
@@ -490,8 +499,8 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
       dk.part = take(s.part);
     }
     // roles of the same shape go in one launch: their operands are the same rows
-    const bool same = key_tiles(K) == key_tiles(V) && value_waves(K, V) == value_waves(V, K) &&
-                      value_tiles(K, V) == value_tiles(V, K);
+    const bool same = key_tiles(K) == key_tiles(V) && value_width(n.io, K, V) == value_width(n.io, V, K) &&
+                      value_tiles(n.io, K, V) == value_tiles(n.io, V, K);
     w.role[0] = dv;
     w.roles = 1;
     if (same) {

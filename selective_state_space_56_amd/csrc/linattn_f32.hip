@@ -22,6 +22,12 @@ __device__ __forceinline__ f32x16 mfma(float a, float b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
 }
 
+// Rows of D: see above.
+struct Layout {
+  static constexpr int kRows = 16, kLane = 4;
+  static constexpr int row(int tile, int i) { return 32 * tile + 8 * (i >> 2) + (i & 3); }
+};
+
 // KT: 32-row tiles of the state; NW: waves, 32 value channels each; CT: 32-step
 // tiles of a chunk.
 template <int KT, int NW, int CT>
@@ -30,7 +36,7 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
   constexpr int ldk = kK + 4, ldv = kV + 4, ldp = C + 4;
   __shared__ Decays<C> dec;
   __shared__ __align__(16) float s_q[C][ldk], s_k[C][ldk], s_v[C][ldv], s_e[C][ldv], s_p[C][ldp];
-  __shared__ float s_red[NW][C], s_row[CT][C], s_col[CT][C];
+  __shared__ float s_red[NW][C], s_row[CT][C];
   Walk at;
   if (!at.find(w, C)) return;
   const MixRole& r = w.role[at.role];
@@ -39,7 +45,7 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
   const int vw = r.V - at.tile * kV;            // value channels from this tile on
 
   f32x16 S[KT];
-  at.enter_state<KT>(w, r, S, col, hi);
+  at.enter_state<Layout>(w, r, S, col, hi);
 
   // rows of the chunk's tokens, 8 values at a time; 0 past its end and its channels
   auto stage = [&](float* to, int ld, int width, const void* from, int64_t stride, int64_t first_col, int have, int64_t c0,
@@ -65,7 +71,7 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
     const int n = at.len - c0 < C ? static_cast<int>(at.len - c0) : C;
     if (wv == 0) {
       const float g = lane < n ? w.g[(at.begin + at.token(lane, c0, n)) * w.g_step + at.head] : 0.0f;
-      chunk_decays<C>(dec, g, n, r.reverse, r.from, r.to);
+      chunk_decays<C>(dec, g, n, r.reverse, r.from, r.to, r.score);
     }
     if (!r.local) stage(&s_q[0][0], ldk, kK, r.q, r.sq, (at.head / r.qdiv) * r.K, r.K, c0, n);
     stage(&s_k[0][0], ldk, kK, r.k, r.sk, (at.head / r.kdiv) * r.K, r.K, c0, n);
@@ -73,7 +79,7 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
     if (r.sums) stage(&s_e[0][0], ldv, kV, r.e, r.se, static_cast<int64_t>(at.head / r.ediv) * r.V + at.tile * kV, vw, c0, n);
     __syncthreads();
     if (!r.local) {
-      at.leave_mark<KT>(w, r, S, c, C, col, hi);
+      at.leave_mark<Layout>(w, r, S, c, C, col, hi);
       // scores, transposed (earlier steps s as rows, steps t as columns), one 32 x 32
       // tile per wave at a time
       int turn = 0;
@@ -100,7 +106,7 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<f32x4*>(&s_p[t][32 * si + 8 * i + 4 * hi]) =
                 f32x4{p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]};
-          if (r.sums && r.pairs) {
+          if (r.sums) {
             f32x16 u = {};
 #pragma unroll 4
             for (int x = 0; x < kV; x += 8) {
@@ -115,8 +121,6 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
               const int s = 32 * si + 8 * (i >> 2) + 4 * hi + (i & 3);
               u[i] = where((s < t) & (s >= from), u[i] * p[i]);
               sum += u[i];
-              const float all = over_32(u[i]);
-              if (lo == 0) s_col[ti][s] = all;
             }
             sum += __shfl_xor(sum, 32);
             if (hi == 0) s_row[si][t] = sum;
@@ -168,19 +172,18 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
             }
           }
         }
-        at.store<F32Io>(w, r, acc, 32 * ti, c0, n, col, hi);
+        at.store<F32Io, Layout>(w, r, acc, 32 * ti, c0, n, col, hi);
       }
       if (r.sums) {
         __syncthreads();
         if (tid < n) {
-          float sum = 0.0f;
+          float sum = 0.0f, both = 0.0f;
 #pragma unroll
           for (int i = 0; i < NW; ++i) sum += s_red[i][tid];
-          if (r.pairs) {
-            for (int i = 0; i <= tid / 32; ++i) sum += s_row[i][tid];
-            for (int i = tid / 32; i < CT; ++i) sum -= s_col[i][tid];
-          }
-          r.sums[(static_cast<int64_t>(at.tile) * w.heads + at.head) * w.rows + at.begin + at.token(tid, c0, n)] = sum;
+          for (int i = 0; i <= tid / 32; ++i) both += s_row[i][tid];
+          float* to = r.sums + (static_cast<int64_t>(at.tile) * w.heads + at.head) * w.rows + at.begin + at.token(tid, c0, n);
+          to[0] = sum;
+          to[static_cast<int64_t>(w.tiles) * w.heads * w.rows] = both;
         }
       }
     }
@@ -203,7 +206,7 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
     gone.add(dec.cut, dec.total);
     __syncthreads();  // the next chunk's rows take these places
   }
-  at.leave_state<KT>(w, r, S, gone, col, hi);
+  at.leave_state<Layout>(w, r, S, gone, col, hi);
 }
 
 template <int KT, int NW, int CT>
@@ -216,7 +219,7 @@ hipError_t launch(const MixCall& w, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_walk_f32(const MixCall& w, int chunk, hipStream_t stream) {
-  const int kt = key_tiles(w.role[0].K), nw = value_waves(w.role[0].K, w.role[0].V);
+  const int kt = key_tiles(w.role[0].K), nw = value_width(MAMBA_F32, w.role[0].K, w.role[0].V) / 32;
   if (kt == 8) return launch<8, 2, 1>(w, stream);
   if (chunk == 32) {
     if (kt == 2) return nw == 2 ? launch<2, 2, 1>(w, stream) : launch<2, 4, 1>(w, stream);

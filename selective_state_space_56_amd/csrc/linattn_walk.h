@@ -6,13 +6,16 @@
 
 namespace mscan {
 
-// 32-row tiles of a workgroup's state, and its waves of 32 value channels each. (With 8
-// tiles, 128 registers of state, the float32 kernel has registers for two waves only; the
-// bfloat16 one shares the rows among two pairs of waves.)
+// 32-row tiles of a workgroup's state, and its value channels, 32 for each of two or
+// four waves. (With 8 tiles, 128 registers of state, the float32 kernel has registers for
+// two waves only, and the bfloat16 one for a quarter of a chunk's rows in flight.)
 inline int key_tiles(int64_t K) { return K <= 64 ? 2 : K <= 128 ? 4 : 8; }
-inline int value_waves(int64_t K, int64_t V) { return V <= 64 || key_tiles(K) == 8 ? 2 : 4; }
-inline int value_tiles(int64_t K, int64_t V) {
-  const int width = 32 * value_waves(K, V);
+inline int value_width(int io, int64_t K, int64_t V) {
+  if (key_tiles(K) == 8) return io == MAMBA_F32 ? 64 : 128;
+  return V <= 64 ? 64 : 128;
+}
+inline int value_tiles(int io, int64_t K, int64_t V) {
+  const int width = value_width(io, K, V);
   return static_cast<int>((V + width - 1) / width);
 }
 inline int64_t walk_units(const MixCall& w) { return w.slots * w.heads * w.tiles * w.roles; }
@@ -88,63 +91,48 @@ struct Walk {
     return c0 + (reverse ? n - 1 - row : row);
   }
 
-  // Register i of tile kt holds S[32 kt + 8 (i / 4) + 4 hi + i % 4][col], or with EIGHT
-  // S[32 kt + 16 (i / 8) + 8 hi + i % 8][col].
-  template <bool EIGHT = false>
-  static __device__ __forceinline__ int row_of(int kt, int i, int hi) {
-    return EIGHT ? 32 * kt + 16 * (i >> 3) + 8 * hi + (i & 7) : 32 * kt + 8 * (i >> 2) + 4 * hi + (i & 3);
-  }
-
-  // The part of row_of that lanes do not differ in, and the lane's own.
-  template <bool EIGHT>
-  static constexpr int row_base(int kt, int i) { return EIGHT ? row_eight(kt, i) : 32 * kt + 8 * (i >> 2) + (i & 3); }
-  static constexpr int row_eight(int kt, int i) { return 32 * kt + 16 * (i >> 3) + (i & 7); }
-
-  // States are reached through a buffer resource, so that a register's address is a
-  // scalar beside the lane's own; what lies past the state is out of its range.
-  template <int KT, bool EIGHT = false, class Tile>
-  __device__ __forceinline__ void write(const MixRole& r, float* to, const Tile (&S)[KT], int col, int hi,
-                                        int row0 = 0) const {
+  // States are held as N tiles whose register i holds row L::row(tile, i) + L::kLane x
+  // part of the state, part being the lane's group; the lane's column is col. They are
+  // reached through a buffer resource, so that a register's address is a scalar beside
+  // the lane's own; what lies past the state is out of its range.
+  template <class L, class Tile, int N>
+  __device__ __forceinline__ void write(const MixRole& r, float* to, const Tile (&S)[N], int col, int part) const {
     const auto rs = make_rsrc(to, static_cast<uint32_t>(r.K * r.V * 4));
-    const int first = row0 + (EIGHT ? 8 : 4) * hi;  // the lane's first row
+    const int first = L::kLane * part;  // the lane's first row
     const uint32_t lane = col < r.V ? static_cast<uint32_t>((first * r.V + col) * 4) : kOffNone;
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
+    for (int k = 0; k < N; ++k) {
       int row_step = r.V * 4;
       asm volatile("" : "+s"(row_step));  // formed here, not kept for every register from the kernel's start on
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int base = row_base<EIGHT>(kt, i);
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[kt][i]), rs, first + base < r.K ? lane : kOffNone,
-                                              base * row_step, 0);
-      }
+      for (int i = 0; i < L::kRows; ++i)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[k][i]), rs, first + L::row(k, i) < r.K ? lane : kOffNone,
+                                              L::row(k, i) * row_step, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 
-  template <int KT, bool EIGHT = false, class Tile>
-  __device__ __forceinline__ void enter_state(const MixCall& w, const MixRole& r, Tile (&S)[KT], int col, int hi,
-                                              int row0 = 0) const {
+  template <class L, class Tile, int N>
+  __device__ __forceinline__ void enter_state(const MixCall& w, const MixRole& r, Tile (&S)[N], int col, int part) const {
     const float* from = r.local ? nullptr : entry ? r.s0 : r.enter;
     if (!from) {
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) S[kt] = Tile{};
+      for (int k = 0; k < N; ++k) S[k] = Tile{};
       return;
     }
     from += ((entry ? static_cast<int64_t>(seq) : slot) * w.heads + head) * r.K * r.V;
     const auto rs = make_rsrc(from, static_cast<uint32_t>(r.K * r.V * 4));
     const bool turned = entry && r.s0_turned;
-    const int first = row0 + (EIGHT ? 8 : 4) * hi;
+    const int first = L::kLane * part;
     const uint32_t lane = static_cast<uint32_t>((turned ? col * r.K + first : first * r.V + col) * 4);
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
+    for (int k = 0; k < N; ++k) {
       int row_step = turned ? 4 : r.V * 4;
       asm volatile("" : "+s"(row_step));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int base = row_base<EIGHT>(kt, i);
-        const uint32_t at = col < r.V && first + base < r.K ? lane : kOffNone;
-        S[kt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, base * row_step, 0));
+      for (int i = 0; i < L::kRows; ++i) {
+        const uint32_t at = col < r.V && first + L::row(k, i) < r.K ? lane : kOffNone;
+        S[k][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, L::row(k, i) * row_step, 0));
       }
       __builtin_amdgcn_sched_barrier(0);  // (a tile's addresses at a time)
     }
@@ -152,47 +140,49 @@ struct Walk {
 
   // The state between chunks, for the gradients of the decays: with time running
   // forward what enters chunk c, in reverse what enters it from behind.
-  template <int KT, bool EIGHT = false, class Tile>
-  __device__ __forceinline__ void leave_mark(const MixCall& w, const MixRole& r, const Tile (&S)[KT], int c, int C, int col,
-                                             int hi, int row0 = 0) const {
+  template <class L, class Tile, int N>
+  __device__ __forceinline__ void leave_mark(const MixCall& w, const MixRole& r, const Tile (&S)[N], int c, int C, int col,
+                                             int part) const {
     const int between = reverse ? c + 1 : c, mark = kMarkSteps / C;
     if (!r.marks || between == 0 || between >= chunks || between % mark) return;
     const int64_t at = first_slot(begin, seq, kMarkSteps) + between / mark;
-    write<KT, EIGHT>(r, r.marks + (at * w.heads + head) * r.K * r.V, S, col, hi, row0);
+    write<L>(r, r.marks + (at * w.heads + head) * r.K * r.V, S, col, part);
   }
 
-  template <int KT, bool EIGHT = false, class Tile>
-  __device__ __forceinline__ void leave_state(const MixCall& w, const MixRole& r, const Tile (&S)[KT], const Gone& gone,
-                                              int col, int hi, int row0 = 0) const {
+  template <class L, class Tile, int N>
+  __device__ __forceinline__ void leave_state(const MixCall& w, const MixRole& r, const Tile (&S)[N], const Gone& gone,
+                                              int col, int part) const {
     const int64_t size = static_cast<int64_t>(r.K) * r.V;
     if (r.local) {
-      write<KT, EIGHT>(r, r.local + (slot * w.heads + head) * size, S, col, hi, row0);
+      write<L>(r, r.local + (slot * w.heads + head) * size, S, col, part);
       if (threadIdx.x == 0 && tile == 0) r.gone[slot * w.heads + head] = gone.cut ? 0.0f : exp_of(gone.sum);
     } else if (r.last && exit) {
-      write<KT, EIGHT>(r, r.last + (static_cast<int64_t>(seq) * w.heads + head) * size, S, col, hi, row0);
+      write<L>(r, r.last + (static_cast<int64_t>(seq) * w.heads + head) * size, S, col, part);
     }
   }
 
-  // Outputs of the chunk's rows t0 + (as row_of), as far as there are tokens.
-  template <class IO, class Tile>
+  // Outputs as D's registers: rows t0 + L::row(0, i) + L::kLane x part of the chunk, as
+  // far as there are tokens.
+  template <class IO, class L, class Tile>
   __device__ __forceinline__ void store(const MixCall& w, const MixRole& r, const Tile& o, int t0, int64_t c0, int n,
-                                        int col, int hi) const {
+                                        int col, int part) const {
     using raw = typename IO::raw;
+    const int first = t0 + L::kLane * part;
     const int64_t stride = r.part ? static_cast<int64_t>(w.heads) * r.V : r.so, step = reverse ? -stride : stride;
-    const int64_t at = (begin + token(0, c0, n)) * stride + static_cast<int64_t>(head) * r.V + col + (t0 + 4 * hi) * step;
+    const int64_t at = (begin + token(0, c0, n)) * stride + static_cast<int64_t>(head) * r.V + col + first * step;
     if (col >= r.V) return;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (t0 + row_of(0, i, hi) >= n) continue;
+    for (int i = 0; i < L::kRows; ++i) {
+      if (first + L::row(0, i) >= n) continue;
       if (r.part)
-        r.part[at + row_base<false>(0, i) * step] = o[i];
+        r.part[at + L::row(0, i) * step] = o[i];
       else
-        static_cast<raw*>(r.o)[at + row_base<false>(0, i) * step] = IO::from_f32(o[i]);
+        static_cast<raw*>(r.o)[at + L::row(0, i) * step] = IO::from_f32(o[i]);
     }
   }
 };
 
 hipError_t launch_walk_f32(const MixCall& w, int chunk, hipStream_t stream);
-hipError_t launch_walk_bf16(const MixCall& w, int chunk, hipStream_t stream);
+hipError_t launch_walk_bf16(const MixCall& w, hipStream_t stream);
 
 }  // namespace mscan
