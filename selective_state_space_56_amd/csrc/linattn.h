@@ -55,6 +55,7 @@ struct MixCall {
   int64_t slots;           // segments at most, over all sequences
   int batch, heads, roles, tiles;
   int per;                 // chunks of a segment
+  uint32_t together;       // consecutive workgroups that read the same rows
 };
 
 // Steps between two marks: where the gradients of the decays start anew.

@@ -284,6 +284,7 @@ hipError_t walk(const MixCall& w, int io, int chunk, hipStream_t stream) {
 hipError_t run(MixCall w, const LinattnSizes& n, bool cut, hipStream_t stream) {
   const int chunk = chunk_of(n);
   w.tiles = value_tiles(n.io, w.role[0].K, w.role[0].V);
+  w.together = static_cast<uint32_t>(n.heads / n.groups * w.tiles * w.roles);
   if (cut) {
     hipError_t e = walk(w, n.io, chunk, stream);
     if (e != hipSuccess) return e;

@@ -47,6 +47,11 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// The leading 16 bits of two values, a's in the low half.
+__device__ __forceinline__ uint32_t leading(float a, float b) {
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
+}
+
 // Two values as N bf16 parts each, in words as pack: with two, hi = bf16(v) and lo =
 // bf16(v - hi); with three, the value's bits eight at a time, whose sum is the value.
 template <int N>
@@ -55,11 +60,11 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&part)[N]) {
     part[0] = pack(a, b);
     part[1] = pack(a - low(part[0]), b - high(part[0]));
   } else {
-    part[0] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
+    part[0] = leading(a, b);
     a -= low(part[0]);
     b -= high(part[0]);
-    part[1] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302);
-    part[2] = __builtin_amdgcn_perm(__float_as_uint(b - high(part[1])), __float_as_uint(a - low(part[1])), 0x07060302);
+    part[1] = leading(a, b);
+    part[2] = leading(a - low(part[1]), b - high(part[1]));
   }
 }
 
@@ -142,6 +147,14 @@ struct Rows {
 __device__ __forceinline__ int fresh(int v) {
   asm volatile("" : "+v"(v));
   return v;
+}
+
+// v's values where the mask's bits are set, else 0, whatever they are. (As bits: chosen by
+// a condition, or as a constant, they would be moved to other registers on all paths.)
+__device__ __forceinline__ void drop(f32x16& v, uint32_t mask) {
+  asm volatile("" : "+v"(mask));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(__float_as_uint(v[i]) & mask);
 }
 
 // Rows of the state's tiles.
@@ -329,10 +342,7 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
         for (int t = 0; t < kTT; ++t) {
           const float f = dec.in[32 * t + lo];
           acc[t] *= f;
-          if (cut) {  // what a cut drops may be anything
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[t][i] = where(f != 0.0f, acc[t][i]);
-          }
+          if (cut) drop(acc[t], f != 0.0f ? 0xffffffffu : 0u);  // what a cut drops may be anything
         }
       }
       __syncthreads();
@@ -391,40 +401,44 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
       // A score of 0 times a value that is not finite is NaN: with such a value among this
       // wave's, steps are added one by one, to the outputs that see them only (whose score
       // is not -0).
+      u32x4 values[C / 16];
       u16x2 most = {};
 #pragma unroll
       for (int j = 0; j < C / 16; ++j) {
-        const u32x4 a = column8<false>(&s_v[16 * j][32 * wv], ldv, lane);
+        values[j] = column8<false>(&s_v[16 * j][32 * wv], ldv, lane);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, a[e] & 0x7fff7fffu));
+          most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, values[j][e] & 0x7fff7fffu));
       }
-      if (!__any((most[0] >= 0x7f80) | (most[1] >= 0x7f80))) {
-#pragma unroll
-        for (int j = 0; j < C / 16; ++j) {
-          const u32x4 a = column8<false>(&s_v[16 * j][32 * wv], ldv, lane);
-#pragma unroll
-          for (int t = j / 2; t < kTT; ++t) {
-            acc[t] = mfma(a, row8(&s_p[0][32 * t + lo][16 * j + 8 * hi]), acc[t]);
-            acc[t] = mfma(a, row8(&s_p[1][32 * t + lo][16 * j + 8 * hi]), acc[t]);
-          }
-        }
-      } else {
+      if (__any((most[0] >= 0x7f80) | (most[1] >= 0x7f80))) {
 #pragma unroll 1
         for (int s = 0; s < n; ++s) {
 #pragma unroll
           for (int t = 0; t < kTT; ++t) {
             const uint16_t score = s_p[0][32 * t + lo][s];
             const float f = Bf16Io::to_f32(score) + Bf16Io::to_f32(s_p[1][32 * t + lo][s]);
-            const bool sees = (score != 0x8000) & (s < 32 * (t + 1));
+            if ((score != 0x8000) & (s < 32 * (t + 1))) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float more = fmaf(f, Bf16Io::to_f32(s_v[s][32 * wv + 8 * (i >> 2) + 4 * hi + (i & 3)]), acc[t][i]);
-              acc[t][i] = sees ? more : acc[t][i];
+              for (int i = 0; i < 16; ++i)
+                acc[t][i] = fmaf(f, Bf16Io::to_f32(s_v[s][32 * wv + 8 * (i >> 2) + 4 * hi + (i & 3)]), acc[t][i]);
             }
           }
         }
+        // nothing is left for the products below (one path for both: see drop)
+#pragma unroll
+        for (int j = 0; j < C / 16; ++j) {
+          uint32_t none = 0;
+          asm volatile("" : "+v"(none));
+          values[j] &= none;
+        }
       }
+#pragma unroll
+      for (int j = 0; j < C / 16; ++j)
+#pragma unroll
+        for (int t = j / 2; t < kTT; ++t) {
+          acc[t] = mfma(values[j], row8(&s_p[0][32 * t + lo][16 * j + 8 * hi]), acc[t]);
+          acc[t] = mfma(values[j], row8(&s_p[1][32 * t + lo][16 * j + 8 * hi]), acc[t]);
+        }
       if (r.part) {
         // shared operands' gradients: a float32 row for each head
         const int first = at.tile * kV + 32 * wv + 4 * hi;
@@ -459,16 +473,13 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
         if (dec.end[s] == 0.0f) *reinterpret_cast<uint32_t*>(&s_v[s][2 * (id % (kV / 2))]) = 0;
       }
       __syncthreads();
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) drop(S[kt], 0);
     }
     const int lane = fresh(threadIdx.x & 63), hi = lane >> 5;
-    const float all = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(dec.all)));
-    if (all != 0.0f) {
+    const float all = dec.all;
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) S[kt] *= all;
-    } else {
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) S[kt] = f32x16{};
-    }
+    for (int kt = 0; kt < KT; ++kt) S[kt] *= all;
 #pragma unroll
     for (int j = 0; j < C / 16; ++j) {
       const u32x4 b = column8<false>(&s_v[16 * j][32 * wv], ldv, lane);

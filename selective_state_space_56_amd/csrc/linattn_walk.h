@@ -59,6 +59,10 @@ struct Walk {
   // False for a workgroup that has nothing to do.
   __device__ __forceinline__ bool find(const MixCall& w, int C) {
     uint32_t u = blockIdx.x;
+    // Consecutive workgroups go to the eight dies in turn; those that read the same rows
+    // (a head's runs and value tiles, heads that share their keys) are kept on one.
+    const uint32_t run = w.together, whole = gridDim.x / (8 * run) * (8 * run);
+    if (u < whole) u = (u / (8 * run) * 8 + u % 8) * run + u / 8 % run;
     role = u % w.roles;
     u /= w.roles;
     tile = u % w.tiles;
