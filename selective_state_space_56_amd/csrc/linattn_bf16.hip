@@ -168,14 +168,19 @@ constexpr int kTiles = kTT * (kTT + 1) / 2;    // of scores: (0, 0), (1, 0), (1,
 
 // Waves per SIMD that the kernels' registers are held to: two workgroups of four waves,
 // where they fit.
-constexpr int least_waves(int KT, int NW) { return NW == 4 && KT < 8 ? 2 : 1; }
+constexpr int least_waves(int KT, int KH) { return KT * KH < 8 ? 2 : 1; }
 
-// KT: 32-row tiles of the state; NW: waves, 32 value channels each; SUMS: with the sums
-// for the decays' gradients.
-template <int KT, int NW, bool SUMS>
-__global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel(MixCall w) {
-  constexpr int C = kC, kK = 32 * KT, kV = 32 * NW, kThreads = 64 * NW;
-  constexpr int kW = kK > kV ? kK : kV;  // widest rows that the queries' tile holds
+// Four waves: NV of them side by side, 32 value channels each, and KH that share the
+// state's rows, KT 32-row tiles each. (Up to 64 channels two waves would do, but leave half
+// of a compute unit's registers and issue slots empty: with KH = 2 each makes half of the
+// state's products and of the outputs what its rows give, and they add one tile of
+// steps for each other.) SUMS: with the sums for the decays' gradients.
+template <int KT, int KH, int NV, bool SUMS>
+__global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_kernel(MixCall w) {
+  constexpr int NW = NV * KH, C = kC, kK = 32 * KT * KH, kV = 32 * NV, kThreads = 64 * NW;
+  static_assert(KH == 1 || KH == kTT, "a tile of steps for each wave that shares rows");
+  // the widest rows that the queries' tile holds (with KH a tile of outputs for each wave)
+  constexpr int kW = KH > 1 && kK < 128 ? 128 : kK > kV ? kK : kV;
   // row strides of the tiles: rows read along, 16 bytes per lane, start 4 banks apart;
   // rows read by the transposing load 16 (values) or 20 (keys, which are read both
   // ways) banks apart
@@ -187,19 +192,20 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
   __shared__ __align__(16) uint16_t s_q[C][ldq], s_k[C][ldk], s_v[C][ldv], s_p[2][C][ldp];
   // the waves' sums for the decays' gradients lie in the padding of the queries' and the
   // scores' rows (with room of their own only one workgroup would fit a compute unit)
-  static_assert(4 * NW <= 2 * (ldq - kW) && 4 * kTT <= 2 * (ldp - C), "a float for each wave, and for each tile");
+  static_assert(4 * NV <= 2 * (ldq - kW) && 4 * kTT <= 2 * (ldp - C), "a float for each wave, and for each tile");
   auto s_red = [&](int t) { return reinterpret_cast<float*>(&s_q[t][kW]); };
   auto s_row = [&](int t) { return reinterpret_cast<float*>(&s_p[0][t][C]); };
   Walk at;
   if (!at.find(w, C)) return;
   const MixRole& r = w.role[at.role];
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = at.tile * kV + 32 * wv + (threadIdx.x & 31);  // this lane's value channel
+  const int vv = wv % NV, kh = wv / NV, k0 = 32 * KT * kh;      // this wave's channels and rows of the state
+  const int col = at.tile * kV + 32 * vv + (threadIdx.x & 31);  // this lane's value channel
   const int vw = r.V - at.tile * kV;
   const bool outputs = r.local == nullptr, sums = SUMS && r.sums;
 
   f32x16 S[KT];
-  at.enter_state<StateRows>(w, r, S, col, threadIdx.x % 64 / 32);
+  at.enter_state<StateRows>(w, r, S, col, threadIdx.x % 64 / 32, k0);
 
   const RowsK rq(r.q, at.begin, r.sq, static_cast<int64_t>(at.head / r.qdiv) * r.K, r.K, at.reverse);
   const RowsK rk(r.k, at.begin, r.sk, static_cast<int64_t>(at.head / r.kdiv) * r.K, r.K, at.reverse);
@@ -271,7 +277,7 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
       f32x16 p[kEach];
       {
         const int lane = fresh(threadIdx.x & 63), lo = lane & 31, hi = lane >> 5;
-        if (sums) at.leave_mark<StateRows>(w, r, S, c, C, col, hi);
+        if (sums) at.leave_mark<StateRows>(w, r, S, c, C, col, hi, k0);
         const bool flat = __builtin_amdgcn_readfirstlane(dec.flat);
 #pragma unroll
         for (int m = 0; m < kEach; ++m) {
@@ -332,7 +338,7 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
             }
 #pragma unroll
             for (int t = 0; t < kTT; ++t) {
-              const u32x4 b = row8(&s_q[32 * t + lo][32 * kt + 16 * j + 8 * hi]);
+              const u32x4 b = row8(&s_q[32 * t + lo][k0 + 32 * kt + 16 * j + 8 * hi]);
 #pragma unroll
               for (int m = 0; m < kParts; ++m) acc[t] = mfma(part[m], b, acc[t]);
             }
@@ -346,6 +352,30 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
         }
       }
       __syncthreads();
+      if constexpr (KH > 1) {
+        // each tile of steps is finished by one of the waves, in the queries' place
+        const int lane = fresh(threadIdx.x & 63);
+        f32x4* half = reinterpret_cast<f32x4*>(&s_q[0][0]) + lane;
+        static_assert(sizeof(s_q) >= NW * 64 * 16 * sizeof(float), "a tile for each wave");
+        const f32x16 give = acc[1 - kh];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          half[(4 * wv + i) * 64] = f32x4{give[4 * i], give[4 * i + 1], give[4 * i + 2], give[4 * i + 3]};
+        __syncthreads();
+        const int other = wv ^ NV;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 take = half[(4 * other + i) * 64];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[0][4 * i + e] = (kh ? acc[1][4 * i + e] : acc[0][4 * i + e]) + take[e];
+          }
+        }
+        __syncthreads();
+      }
+      // from here on acc[t] is tile first + t
+      constexpr int kOwn = KH > 1 ? 1 : kTT;
+      const int first = KH > 1 ? kh : 0;
       if (SUMS && !sums && next != at.stop) fetch_q(next);
       if (sums) {
         const int tid = fresh(threadIdx.x), lane = tid & 63, lo = lane & 31, hi = lane >> 5;
@@ -373,24 +403,25 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
         }
         // and what the state that enters gives, with the same rows
 #pragma unroll
-        for (int t = 0; t < kTT; ++t) {
+        for (int t = 0; t < kOwn; ++t) {
+          const int row = 32 * (first + t) + lo;
           float sum = 0.0f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const u32x2 e = *reinterpret_cast<const u32x2*>(&s_q[32 * t + lo][32 * wv + 8 * i + 4 * hi]);
+            const u32x2 e = *reinterpret_cast<const u32x2*>(&s_q[row][32 * vv + 8 * i + 4 * hi]);
             sum = fmaf(acc[t][4 * i], low(e[0]), sum);
             sum = fmaf(acc[t][4 * i + 1], high(e[0]), sum);
             sum = fmaf(acc[t][4 * i + 2], low(e[1]), sum);
             sum = fmaf(acc[t][4 * i + 3], high(e[1]), sum);
           }
           sum = over_halves(sum);
-          if (hi == 0) s_red(32 * t + lo)[wv] = sum;
+          if (hi == 0) s_red(row)[vv] = sum;
         }
         __syncthreads();  // the outputs take the rows' place
         if (tid < n) {
           float sum = 0.0f, both = 0.0f;
 #pragma unroll
-          for (int i = 0; i < NW; ++i) sum += s_red(tid)[i];
+          for (int i = 0; i < NV; ++i) sum += s_red(tid)[i];
           for (int i = 0; i <= tid / 32; ++i) both += s_row(tid)[i];
           float* to = r.sums + (static_cast<int64_t>(at.tile) * w.heads + at.head) * w.rows + at.begin + at.token(tid, c0, n);
           to[0] = sum;
@@ -405,7 +436,7 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
       u16x2 most = {};
 #pragma unroll
       for (int j = 0; j < C / 16; ++j) {
-        values[j] = column8<false>(&s_v[16 * j][32 * wv], ldv, lane);
+        values[j] = column8<false>(&s_v[16 * j][32 * vv], ldv, lane);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, values[j][e] & 0x7fff7fffu));
@@ -414,13 +445,14 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
 #pragma unroll 1
         for (int s = 0; s < n; ++s) {
 #pragma unroll
-          for (int t = 0; t < kTT; ++t) {
-            const uint16_t score = s_p[0][32 * t + lo][s];
-            const float f = Bf16Io::to_f32(score) + Bf16Io::to_f32(s_p[1][32 * t + lo][s]);
-            if ((score != 0x8000) & (s < 32 * (t + 1))) {
+          for (int t = 0; t < kOwn; ++t) {
+            const int row = 32 * (first + t) + lo;
+            const uint16_t score = s_p[0][row][s];
+            const float f = Bf16Io::to_f32(score) + Bf16Io::to_f32(s_p[1][row][s]);
+            if ((score != 0x8000) & (s < 32 * (first + t + 1))) {
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                acc[t][i] = fmaf(f, Bf16Io::to_f32(s_v[s][32 * wv + 8 * (i >> 2) + 4 * hi + (i & 3)]), acc[t][i]);
+                acc[t][i] = fmaf(f, Bf16Io::to_f32(s_v[s][32 * vv + 8 * (i >> 2) + 4 * hi + (i & 3)]), acc[t][i]);
             }
           }
         }
@@ -433,30 +465,33 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
         }
       }
 #pragma unroll
-      for (int j = 0; j < C / 16; ++j)
+      for (int j = 0; j < C / 16; ++j) {
+        if (KH > 1 && j / 2 > first) break;
 #pragma unroll
-        for (int t = j / 2; t < kTT; ++t) {
-          acc[t] = mfma(values[j], row8(&s_p[0][32 * t + lo][16 * j + 8 * hi]), acc[t]);
-          acc[t] = mfma(values[j], row8(&s_p[1][32 * t + lo][16 * j + 8 * hi]), acc[t]);
+        for (int t = KH > 1 ? 0 : j / 2; t < kOwn; ++t) {
+          const int row = 32 * (first + t) + lo;
+          acc[t] = mfma(values[j], row8(&s_p[0][row][16 * j + 8 * hi]), acc[t]);
+          acc[t] = mfma(values[j], row8(&s_p[1][row][16 * j + 8 * hi]), acc[t]);
         }
+      }
       if (r.part) {
         // shared operands' gradients: a float32 row for each head
-        const int first = at.tile * kV + 32 * wv + 4 * hi;
-        float* to = r.part + (at.begin + at.token(0, c0, n)) * w.heads * r.V + static_cast<int64_t>(at.head) * r.V + first;
+        const int channel = at.tile * kV + 32 * vv + 4 * hi;
+        float* to = r.part + (at.begin + at.token(0, c0, n)) * w.heads * r.V + static_cast<int64_t>(at.head) * r.V + channel;
         const int64_t step = static_cast<int64_t>(at.reverse ? -w.heads : w.heads) * r.V;
 #pragma unroll
-        for (int t = 0; t < kTT; ++t)
+        for (int t = 0; t < kOwn; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (32 * t + lo < n && first + 8 * i < r.V)
-              *reinterpret_cast<Words<float, 4, 4>*>(to + (32 * t + lo) * step + 8 * i) =
+            if (32 * (first + t) + lo < n && channel + 8 * i < r.V)
+              *reinterpret_cast<Words<float, 4, 4>*>(to + (32 * (first + t) + lo) * step + 8 * i) =
                   Words<float, 4, 4>{acc[t][4 * i], acc[t][4 * i + 1], acc[t][4 * i + 2], acc[t][4 * i + 3]};
       } else {
 #pragma unroll
-        for (int t = 0; t < kTT; ++t)
+        for (int t = 0; t < kOwn; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<u32x2*>(&s_q[32 * t + lo][32 * wv + 8 * i + 4 * hi]) =
+            *reinterpret_cast<u32x2*>(&s_q[32 * (first + t) + lo][32 * vv + 8 * i + 4 * hi]) =
                 u32x2{pack(acc[t][4 * i], acc[t][4 * i + 1]), pack(acc[t][4 * i + 2], acc[t][4 * i + 3])};
       }
     }
@@ -482,7 +517,7 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
     for (int kt = 0; kt < KT; ++kt) S[kt] *= all;
 #pragma unroll
     for (int j = 0; j < C / 16; ++j) {
-      const u32x4 b = column8<false>(&s_v[16 * j][32 * wv], ldv, lane);
+      const u32x4 b = column8<false>(&s_v[16 * j][32 * vv], ldv, lane);
       const f32x4 f0 = *reinterpret_cast<const f32x4*>(&dec.end[16 * j + 8 * hi]);
       const f32x4 f1 = *reinterpret_cast<const f32x4*>(&dec.end[16 * j + 8 * hi + 4]);
       u32x4 part[3];
@@ -496,7 +531,7 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
       }
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        const u32x4 a = column8<true>(&s_k[16 * j][32 * kt], ldk, lane);
+        const u32x4 a = column8<true>(&s_k[16 * j][k0 + 32 * kt], ldk, lane);
 #pragma unroll
         for (int m = 0; m < 3; ++m) S[kt] = mfma(a, part[m], S[kt]);
       }
@@ -505,26 +540,25 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW)) void walk_bf16_kernel
     __syncthreads();  // the next chunk's rows take these places
   }
   if (at.first != at.stop) flush(at.stop - at.step);
-  at.leave_state<StateRows>(w, r, S, gone, col, threadIdx.x % 64 / 32);
+  at.leave_state<StateRows>(w, r, S, gone, col, threadIdx.x % 64 / 32, k0);
 }
 
-template <int KT, int NW>
+template <int KT, int KH, int NV>
 hipError_t launch(const MixCall& w, hipStream_t stream) {
   bool sums = false;
   for (int k = 0; k < w.roles; ++k) sums |= w.role[k].sums != nullptr && !w.role[k].local;
   const dim3 grid(static_cast<unsigned>(walk_units(w)));
   if (sums)
-    hipLaunchKernelGGL((walk_bf16_kernel<KT, NW, true>), grid, dim3(64 * NW), 0, stream, w);
+    hipLaunchKernelGGL((walk_bf16_kernel<KT, KH, NV, true>), grid, dim3(64 * NV * KH), 0, stream, w);
   else
-    hipLaunchKernelGGL((walk_bf16_kernel<KT, NW, false>), grid, dim3(64 * NW), 0, stream, w);
+    hipLaunchKernelGGL((walk_bf16_kernel<KT, KH, NV, false>), grid, dim3(64 * NV * KH), 0, stream, w);
   return hipGetLastError();
 }
 
 template <int KT>
 hipError_t by_values(const MixCall& w, hipStream_t stream) {
-  if constexpr (KT < 8)
-    if (value_width(MAMBA_BF16, w.role[0].K, w.role[0].V) == 64) return launch<KT, 2>(w, stream);
-  return launch<KT, 4>(w, stream);
+  return value_width(MAMBA_BF16, w.role[0].K, w.role[0].V) == 64 ? launch<KT / 2, 2, 2>(w, stream)
+                                                                 : launch<KT, 1, 4>(w, stream);
 }
 
 #ifdef ONLY

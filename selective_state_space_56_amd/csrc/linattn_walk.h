@@ -6,14 +6,10 @@
 
 namespace mscan {
 
-// 32-row tiles of a workgroup's state, and its value channels, 32 for each of two or
-// four waves. (With 8 tiles, 128 registers of state, the float32 kernel has registers for
-// two waves only, and the bfloat16 one for a quarter of a chunk's rows in flight.)
+// 32-row tiles of a workgroup's state, and its value channels. (With 8 tiles, 128
+// registers of state, the float32 kernel has registers for two waves only.)
 inline int key_tiles(int64_t K) { return K <= 64 ? 2 : K <= 128 ? 4 : 8; }
-inline int value_width(int io, int64_t K, int64_t V) {
-  if (key_tiles(K) == 8) return io == MAMBA_F32 ? 64 : 128;
-  return V <= 64 ? 64 : 128;
-}
+inline int value_width(int io, int64_t K, int64_t V) { return V <= 64 || (io == MAMBA_F32 && key_tiles(K) == 8) ? 64 : 128; }
 inline int value_tiles(int io, int64_t K, int64_t V) {
   const int width = value_width(io, K, V);
   return static_cast<int>((V + width - 1) / width);
@@ -96,13 +92,14 @@ struct Walk {
   }
 
   // States are held as N tiles whose register i holds row L::row(tile, i) + L::kLane x
-  // part of the state, part being the lane's group; the lane's column is col. They are
+  // part of the state (and row0 rows on), part being the lane's group; the lane's column is col. They are
   // reached through a buffer resource, so that a register's address is a scalar beside
   // the lane's own; what lies past the state is out of its range.
   template <class L, class Tile, int N>
-  __device__ __forceinline__ void write(const MixRole& r, float* to, const Tile (&S)[N], int col, int part) const {
+  __device__ __forceinline__ void write(const MixRole& r, float* to, const Tile (&S)[N], int col, int part,
+                                        int row0 = 0) const {
     const auto rs = make_rsrc(to, static_cast<uint32_t>(r.K * r.V * 4));
-    const int first = L::kLane * part;  // the lane's first row
+    const int first = row0 + L::kLane * part;  // the lane's first row
     const uint32_t lane = col < r.V ? static_cast<uint32_t>((first * r.V + col) * 4) : kOffNone;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -117,7 +114,8 @@ struct Walk {
   }
 
   template <class L, class Tile, int N>
-  __device__ __forceinline__ void enter_state(const MixCall& w, const MixRole& r, Tile (&S)[N], int col, int part) const {
+  __device__ __forceinline__ void enter_state(const MixCall& w, const MixRole& r, Tile (&S)[N], int col, int part,
+                                              int row0 = 0) const {
     const float* from = r.local ? nullptr : entry ? r.s0 : r.enter;
     if (!from) {
 #pragma unroll
@@ -127,7 +125,7 @@ struct Walk {
     from += ((entry ? static_cast<int64_t>(seq) : slot) * w.heads + head) * r.K * r.V;
     const auto rs = make_rsrc(from, static_cast<uint32_t>(r.K * r.V * 4));
     const bool turned = entry && r.s0_turned;
-    const int first = L::kLane * part;
+    const int first = row0 + L::kLane * part;
     const uint32_t lane = static_cast<uint32_t>((turned ? col * r.K + first : first * r.V + col) * 4);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -146,22 +144,22 @@ struct Walk {
   // forward what enters chunk c, in reverse what enters it from behind.
   template <class L, class Tile, int N>
   __device__ __forceinline__ void leave_mark(const MixCall& w, const MixRole& r, const Tile (&S)[N], int c, int C, int col,
-                                             int part) const {
+                                             int part, int row0 = 0) const {
     const int between = reverse ? c + 1 : c, mark = kMarkSteps / C;
     if (!r.marks || between == 0 || between >= chunks || between % mark) return;
     const int64_t at = first_slot(begin, seq, kMarkSteps) + between / mark;
-    write<L>(r, r.marks + (at * w.heads + head) * r.K * r.V, S, col, part);
+    write<L>(r, r.marks + (at * w.heads + head) * r.K * r.V, S, col, part, row0);
   }
 
   template <class L, class Tile, int N>
   __device__ __forceinline__ void leave_state(const MixCall& w, const MixRole& r, const Tile (&S)[N], const Gone& gone,
-                                              int col, int part) const {
+                                              int col, int part, int row0 = 0) const {
     const int64_t size = static_cast<int64_t>(r.K) * r.V;
     if (r.local) {
-      write<L>(r, r.local + (slot * w.heads + head) * size, S, col, part);
+      write<L>(r, r.local + (slot * w.heads + head) * size, S, col, part, row0);
       if (threadIdx.x == 0 && tile == 0) r.gone[slot * w.heads + head] = gone.cut ? 0.0f : exp_of(gone.sum);
     } else if (r.last && exit) {
-      write<L>(r, r.last + (static_cast<int64_t>(seq) * w.heads + head) * size, S, col, part);
+      write<L>(r, r.last + (static_cast<int64_t>(seq) * w.heads + head) * size, S, col, part, row0);
     }
   }
 
