@@ -12,6 +12,7 @@ namespace {
 // gone_p enter_p + local_p, of which local and gone are known by then; enter takes
 // local's place. A thread takes four elements of one (sequence, head).
 constexpr int kJoinThreads = 256;
+constexpr int kJoinAhead = 8;
 
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk, int64_t blocks) {
   const MixRole& r = w.role[blockIdx.y];
@@ -30,19 +31,30 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk
     for (int k = 0; k < 4; ++k)
       cur[k] = r.s0_turned ? from[(e + k) % r.V * r.K + (e + k) / r.V] : from[e + k];
   }
-  for (int p = 0; p < segs; ++p) {
-    const int64_t at = (base + (r.reverse ? segs - 1 - p : p)) * w.heads + head;
-    float* to = r.local + at * size + e;
-    float own[4] = {}, gone = 0.0f;
-    if (p + 1 < segs) {
-      Piece<F32Io, 4> piece;
-      piece.load(to);
-      for (int k = 0; k < 4; ++k) own[k] = piece.get(k);
-      gone = r.gone[at];
+  // kJoinAhead segments' loads go out together
+  for (int p0 = 0; p0 < segs; p0 += kJoinAhead) {
+    float own[kJoinAhead][4], gone[kJoinAhead];
+#pragma unroll
+    for (int i = 0; i < kJoinAhead; ++i) {
+      Piece<F32Io, 4> piece = {};
+      gone[i] = 0.0f;
+      if (p0 + i + 1 < segs) {  // (nobody needs what the last one leaves)
+        const int64_t at = (base + (r.reverse ? segs - 1 - p0 - i : p0 + i)) * w.heads + head;
+        piece.load(r.local + at * size + e);
+        gone[i] = r.gone[at];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) own[i][k] = piece.get(k);
     }
-    for (int k = 0; k < 4; ++k) {
-      to[k] = cur[k];
-      cur[k] = gone != 0.0f ? fmaf(gone, cur[k], own[k]) : own[k];
+#pragma unroll
+    for (int i = 0; i < kJoinAhead; ++i) {
+      if (p0 + i >= segs) break;
+      const int64_t at = (base + (r.reverse ? segs - 1 - p0 - i : p0 + i)) * w.heads + head;
+      Piece<F32Io, 4> piece;
+      piece.set(cur);
+      piece.store(r.local + at * size + e);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) cur[k] = gone[i] != 0.0f ? fmaf(gone[i], cur[k], own[i][k]) : own[i][k];
     }
   }
 }
@@ -227,18 +239,25 @@ int chunk_of(const LinattnSizes& n) { return n.io == MAMBA_F32 && (n.K > n.V ? n
 int64_t chunks_of(const LinattnSizes& n) { return (n.rows + chunk_of(n) - 1) / chunk_of(n); }
 
 // Chunks of a segment, when `walks` workgroups walk each sequence. One segment per
-// sequence reads everything once; more let a few long sequences fill the machine, at
-// the price of reading keys and values twice. Of packed sequences the lengths are not
-// known here: they are cut as one would be, unless there are very many.
-constexpr int64_t kLeastPer = 8;
+// sequence reads everything once; more let few sequences fill the machine, two
+// workgroups for each compute unit, at the price of reading keys and values twice and of
+// the states between. Sequences of one length get as many segments as workgroups fit (one
+// more would wait for a place: 131072 steps of 20 heads, 500 workgroups 1.25 ms, 520 1.32).
+// Of packed sequences the lengths are not known here: they are cut as one would be, unless
+// there are very many. Down to one chunk: at least 8, 4, 2 and 1 of them took 87, 57, 47
+// and 54 us for 1 x 2048 steps of 16 heads (128 x 128 bf16), 49, 51, 36 and 31 for 512 of 8, and
+// 675, 377, 218 and 145 for the gradients of 881 of 6 heads (40 x 72 fp32).
 int per_of(const LinattnSizes& n, int64_t walks) {
-  const int64_t chunks = chunks_of(n), want = 2 * compute_units();
-  const int64_t whole = chunks + 1;
-  const int64_t units = n.batch * walks;
-  if (units >= (n.packed ? 16 * want : want / 2)) return static_cast<int>(whole);
-  int64_t per = (chunks * walks + want - 1) / want;
-  if (per < kLeastPer) per = kLeastPer;
-  return static_cast<int>(per < whole ? per : whole);
+  const int64_t chunks = chunks_of(n), want = 2 * compute_units(), whole = chunks + 1, units = n.batch * walks;
+  if (n.packed) {
+    if (units >= 16 * want) return static_cast<int>(whole);
+    const int64_t per = (chunks * walks + want - 1) / want;
+    return static_cast<int>(per < 1 ? 1 : per < whole ? per : whole);
+  }
+  if (units == 0 || 2 * units > want) return static_cast<int>(whole);
+  const int64_t own = (n.seqlen + chunk_of(n) - 1) / chunk_of(n), segs = want / units;
+  const int64_t per = segs > own ? 1 : (own + segs - 1) / segs;
+  return static_cast<int>(per < 1 ? 1 : per);
 }
 bool split(const LinattnSizes& n, int per) { return per <= (n.packed ? chunks_of(n) : (n.seqlen - 1) / chunk_of(n)); }
 
