@@ -69,7 +69,8 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk
 // summed from the sequence's end, which is the same, would lose what strong decays
 // leave. The first term goes from chunk to chunk, <S_out, dS_out> - sum a + sum b,
 // and is formed anew from the states at every mark. One workgroup per stretch between
-// marks and head.
+// marks and head: its waves form their chunks' sums side by side, and the first terms
+// follow from those.
 constexpr int kDecayThreads = 256;
 
 struct DecayGrad {
@@ -85,15 +86,24 @@ struct DecayGrad {
   int atiles, btiles, K, V;
 };
 
+// Sum over a wave, in each lane.
+__device__ __forceinline__ double over_wave(double v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+
 template <int C>
 __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) {
   const MixCall& w = p.w;
-  __shared__ double s_sum[kDecayThreads / 64];
-  __shared__ Decays<C> dec;
-  const int tid = threadIdx.x, lane = tid & 63;
+  constexpr int kMark = kMarkSteps / C, kWaves = kDecayThreads / 64, kEach = kMark / kWaves;
+  constexpr int kBlock = 64;  // channels of the states' product at a time, each way
+  __shared__ float s_state[kBlock][kBlock + 1];
+  __shared__ double s_sum[kWaves], s_a[kMark], s_b[kMark];
+  __shared__ int s_keeps[kMark];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int head = blockIdx.x % w.heads;
   const int64_t slot = blockIdx.x / w.heads;
-  constexpr int kMark = kMarkSteps / C;
   const int seq = sequence_at(w.offsets, w.batch, w.seqlen, w.rows, kMarkSteps, slot);
   const Sequence s = sequence_of(w.offsets, seq, w.seqlen, w.rows);
   const int64_t chunks = (s.len + C - 1) / C, m = slot - first_slot(s.begin, seq, kMarkSteps), begin = m * kMark;
@@ -101,65 +111,125 @@ __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) 
     if (p.parts && tid == 0) p.parts[slot * w.heads + head] = 0.0f;
     return;
   }
-  const int64_t end = begin + kMark < chunks ? begin + kMark : chunks;
-  // <S, dS> at the stretch's end
+  const int count = static_cast<int>(begin + kMark < chunks ? kMark : chunks - begin);
+  // <S, dS> at the stretch's end; S is there by value channels
   const int64_t size = static_cast<int64_t>(p.K) * p.V;
   const float* S = p.marks + ((slot + 1) * w.heads + head) * size;
   const float* dS = p.dmarks + ((slot + 1) * w.heads + head) * size;
-  if (end == chunks) {
+  if (begin + count == chunks) {
     S = p.last ? p.last + (static_cast<int64_t>(seq) * w.heads + head) * size : nullptr;
     dS = p.dlast ? p.dlast + (static_cast<int64_t>(seq) * w.heads + head) * size : nullptr;
   }
+  // each wave's chunks: lane = step
+  float g[kEach];
+  double a[kEach], b[kEach];
+  bool on[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int64_t at = (begin + wave + i * kWaves) * C + lane;
+    on[i] = wave + i * kWaves < count && lane < C && at < s.len;
+    g[i] = on[i] ? w.g[(s.begin + at) * w.g_step + head] : 0.0f;
+    a[i] = b[i] = 0.0;
+  }
+  const int64_t first = head * w.rows + s.begin + (begin + wave) * C + lane, plane = static_cast<int64_t>(w.heads) * w.rows;
+  for (int k = 0; k < p.atiles; ++k)
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (on[i]) {
+        const float* from = p.a + k * plane + first + i * kWaves * C;
+        a[i] += from[0];
+        b[i] -= from[p.atiles * plane];
+      }
+  for (int k = 0; k < p.btiles; ++k)
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (on[i]) {
+        const float* from = p.b + k * plane + first + i * kWaves * C;
+        b[i] += from[0];
+        b[i] += from[p.btiles * plane];
+      }
   double dot = 0.0;
   if (S && dS)
-    for (int64_t e = tid; e < size; e += kDecayThreads)
-      dot += static_cast<double>(dS[e]) * S[e % p.V * p.K + e / p.V];
+    for (int k0 = 0; k0 < p.K; k0 += kBlock)
+      for (int v0 = 0; v0 < p.V; v0 += kBlock) {
+        constexpr int kPieces = kBlock * kBlock / 4 / kDecayThreads;
+        float4 u[kPieces], t[kPieces];
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) dot += __shfl_xor(dot, off);
-  if (lane == 0) s_sum[tid >> 6] = dot;
-  __syncthreads();
-  if (tid >= 64) return;
-  double X = 0.0, all = 0.0;
-  for (int k = 0; k < kDecayThreads / 64; ++k) X += s_sum[k];
-  for (int64_t c = end - 1; c >= begin; --c) {
-    const int64_t c0 = c * C, row = s.begin + c0 + lane;
-    const int n = s.len - c0 < C ? static_cast<int>(s.len - c0) : C;
-    const bool live = lane < n;
-    const float g = live ? w.g[row * w.g_step + head] : 0.0f;
-    const float kept = chunk_decays<C>(dec, g, n, false, 1.0f, 1.0f, 1.0f);
-    double a = 0.0, b = 0.0;
-    if (live) {
-      for (int k = 0; k < p.atiles; ++k) {
-        const float* from = p.a + (static_cast<int64_t>(k) * w.heads + head) * w.rows + row;
-        a += from[0];
-        b -= from[static_cast<int64_t>(p.atiles) * w.heads * w.rows];
+        for (int i = 0; i < kPieces; ++i) {
+          const int r = (tid + i * kDecayThreads) / (kBlock / 4), c = (tid + i * kDecayThreads) % (kBlock / 4) * 4;
+          u[i] = t[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (k0 + r < p.K && v0 + c < p.V)
+            u[i] = *reinterpret_cast<const float4*>(dS + static_cast<int64_t>(k0 + r) * p.V + v0 + c);
+          if (v0 + r < p.V && k0 + c < p.K)
+            t[i] = *reinterpret_cast<const float4*>(S + static_cast<int64_t>(v0 + r) * p.K + k0 + c);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int r = (tid + i * kDecayThreads) / (kBlock / 4), c = (tid + i * kDecayThreads) % (kBlock / 4) * 4;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s_state[r][c + k] = (&u[i].x)[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int r = (tid + i * kDecayThreads) / (kBlock / 4), c = (tid + i * kDecayThreads) % (kBlock / 4) * 4;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dot += static_cast<double>(s_state[c + k][r]) * (&t[i].x)[k];
+        }
       }
-      for (int k = 0; k < p.btiles; ++k) {
-        const float* from = p.b + (static_cast<int64_t>(k) * w.heads + head) * w.rows + row;
-        b += from[0];
-        b += from[static_cast<int64_t>(p.btiles) * w.heads * w.rows];
-      }
-    }
-    double pre = a, post = b;  // sums up to here, and from here on
+  dot = over_wave(dot);
+  if (lane == 0) s_sum[wave] = dot;
+  // sums before and from each step on, and over all of a chunk
+  double within[kEach];
+  bool live[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int c = wave + i * kWaves;
+    const bool cut = on[i] && g[i] <= kNoDecay;
+    double pre = a[i], post = b[i];  // sums up to here, and from here on
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const double u = __shfl_up(pre, off), v = __shfl_down(post, off);
       if (lane >= off) pre += u;
       if (lane + off < 64) post += v;
     }
-    const double sum_a = __shfl(pre, 63), sum_b = __shfl(post, 0);
+    const double total = over_wave(cut ? 0.0 : static_cast<double>(g[i]));
+    if (lane == 63) s_a[c] = pre;
+    if (lane == 0) {
+      s_b[c] = post;
+      s_keeps[c] = !__any(cut) && exp_exactly(total) != 0.0f;
+    }
     pre = __shfl_up(pre, 1);
-    if (lane == 0) pre = 0.0;
-    const double through = kept != 0.0f ? X - sum_a : 0.0;
-    const double grad = live && !(g <= kNoDecay) ? through + pre + post : 0.0;
-    if (p.dg && live) p.dg[row * w.heads + head] = static_cast<float>(grad);
-    all += grad;
-    X = through + sum_b;
+    within[i] = (lane == 0 ? 0.0 : pre) + post;
+    live[i] = on[i] && !cut;  // the gradient of a cut is 0
+    if (p.dg && cut) p.dg[(s.begin + (begin + c) * C + lane) * w.heads + head] = 0.0f;
+  }
+  __syncthreads();
+  double X = 0.0, all = 0.0;
+  for (int k = 0; k < kWaves; ++k) X += s_sum[k];
+  // from the stretch's end to its start, every wave for itself
+  for (int c = count - 1; c >= 0; --c) {
+    const double through = s_keeps[c] ? X - s_a[c] : 0.0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (c == wave + i * kWaves && live[i]) {
+        const double grad = through + within[i];
+        if (p.dg) p.dg[(s.begin + (begin + c) * C + lane) * w.heads + head] = static_cast<float>(grad);
+        all += grad;
+      }
+    X = through + s_b[c];
   }
   if (!p.parts) return;
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) all += __shfl_xor(all, off);
-  if (lane == 0) p.parts[slot * w.heads + head] = static_cast<float>(all);
+  all = over_wave(all);
+  __syncthreads();
+  if (lane == 0) s_sum[wave] = all;
+  __syncthreads();
+  if (tid == 0) {
+    double sum = 0.0;
+    for (int k = 0; k < kWaves; ++k) sum += s_sum[k];
+    p.parts[slot * w.heads + head] = static_cast<float>(sum);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -320,7 +390,7 @@ hipError_t run(MixCall w, const LinattnSizes& n, bool cut, hipStream_t stream) {
 }
 
 hipError_t zero_rest(const RestRows& z, hipStream_t stream) {
-  hipLaunchKernelGGL(zero_rest_kernel, dim3(static_cast<unsigned>(z.rows < 2048 ? z.rows : 2048)), dim3(256), 0, stream, z);
+  hipLaunchKernelGGL(zero_rest_kernel, dim3(static_cast<unsigned>(z.rows < 256 ? z.rows : 256)), dim3(256), 0, stream, z);
   return hipGetLastError();
 }
 
