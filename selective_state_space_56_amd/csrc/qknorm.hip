@@ -104,13 +104,13 @@ __device__ __forceinline__ void store_row(const float (&x)[8], typename IO::raw*
 }
 
 // The lane's pairs turned; BACK: by the angles' negatives.
-template <bool BACK>
-__device__ __forceinline__ void turn_row(float (&x)[8], const Turn& t, const Place& s, bool interleaved) {
+template <bool BACK, bool INTER>
+__device__ __forceinline__ void turn_row(float (&x)[8], const Turn& t, const Place& s) {
   if (!s.turns) return;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float sn = BACK ? -t.s[e] : t.s[e];
-    const int i = interleaved ? 2 * e : e, j = interleaved ? 2 * e + 1 : 4 + e;
+    const int i = INTER ? 2 * e : e, j = INTER ? 2 * e + 1 : 4 + e;
     const float a = x[i], b = x[j];
     x[i] = fmaf(a, t.c[e], -b * sn);
     x[j] = fmaf(b, t.c[e], a * sn);
@@ -132,7 +132,7 @@ __device__ __forceinline__ void load_weight(float (&w)[8], const float* from, co
 __device__ __forceinline__ float rstd_of(float ms, float eps) { return 1.0f / sqrtf(ms + eps); }
 
 // A wave takes `each` heads of one token at a time, 64 / LP of them side by side.
-template <class IO>
+template <class IO, bool INTER>
 __global__ __launch_bounds__(kThreads) void qknorm_fwd_kernel(QkNormProblem p, int LP, int each, int64_t units, int parts) {
   using raw = typename IO::raw;
   const Place s = place_of(p, LP);
@@ -160,14 +160,14 @@ __global__ __launch_bounds__(kThreads) void qknorm_fwd_kernel(QkNormProblem p, i
       const float r = rstd_of(over_row(sq, LP) * scale, p.eps);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = x[e] * r * (key ? wk[e] : wq[e]);
-      turn_row<false>(x, t, s, p.interleaved);
+      turn_row<false, INTER>(x, t, s);
       if (on)
         store_row<IO>(x, key ? static_cast<raw*>(p.ko) + token * p.sko + at : static_cast<raw*>(p.qo) + token * p.sqo + at, s);
     }
   }
 }
 
-template <class IO>
+template <class IO, bool INTER>
 __global__ __launch_bounds__(kThreads) void qknorm_bwd_kernel(QkNormProblem p, int LP, int each, int64_t units, int parts,
                                                               float* sums) {
   using raw = typename IO::raw;
@@ -194,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void qknorm_bwd_kernel(QkNormProblem p, i
         load_row<IO>(dy, key ? static_cast<const raw*>(p.dko) + token * p.sdko + at
                              : static_cast<const raw*>(p.dqo) + token * p.sdqo + at, s);
       }
-      turn_row<true>(dy, t, s, p.interleaved);
+      turn_row<true, INTER>(dy, t, s);
       float sq = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
@@ -294,10 +294,10 @@ Plan bwd_plan(int64_t tokens, int64_t heads, int64_t dim) {
 hipError_t launch_qknorm_fwd(const QkNormProblem& p, hipStream_t stream) {
   const Plan s = plan_of(p.tokens, p.qheads + p.kheads, p.dim, compute_units() * kFwdWavesPerCu);
   const dim3 grid(static_cast<unsigned>(s.groups < (1 << 22) ? s.groups : 1 << 22));
-  if (p.io == MAMBA_BF16)
-    hipLaunchKernelGGL((qknorm_fwd_kernel<Bf16Io>), grid, dim3(kThreads), 0, stream, p, s.LP, s.each, s.units, s.parts);
-  else
-    hipLaunchKernelGGL((qknorm_fwd_kernel<F32Io>), grid, dim3(kThreads), 0, stream, p, s.LP, s.each, s.units, s.parts);
+  const auto kernel = p.io == MAMBA_BF16 ? p.interleaved ? qknorm_fwd_kernel<Bf16Io, true> : qknorm_fwd_kernel<Bf16Io, false>
+                      : p.interleaved    ? qknorm_fwd_kernel<F32Io, true>
+                                         : qknorm_fwd_kernel<F32Io, false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, p, s.LP, s.each, s.units, s.parts);
   return hipGetLastError();
 }
 
@@ -313,10 +313,10 @@ hipError_t launch_qknorm_bwd(const QkNormProblem& p, void* workspace, hipStream_
     const Plan s = bwd_plan(p.tokens, p.qheads + p.kheads, p.dim);
     const dim3 grid(static_cast<unsigned>(s.groups));
     groups = s.groups;
-    if (p.io == MAMBA_BF16)
-      hipLaunchKernelGGL((qknorm_bwd_kernel<Bf16Io>), grid, dim3(kThreads), 0, stream, p, s.LP, s.each, s.units, s.parts, sums);
-    else
-      hipLaunchKernelGGL((qknorm_bwd_kernel<F32Io>), grid, dim3(kThreads), 0, stream, p, s.LP, s.each, s.units, s.parts, sums);
+    const auto kernel = p.io == MAMBA_BF16 ? p.interleaved ? qknorm_bwd_kernel<Bf16Io, true> : qknorm_bwd_kernel<Bf16Io, false>
+                        : p.interleaved    ? qknorm_bwd_kernel<F32Io, true>
+                                           : qknorm_bwd_kernel<F32Io, false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, p, s.LP, s.each, s.units, s.parts, sums);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

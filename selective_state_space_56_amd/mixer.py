@@ -30,9 +30,12 @@ class LinattnStrides(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("q", "k", "v", "out", "dq", "dk", "dv")]
 
 
+_Sections = ctypes.c_int64 * AXES
+
+
 class QkNormDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "qheads", "kheads", "headdim", "rotary")] + [
-        ("sections", ctypes.c_int64 * AXES), ("naxes", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+        ("sections", _Sections), ("naxes", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
         ("eps", ctypes.c_float), ("flags", ctypes.c_uint32)]
 
 
@@ -96,41 +99,38 @@ class _Call:
     """The checked arguments that linear attention's calls share."""
 
     def __init__(self, who, q, k, v, g, scale, offsets=None, token=False):
-        lead = 2 if offsets is None and not token else 1
-        what = ("(batch, heads, size)" if token else "(batch, L, heads, size)" if lead == 2 else "(tokens, heads, size)")
-        self.io, self.dev = _io_of(who, v, lead + 2, f"v must be {what}")
-        if not isinstance(q, torch.Tensor) or q.dim() != lead + 2:
+        dims = 4 if offsets is None and not token else 3
+        what = ("(batch, heads, size)" if token else "(batch, L, heads, size)" if dims == 4 else "(tokens, heads, size)")
+        self.io, self.dev = io, dev = _io_of(who, v, dims, f"v must be {what}")
+        if not isinstance(q, torch.Tensor) or q.dim() != dims:
             raise ValueError(f"{who}: q must be {what}")
-        io, dev = self.io, self.dev
-        self.lead, self.H, self.V = v.shape[:lead], v.shape[lead], v.shape[lead + 1]
-        G, K = q.shape[lead], q.shape[lead + 1]
-        self.K = K
-        if G < 1 or self.H % G:
-            raise ValueError(f"{who}: {G} heads of q and k must divide the {self.H} of v")
-        self.qk = self.lead + (G, K)
-        self.shape = v.shape
-        self.sq = _heads(q, "q", self.qk, io, dev)
-        self.sk = _heads(k, "k", self.qk, io, dev)
-        self.sv = _heads(v, "v", v.shape, io, dev)
+        self.shape, self.qk = shape, qk = v.shape, q.shape
+        *lead, H, V = shape
+        *other, G, K = qk
+        if other != lead:
+            raise ValueError(f"q has shape {tuple(qk)}, expected {(*lead, G, K)}")
+        if G < 1 or H % G:
+            raise ValueError(f"{who}: {G} heads of q and k must divide the {H} of v")
+        self.sq, self.sk = _heads(q, "q", qk, io, dev), _heads(k, "k", qk, io, dev)
+        self.sv = _heads(v, "v", shape, io, dev)
         flags = 0
+        if g is None:
+            raise TypeError("g must be a torch.Tensor")
         if isinstance(g, torch.Tensor) and g.dim() == 1:
-            _whole(g, "g", (self.H,), F32, dev)
+            _whole(g, "g", (H,), F32, dev)
             flags = HEAD_DECAY
         else:
-            if g is None:
-                raise TypeError("g must be a torch.Tensor")
-            _whole(g, "g", self.lead + (self.H,), F32, dev)
+            _whole(g, "g", (*lead, H), F32, dev)
         if offsets is None:
-            batch, seqlen = self.lead[0], 1 if token else self.lead[1]
+            batch, seqlen = lead[0], 1 if token else lead[1]
         else:
             if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 1:
                 raise ValueError(f"{who}: offsets must be (sequences + 1,)")
             _whole(offsets, "offsets", offsets.shape, torch.int64, dev)
-            batch, seqlen = offsets.shape[0] - 1, self.lead[0]
+            batch, seqlen = offsets.shape[0] - 1, lead[0]
             flags |= PACKED
-        self.state = (batch, self.H, K, self.V)
-        self.desc = LinattnDesc(batch, seqlen, self.H, G, K, self.V, _IO[io], flags,
-                                K ** -0.5 if scale is None and K else scale or 0.0)
+        self.state = (batch, H, K, V)
+        self.desc = LinattnDesc(batch, seqlen, H, G, K, V, _IO[io], flags, K ** -0.5 if scale is None and K else scale or 0.0)
 
     def zero_rest(self):
         if self.desc.flags & PACKED:
@@ -161,13 +161,13 @@ def linear_attn_fwd(q, k, v, g, *, scale=None, h0=None, offsets=None, out=None, 
     lib = _library()
     c = _Call("linear_attn_fwd", q, k, v, g, scale, offsets)
     _whole(h0, "h0", c.state, F32, c.dev)
-    if out is None:
-        out = torch.empty(c.shape, dtype=c.io, device=c.dev)
-        c.zero_rest()
     so = _heads(out, "out", c.shape, c.io, c.dev)
+    if out is None:
+        out = torch.empty_like(v)
+        c.zero_rest()
+    _whole(last_state, "last_state", c.state, F32, c.dev)
     if last_state is None and return_last_state:
         last_state = _new(c.state, F32, c.dev)
-    _whole(last_state, "last_state", c.state, F32, c.dev)
     d = ctypes.byref(c.desc)
     ws, nbytes = _workspace(c.dev, lib.mamba_linattn_workspace_size, d)
     _run(c.dev, lib.mamba_linattn_fwd, d, c.strides(so), _p(q), _p(k), _p(v), _p(g), _p(h0), _p(offsets), _p(out),
@@ -191,17 +191,17 @@ def linear_attn_bwd(q, k, v, g, dout, *, scale=None, h0=None, offsets=None, dlas
         raise TypeError("dout must be a torch.Tensor")
     _whole(h0, "h0", c.state, F32, c.dev)
     _whole(dlast, "dlast", c.state, F32, c.dev)
-    make = torch.empty
+    make = torch.empty_like
     if dq is None and dk is None and dv is None:
         c.zero_rest()
     elif offsets is not None:
-        make = torch.zeros
-    dq = make(c.qk, dtype=c.io, device=c.dev) if dq is None else dq
-    dk = make(c.qk, dtype=c.io, device=c.dev) if dk is None else dk
-    dv = make(c.shape, dtype=c.io, device=c.dev) if dv is None else dv
+        make = torch.zeros_like
     sdq, sdk = _heads(dq, "dq", c.qk, c.io, c.dev), _heads(dk, "dk", c.qk, c.io, c.dev)
     sdv = _heads(dv, "dv", c.shape, c.io, c.dev)
-    dg = make(g.shape, dtype=F32, device=c.dev) if want_dg else None
+    dq = make(q) if dq is None else dq
+    dk = make(k) if dk is None else dk
+    dv = make(v) if dv is None else dv
+    dg = make(g) if want_dg else None
     dh0 = _new(c.state, F32, c.dev) if want_dh0 else None
     d = ctypes.byref(c.desc)
     ws, nbytes = _workspace(c.dev, lib.mamba_linattn_bwd_workspace_size, d)
@@ -220,9 +220,9 @@ def linear_attn_update(state, q, k, v, g, *, scale=None, out=None):
     if state is None:
         raise TypeError("state must be a torch.Tensor")
     _whole(state, "state", c.state, F32, c.dev)
-    if out is None:
-        out = torch.empty(c.shape, dtype=c.io, device=c.dev)
     so = _heads(out, "out", c.shape, c.io, c.dev)
+    if out is None:
+        out = torch.empty_like(v)
     _run(c.dev, lib.mamba_linattn_update, ctypes.byref(c.desc), c.strides(so), _p(state), _p(q), _p(k), _p(v), _p(g),
          _p(out))
     return out
@@ -244,9 +244,12 @@ class _QkCall:
             raise ValueError(f"{who}: freqs must be (pairs,)")
         pairs = freqs.shape[0]
         _whole(freqs, "freqs", (pairs,), F32, dev)
-        sections = (pairs,) if sections is None else tuple(int(v) for v in sections)
-        if not 1 <= len(sections) <= AXES:
-            raise ValueError(f"{who}: 1 to {AXES} sections")
+        if sections is None:
+            sections = (pairs,)
+        else:
+            sections = tuple(int(v) for v in sections)
+            if not 1 <= len(sections) <= AXES:
+                raise ValueError(f"{who}: 1 to {AXES} sections")
         if positions is None:
             raise TypeError("positions must be a torch.Tensor")
         one = len(sections) == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 1
@@ -254,7 +257,7 @@ class _QkCall:
         _whole(q_weight, "q_weight", (dim,), F32, dev)
         _whole(k_weight, "k_weight", (dim,), F32, dev)
         self.dim = dim
-        self.desc = QkNormDesc(n, hq, hk, dim, 2 * pairs, (ctypes.c_int64 * AXES)(*sections), len(sections), _IO[io], eps,
+        self.desc = QkNormDesc(n, hq, hk, dim, 2 * pairs, _Sections(*sections), len(sections), _IO[io], eps,
                                INTERLEAVED if interleaved else 0)
 
     def strides(self, sqo, sko, sdq=0, sdk=0):
@@ -275,13 +278,13 @@ def qk_norm_rope_fwd(q, k, positions, freqs, q_weight=None, k_weight=None, *, ep
     input itself (in place)."""
     lib = _library()
     c = _QkCall("qk_norm_rope_fwd", q, k, positions, freqs, q_weight, k_weight, eps, sections, interleaved)
-    if q_out is None:
-        q_out = torch.empty(c.qs, dtype=c.io, device=c.dev)
-    if k_out is None and k is not None:
-        k_out = torch.empty(c.ks, dtype=c.io, device=c.dev)
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
     s = c.strides(_heads(q_out, "q_out", c.qs, c.io, c.dev), _heads(k_out, "k_out", c.ks, c.io, c.dev))
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    if k_out is None and k is not None:
+        k_out = torch.empty_like(k)
     _run(c.dev, lib.mamba_qknorm_fwd, ctypes.byref(c.desc), s, _p(q), _p(k), _p(positions), _p(freqs), _p(q_weight),
          _p(k_weight), _p(q_out), _p(k_out))
     return q_out, k_out
@@ -301,11 +304,11 @@ def qk_norm_rope_bwd(q, k, positions, freqs, q_weight, k_weight, dq_out, dk_out,
     if k is None and dk is not None:
         raise ValueError("dk without k")
     sqo, sko = _heads(dq_out, "dq_out", c.qs, c.io, c.dev), _heads(dk_out, "dk_out", c.ks, c.io, c.dev)
-    if dq is None:
-        dq = torch.empty(c.qs, dtype=c.io, device=c.dev)
-    if dk is None and k is not None:
-        dk = torch.empty(c.ks, dtype=c.io, device=c.dev)
     s = c.strides(sqo, sko, _heads(dq, "dq", c.qs, c.io, c.dev), _heads(dk, "dk", c.ks, c.io, c.dev))
+    if dq is None:
+        dq = torch.empty_like(q)
+    if dk is None and k is not None:
+        dk = torch.empty_like(k)
     dwq = None if q_weight is None else torch.empty_like(q_weight)
     dwk = None if k_weight is None else torch.empty_like(k_weight)
     d = ctypes.byref(c.desc)
