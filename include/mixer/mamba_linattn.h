@@ -23,8 +23,9 @@
  * one after another in seqlen token rows: sequence i is rows offsets[i] ..
  * offsets[i + 1] - 1 (none when they are equal), offsets being batch + 1 values
  * on the device that do not decrease, in 0 .. seqlen. They are read when the
- * kernels run; a value outside 0 .. seqlen counts as the nearer end, one below
- * its predecessor as that. Rows of no sequence are left as they were, unless
+ * kernels run; a value outside 0 .. seqlen counts as the nearer end. With values
+ * that decrease the outputs hold unspecified numbers, but nothing outside them
+ * is written. Rows of no sequence are left as they were, unless
  * MAMBA_LINATTN_ZERO_REST asks for zeros in those before the first and behind
  * the last sequence.
  *
@@ -34,8 +35,12 @@
  * outputs and workspaces are. io tensors (q, k, v, out and their gradients) are
  * float32 or bfloat16; g, states, dg and dh0 are float32. States, products and
  * sums are held in float32; with bfloat16 io the products are taken on the
- * matrix cores from bfloat16 operands, float32 ones as sums of two or three
- * bfloat16 parts, the outputs rounded once. Results are deterministic.
+ * matrix cores from bfloat16 operands, and what is float32 goes in as a sum of
+ * bfloat16 parts: three, whose sum is the value, where it makes the state, and
+ * two, off by 2^-17 of each term, where it makes an output. The outputs are
+ * rounded once. (Parts of an infinity, or of a value that rounds to one in
+ * bfloat16, add up to NaN: such a state or score reaches the outputs as NaN.)
+ * Results are deterministic.
  */
 #ifndef MAMBA_LINATTN_H
 #define MAMBA_LINATTN_H
@@ -73,8 +78,9 @@ typedef struct mamba_linattn_desc {
  * be column slices of one projection's rows and their gradients of one
  * gradient's; 0 = contiguous (heads * head size). Elements within a row stay
  * contiguous. `out` is out's, or dout's in the backward. Below a row's length:
- * MAMBA_ERR_INVALID_ARG; above 2^23 (a row's length too): MAMBA_ERR_UNSUPPORTED. A NULL struct means
- * all contiguous. Any two inputs may interleave, and so may dq, dk and dv.
+ * MAMBA_ERR_INVALID_ARG; above 2^23, also of contiguous rows:
+ * MAMBA_ERR_UNSUPPORTED. A NULL struct means all contiguous. Any two inputs may
+ * interleave, and so may dq, dk and dv.
  */
 typedef struct mamba_linattn_strides {
   int64_t q, k, v, out, dq, dk, dv;
@@ -125,7 +131,7 @@ mamba_status mamba_linattn_fwd(const mamba_linattn_desc *desc,
  *   dlast      : (batch, H, K, V) float32 or NULL (zero).
  *   dq, dk     : (rows, G, K) io dtype, written.
  *   dv         : (rows, H, V) io dtype, written.
- *   dg         : as g, float32, written, or NULL (skip; about a third less work).
+ *   dg         : as g, float32, written, or NULL (skip, which takes less time).
  *   dh0        : (batch, H, K, V) float32 or NULL (skip), written.
  * Overlap and alignment as the forward, except that dq, dk and dv may
  * interleave.

@@ -561,16 +561,11 @@ hipError_t by_values(const MixCall& w, hipStream_t stream) {
                                                                  : launch<KT, 1, 4>(w, stream);
 }
 
-#ifdef ONLY
-template __global__ void walk_bf16_kernel<ONLY, true>(MixCall);
-template __global__ void walk_bf16_kernel<ONLY, false>(MixCall);
 }  // namespace
-#else
-}  // namespace
+
 hipError_t launch_walk_bf16(const MixCall& w, hipStream_t stream) {
   const int kt = key_tiles(w.role[0].K);
   return kt == 2 ? by_values<2>(w, stream) : kt == 4 ? by_values<4>(w, stream) : by_values<8>(w, stream);
 }
-#endif
 
 }  // namespace mscan
