@@ -46,7 +46,7 @@ def scan(q, k, v, g, scale, S, before=None):
         D = e * (keep(D) + gt * keep(M))
         M = e * keep(M) + own.abs()
         states.append((S, M, D))
-        outs.append(tuple(scale * torch.einsum("hk,hkv->hv", q[t] if i == 0 else q[t].abs(), x)
+        outs.append(tuple((abs(scale) if i else scale) * torch.einsum("hk,hkv->hv", q[t].abs() if i else q[t], x)
                           for i, x in enumerate((S, M, D))))
     return outs, states
 
@@ -112,7 +112,7 @@ def linattn(q, k, v, g, scale, h0=None, offsets=None, dout=None, dlast=None):
             _, Sm, Sd = states[t]
             ad = do[r].abs()
             grads["dq"][0][r] = scale * torch.einsum("hkv,hv->hk", states[t][0], do[r])
-            grads["dq"][1][r] = bound(scale * torch.einsum("hkv,hv->hk", Sm, ad), scale * torch.einsum("hkv,hv->hk", Sd, ad),
+            grads["dq"][1][r] = bound(abs(scale) * torch.einsum("hkv,hv->hk", Sm, ad), abs(scale) * torch.einsum("hkv,hv->hk", Sd, ad),
                                       t + N, io)
             av, ak = ve[r].abs(), ke[r].abs()
             grads["dk"][0][r] = torch.einsum("hkv,hv->hk", dS, ve[r])
@@ -171,8 +171,8 @@ def update(state, q, k, v, g, scale):
     new = kept + own
     err = kept.abs() * (torch.where(cut, 0.0, g.abs()) * 2 * U + 4 * U) + 2 * U * (kept.abs() + own.abs())
     o = scale * (q[..., None] * new).sum(-2)
-    mag = scale * (q.abs()[..., None] * (new.abs() + err)).sum(-2)
-    return {"state": (new, err), "out": (o, scale * (q.abs()[..., None] * err).sum(-2) + mag * (K + 4) * U)}
+    mag = abs(scale) * (q.abs()[..., None] * (new.abs() + err)).sum(-2)
+    return {"state": (new, err), "out": (o, abs(scale) * (q.abs()[..., None] * err).sum(-2) + mag * (K + 4) * U)}
 
 
 def angles(positions, freqs, sections):
