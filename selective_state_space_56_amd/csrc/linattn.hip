@@ -305,7 +305,7 @@ int64_t compute_units() {
 }
 
 // Steps of a chunk: what the kernels' tiles hold.
-int chunk_of(const LinattnSizes& n) { return n.io == MAMBA_F32 && (n.K > n.V ? n.K : n.V) > 128 ? 32 : 64; }
+int chunk_of(const LinattnSizes& n) { return n.io == MAMBA_F32 ? 32 : 64; }
 int64_t chunks_of(const LinattnSizes& n) { return (n.rows + chunk_of(n) - 1) / chunk_of(n); }
 
 // Chunks of a segment, when `walks` workgroups walk each sequence. One segment per
@@ -316,7 +316,7 @@ int64_t chunks_of(const LinattnSizes& n) { return (n.rows + chunk_of(n) - 1) / c
 // Of packed sequences the lengths are not known here: they are cut as one would be, unless
 // there are very many. Down to one chunk: at least 8, 4, 2 and 1 of them took 87, 57, 47
 // and 54 us for 1 x 2048 steps of 16 heads (128 x 128 bf16), 49, 51, 36 and 31 for 512 of 8, and
-// 675, 377, 218 and 145 for the gradients of 881 of 6 heads (40 x 72 fp32).
+// 675, 377, 218 and 145 for the gradients of 881 of 6 heads (40 x 72 fp32, in chunks of 64).
 int per_of(const LinattnSizes& n, int64_t walks) {
   const int64_t chunks = chunks_of(n), want = 2 * compute_units(), whole = chunks + 1, units = n.batch * walks;
   if (n.packed) {
@@ -366,13 +366,13 @@ void give_segments(MixRole& r, const SegmentBytes& s, char*& at) {
 }
 
 hipError_t walk(const MixCall& w, int io, int chunk, hipStream_t stream) {
-  return io == MAMBA_BF16 ? launch_walk_bf16(w, stream) : launch_walk_f32(w, chunk, stream);
+  return io == MAMBA_BF16 ? launch_walk_bf16(w, stream) : launch_walk_f32(w, stream);
 }
 
 // The runs of w: with segments, first what each leaves, then what enters each.
 hipError_t run(MixCall w, const LinattnSizes& n, bool cut, hipStream_t stream) {
   const int chunk = chunk_of(n);
-  w.tiles = value_tiles(n.io, w.role[0].K, w.role[0].V);
+  w.tiles = value_tiles(w.role[0].V);
   w.together = static_cast<uint32_t>(n.heads / n.groups * w.tiles * w.roles);
   if (cut) {
     hipError_t e = walk(w, n.io, chunk, stream);
@@ -395,7 +395,7 @@ hipError_t zero_rest(const RestRows& z, hipStream_t stream) {
 }
 
 // Workgroups of the backward's three runs for each sequence.
-int64_t bwd_walks(const LinattnSizes& n) { return n.heads * (value_tiles(n.io, n.K, n.V) + 2 * value_tiles(n.io, n.V, n.K)); }
+int64_t bwd_walks(const LinattnSizes& n) { return n.heads * (value_tiles(n.V) + 2 * value_tiles(n.K)); }
 
 // The backward's workspace.
 struct BwdBytes {
@@ -409,8 +409,8 @@ BwdBytes bwd_bytes(const LinattnSizes& n, bool head_decay) {
   s.seg = segment_bytes(n, per_of(n, bwd_walks(n)));
   s.mark_slots = slots_of(n.rows, n.batch, kMarkSteps);
   s.marks = r256(static_cast<size_t>(s.mark_slots) * n.heads * n.K * n.V * 4);
-  s.a = r256(static_cast<size_t>(2 * value_tiles(n.io, n.K, n.V)) * n.heads * n.rows * 4);
-  s.b = r256(static_cast<size_t>(2 * value_tiles(n.io, n.V, n.K)) * n.heads * n.rows * 4);
+  s.a = r256(static_cast<size_t>(2 * value_tiles(n.V)) * n.heads * n.rows * 4);
+  s.b = r256(static_cast<size_t>(2 * value_tiles(n.K)) * n.heads * n.rows * 4);
   s.last = r256(static_cast<size_t>(n.batch) * n.heads * n.K * n.V * 4);
   s.part = n.heads == n.groups ? 0 : r256(static_cast<size_t>(n.rows) * n.heads * n.K * 4);
   s.parts = head_decay ? r256(static_cast<size_t>(s.mark_slots) * n.heads * 4) : 0;
@@ -421,7 +421,7 @@ BwdBytes bwd_bytes(const LinattnSizes& n, bool head_decay) {
 
 size_t linattn_fwd_workspace_bytes(const LinattnSizes& n) {
   if (n.rows == 0 || n.heads == 0 || n.batch == 0) return 0;
-  return segment_bytes(n, per_of(n, n.heads * value_tiles(n.io, n.K, n.V))).total();
+  return segment_bytes(n, per_of(n, n.heads * value_tiles(n.V))).total();
 }
 
 size_t linattn_bwd_workspace_bytes(const LinattnSizes& n, bool head_decay) {
@@ -445,7 +445,7 @@ hipError_t launch_linattn_fwd(const LinattnProblem& p, void* workspace, hipStrea
   }
   if (n.batch == 0) return hipSuccess;
   MixCall w = call_of(p);
-  const int per = per_of(n, n.heads * value_tiles(n.io, n.K, n.V));
+  const int per = per_of(n, n.heads * value_tiles(n.V));
   set_segments(w, n, per);
   w.roles = 1;
   MixRole& r = w.role[0];
@@ -579,8 +579,8 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
       d.dlast = p.dlast;
       d.dg = f.head_decay ? nullptr : p.dg;
       d.parts = f.head_decay ? take(s.parts) : nullptr;
-      d.atiles = value_tiles(n.io, K, V);
-      d.btiles = value_tiles(n.io, V, K);
+      d.atiles = value_tiles(V);
+      d.btiles = value_tiles(K);
       d.K = K;
       d.V = V;
     }
@@ -589,8 +589,8 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
       dk.part = take(s.part);
     }
     // roles of the same shape go in one launch: their operands are the same rows
-    const bool same = key_tiles(K) == key_tiles(V) && value_width(n.io, K, V) == value_width(n.io, V, K) &&
-                      value_tiles(n.io, K, V) == value_tiles(n.io, V, K);
+    const bool same = key_tiles(K) == key_tiles(V) && value_width(V) == value_width(K) &&
+                      value_tiles(V) == value_tiles(K);
     w.role[0] = dv;
     w.roles = 1;
     if (same) {

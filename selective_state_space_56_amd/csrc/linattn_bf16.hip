@@ -557,7 +557,7 @@ hipError_t launch(const MixCall& w, hipStream_t stream) {
 
 template <int KT>
 hipError_t by_values(const MixCall& w, hipStream_t stream) {
-  return value_width(MAMBA_BF16, w.role[0].K, w.role[0].V) == 64 ? launch<KT / 2, 2, 2>(w, stream)
+  return value_width(w.role[0].V) == 64 ? launch<KT / 2, 2, 2>(w, stream)
                                                                  : launch<KT, 1, 4>(w, stream);
 }
 

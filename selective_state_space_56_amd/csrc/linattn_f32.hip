@@ -8,7 +8,13 @@
 // operands agree: taken as rows 8 j + 4 (l / 32) + e of the four instructions e,
 // they make S and the scores usable as operands just as they stand in the
 // registers of D, and four of A's values are one 16-byte read.
-#include "linattn.h"
+//
+// Bound by the matrix cores: 8 x 2048 steps of 40 heads of 128 x 128 take 1.05 ms, 49
+// TFLOP/s of 152 that a large product reaches, since 320 workgroups on 256 compute units are
+// two rounds for some. Chunks of 32 steps, not 64 as with bf16: half the scores, and
+// two workgroups fit a compute unit, one of which has products to issue while the other
+// waits (64 steps and one workgroup, rows loaded when they were needed: 1.80 ms, its
+// gradients 4.83 against 2.76). The next chunk's rows are loaded while one is worked on.
 #include "linattn_walk.h"
 
 namespace mscan {
@@ -22,168 +28,212 @@ __device__ __forceinline__ f32x16 mfma(float a, float b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
 }
 
+constexpr int kC = 32;  // steps of a chunk
+
 // Rows of D: see above.
 struct Layout {
   static constexpr int kRows = 16, kLane = 4;
   static constexpr int row(int tile, int i) { return 32 * tile + 8 * (i >> 2) + (i & 3); }
 };
 
-// KT: 32-row tiles of the state; NW: waves, 32 value channels each; CT: 32-step
-// tiles of a chunk.
-template <int KT, int NW, int CT>
-__global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
-  constexpr int C = 32 * CT, kK = 32 * KT, kV = 32 * NW, kThreads = 64 * NW;
+// One operand's rows of a chunk, 8 values at a time: W per row (0 from `have` on and past
+// the chunk's end), N pieces per thread.
+template <int W, int THREADS>
+struct Rows {
+  static constexpr int kPer = W / 8, N = kC * kPer / THREADS;
+  static_assert(kC * kPer % THREADS == 0, "whole rows of pieces");
+  const float* base;
+  int64_t stride;
+  int have;
+  bool back;
+
+  __device__ __forceinline__ Rows(const void* p, int64_t first_row, int64_t stride_, int64_t first_col, int have_, bool reverse)
+      : base(static_cast<const float*>(p) + first_row * stride_ + first_col), stride(stride_), have(have_), back(reverse) {}
+  // rows of a chunk that starts c0 steps into the sequence and has n
+  __device__ __forceinline__ void load(f32x4 (&to)[2 * N], int64_t c0, int n) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int id = threadIdx.x + i * THREADS, row = id / kPer, x = 8 * (id % kPer);
+      to[2 * i] = to[2 * i + 1] = f32x4{};
+      if (row < n && x < have) {
+        Piece<F32Io, 8> v;
+        v.load(base + (c0 + (back ? n - 1 - row : row)) * stride + x);
+        to[2 * i] = f32x4{v.get(0), v.get(1), v.get(2), v.get(3)};
+        to[2 * i + 1] = f32x4{v.get(4), v.get(5), v.get(6), v.get(7)};
+      }
+    }
+  }
+  static __device__ __forceinline__ void keep(const f32x4 (&from)[2 * N], float* tile, int ld) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int id = threadIdx.x + i * THREADS;
+      float* to = tile + id / kPer * ld + 8 * (id % kPer);
+      *reinterpret_cast<f32x4*>(to) = from[2 * i];
+      *reinterpret_cast<f32x4*>(to + 4) = from[2 * i + 1];
+    }
+  }
+};
+
+// Waves per SIMD that the kernels' registers are held to: two workgroups, where they fit.
+constexpr int least_waves(int KT, int NW, bool sums) { return KT == 8 || (KT == 4 && NW == 2 && sums) ? 1 : 2; }
+
+// KT: 32-row tiles of the state; NW: waves, 32 value channels each; SUMS: with the sums for
+// the decays' gradients.
+template <int KT, int NW, bool SUMS>
+__global__ __launch_bounds__(64 * NW, least_waves(KT, NW, SUMS)) void walk_f32_kernel(MixCall w) {
+  constexpr int C = kC, kK = 32 * KT, kV = 32 * NW, kThreads = 64 * NW;
   constexpr int ldk = kK + 4, ldv = kV + 4, ldp = C + 4;
+  using RowsK = Rows<kK, kThreads>;
+  using RowsV = Rows<kV, kThreads>;
   __shared__ Decays<C> dec;
-  __shared__ __align__(16) float s_q[C][ldk], s_k[C][ldk], s_v[C][ldv], s_e[C][ldv], s_p[C][ldp];
-  __shared__ float s_red[NW][C], s_row[CT][C];
+  __shared__ __align__(16) float s_q[C][ldk], s_k[C][ldk], s_v[C][ldv], s_e[SUMS ? C : 1][ldv], s_p[C][ldp];
+  __shared__ float s_red[SUMS ? NW : 1][C], s_row[C];
   Walk at;
   if (!at.find(w, C)) return;
   const MixRole& r = w.role[at.role];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, lo = lane & 31, hi = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, lo = lane & 31, hi = lane >> 5;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = at.tile * kV + 32 * wv + lo;  // this lane's value channel
   const int vw = r.V - at.tile * kV;            // value channels from this tile on
+  const bool outputs = r.local == nullptr, sums = SUMS && r.sums;
 
   f32x16 S[KT];
   at.enter_state<Layout>(w, r, S, col, hi);
 
-  // rows of the chunk's tokens, 8 values at a time; 0 past its end and its channels
-  auto stage = [&](float* to, int ld, int width, const void* from, int64_t stride, int64_t first_col, int have, int64_t c0,
-                   int n) {
-    const int per = width / 8;
-    for (int id = tid; id < C * per; id += kThreads) {
-      const int row = id / per, x = 8 * (id % per);
-      f32x4 a = {}, b = {};
-      if (row < n && x < have) {
-        Piece<F32Io, 8> p;
-        p.load(static_cast<const float*>(from) + (at.begin + at.token(row, c0, n)) * stride + first_col + x);
-        a = f32x4{p.get(0), p.get(1), p.get(2), p.get(3)};
-        b = f32x4{p.get(4), p.get(5), p.get(6), p.get(7)};
-      }
-      *reinterpret_cast<f32x4*>(to + row * ld + x) = a;
-      *reinterpret_cast<f32x4*>(to + row * ld + x + 4) = b;
-    }
+  const RowsK rq(r.q, at.begin, r.sq, static_cast<int64_t>(at.head / r.qdiv) * r.K, r.K, at.reverse);
+  const RowsK rk(r.k, at.begin, r.sk, static_cast<int64_t>(at.head / r.kdiv) * r.K, r.K, at.reverse);
+  const RowsV rv(r.v, at.begin, r.sv, static_cast<int64_t>(at.head / r.vdiv) * r.V + at.tile * kV, vw, at.reverse);
+  const RowsV re(r.e, at.begin, r.se, static_cast<int64_t>(at.head / r.ediv) * r.V + at.tile * kV, vw, at.reverse);
+  f32x4 q[2 * RowsK::N], k[2 * RowsK::N], v[2 * RowsV::N], x[2 * RowsV::N];
+  float g = 0.0f;
+  auto tokens = [&](int c) {
+    const int64_t left = at.len - static_cast<int64_t>(c) * C;
+    return left < C ? static_cast<int>(left) : C;
+  };
+  auto fetch = [&](int c) {
+    const int64_t c0 = static_cast<int64_t>(c) * C;
+    const int n = tokens(c);
+    rk.load(k, c0, n);
+    rv.load(v, c0, n);
+    if (outputs) rq.load(q, c0, n);
+    if (sums) re.load(x, c0, n);
+    if (wv == NW - 1) g = lane < n ? w.g[(at.begin + at.token(lane, c0, n)) * w.g_step + at.head] : 0.0f;
   };
 
   Gone gone;
+  if (at.first != at.stop) fetch(at.first);
   for (int c = at.first; c != at.stop; c += at.step) {
     const int64_t c0 = static_cast<int64_t>(c) * C;
-    const int n = at.len - c0 < C ? static_cast<int>(at.len - c0) : C;
-    if (wv == 0) {
-      const float g = lane < n ? w.g[(at.begin + at.token(lane, c0, n)) * w.g_step + at.head] : 0.0f;
-      chunk_decays<C>(dec, g, n, r.reverse, r.from, r.to, r.score);
-    }
-    if (!r.local) stage(&s_q[0][0], ldk, kK, r.q, r.sq, (at.head / r.qdiv) * r.K, r.K, c0, n);
-    stage(&s_k[0][0], ldk, kK, r.k, r.sk, (at.head / r.kdiv) * r.K, r.K, c0, n);
-    stage(&s_v[0][0], ldv, kV, r.v, r.sv, static_cast<int64_t>(at.head / r.vdiv) * r.V + at.tile * kV, vw, c0, n);
-    if (r.sums) stage(&s_e[0][0], ldv, kV, r.e, r.se, static_cast<int64_t>(at.head / r.ediv) * r.V + at.tile * kV, vw, c0, n);
+    const int n = tokens(c), next = c + at.step;
+    if (wv == NW - 1) chunk_decays<C>(dec, g, n, r.reverse, r.from, r.to, r.score);
+    RowsK::keep(k, &s_k[0][0], ldk);
+    RowsV::keep(v, &s_v[0][0], ldv);
+    if (outputs) RowsK::keep(q, &s_q[0][0], ldk);
+    if (sums) RowsV::keep(x, &s_e[0][0], ldv);
+    if (next != at.stop) fetch(next);
     __syncthreads();
-    if (!r.local) {
+    if (outputs) {
       at.leave_mark<Layout>(w, r, S, c, C, col, hi);
-      // scores, transposed (earlier steps s as rows, steps t as columns), one 32 x 32
-      // tile per wave at a time
-      int turn = 0;
-      for (int ti = 0; ti < CT; ++ti)
-        for (int si = 0; si <= ti; ++si, ++turn) {
-          if (turn % NW != wv) continue;
-          f32x16 p = {};
+      // one wave makes the scores, transposed (earlier steps s as rows, steps t as columns),
+      // and another what the other operands' rows give, each chunk the next ones
+      const int scores = c % NW, others = (c + 1) % NW;
+      f32x16 u = {};
+      if (wv == scores) {
+        f32x16 p = {};
 #pragma unroll 4
-          for (int x = 0; x < kK; x += 8) {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(&s_k[32 * si + lo][x + 4 * hi]);
-            const f32x4 b = *reinterpret_cast<const f32x4*>(&s_q[32 * ti + lo][x + 4 * hi]);
+        for (int j = 0; j < kK; j += 8) {
+          const f32x4 a = *reinterpret_cast<const f32x4*>(&s_k[lo][j + 4 * hi]);
+          const f32x4 b = *reinterpret_cast<const f32x4*>(&s_q[lo][j + 4 * hi]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p = mfma(a[e], b[e], p);
-          }
-          const int t = 32 * ti + lo, from = dec.from[t];
-          const double ell = dec.ell[t];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int s = 32 * si + 8 * (i >> 2) + 4 * hi + (i & 3);
-            const float f = exp_of(ell - dec.ell[s]) * r.score;
-            p[i] = where((s <= t) & (s >= from), p[i] * f);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<f32x4*>(&s_p[t][32 * si + 8 * i + 4 * hi]) =
-                f32x4{p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]};
-          if (r.sums) {
-            f32x16 u = {};
-#pragma unroll 4
-            for (int x = 0; x < kV; x += 8) {
-              const f32x4 a = *reinterpret_cast<const f32x4*>(&s_v[32 * si + lo][x + 4 * hi]);
-              const f32x4 b = *reinterpret_cast<const f32x4*>(&s_e[32 * ti + lo][x + 4 * hi]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) u = mfma(a[e], b[e], u);
-            }
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int s = 32 * si + 8 * (i >> 2) + 4 * hi + (i & 3);
-              u[i] = where((s < t) & (s >= from), u[i] * p[i]);
-              sum += u[i];
-            }
-            sum += __shfl_xor(sum, 32);
-            if (hi == 0) s_row[si][t] = sum;
-          }
+          for (int e = 0; e < 4; ++e) p = mfma(a[e], b[e], p);
         }
-      __syncthreads();
-      for (int ti = 0; ti < CT; ++ti) {
-        f32x16 acc = {};
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(&s_q[32 * ti + lo][32 * kt + 8 * j + 4 * hi]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc = mfma(a[e], S[kt][4 * j + e], acc);
-          }
+        const int from = dec.from[lo];
+        const double ell = dec.ell[lo];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int t = 32 * ti + 8 * (i >> 2) + 4 * hi + (i & 3);
-          const float f = dec.in[t];
-          acc[i] = where(f != 0.0f, acc[i] * f);
-          if (r.sums) {
-            const float all = over_32(acc[i] * s_e[t][32 * wv + lo]);
-            if (lo == 0) s_red[wv][t] = all;
-          }
+          const int s = 8 * (i >> 2) + 4 * hi + (i & 3);
+          const float f = exp_of(ell - dec.ell[s]) * r.score;
+          p[i] = where((s <= lo) & (s >= from), p[i] * f);
         }
-        const f32x16 before = acc;
-        for (int si = 0; si <= ti; ++si)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(&s_p[32 * ti + lo][32 * si + 8 * j + 4 * hi]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc = mfma(a[e], s_v[32 * si + 8 * j + 4 * hi + e][32 * wv + lo], acc);
-          }
-        // a score of 0 times a value that is not finite is NaN: where an output is not
-        // finite, its steps are added one by one, those that it sees only
-        float worst = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) worst = fmaf(acc[i], 0.0f, worst);
-        if (__any(worst != 0.0f)) {
-          acc = before;
-          for (int s = 0; s < 32 * (ti + 1); ++s) {
-            const float v = s_v[s][32 * wv + lo];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int t = 32 * ti + 8 * (i >> 2) + 4 * hi + (i & 3);
-              const float more = fmaf(s_p[t][s], v, acc[i]);
-              acc[i] = ((s <= t) & (s >= dec.from[t])) ? more : acc[i];
-            }
-          }
-        }
-        at.store<F32Io, Layout>(w, r, acc, 32 * ti, c0, n, col, hi);
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<f32x4*>(&s_p[lo][8 * i + 4 * hi]) = f32x4{p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]};
       }
-      if (r.sums) {
+      if (sums && wv == others) {
+#pragma unroll 4
+        for (int j = 0; j < kV; j += 8) {
+          const f32x4 a = *reinterpret_cast<const f32x4*>(&s_v[lo][j + 4 * hi]);
+          const f32x4 b = *reinterpret_cast<const f32x4*>(&s_e[lo][j + 4 * hi]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) u = mfma(a[e], b[e], u);
+        }
+      }
+      // what the state that enters gives
+      f32x16 acc = {};
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4 a = *reinterpret_cast<const f32x4*>(&s_q[lo][32 * kt + 8 * j + 4 * hi]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc = mfma(a[e], S[kt][4 * j + e], acc);
+        }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int t = 8 * (i >> 2) + 4 * hi + (i & 3);
+        const float f = dec.in[t];
+        acc[i] = where(f != 0.0f, acc[i] * f);
+        if (sums) {
+          const float all = over_32(acc[i] * s_e[t][32 * wv + lo]);
+          if (lo == 0) s_red[wv][t] = all;
+        }
+      }
+      __syncthreads();
+      if (sums && wv == others) {
+        const int from = dec.from[lo];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int s = 8 * (i >> 2) + 4 * hi + (i & 3);
+          sum += where((s < lo) & (s >= from), u[i] * s_p[lo][s]);
+        }
+        sum += __shfl_xor(sum, 32);
+        if (hi == 0) s_row[lo] = sum;
+      }
+      const f32x16 before = acc;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(&s_p[lo][8 * j + 4 * hi]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc = mfma(a[e], s_v[8 * j + 4 * hi + e][32 * wv + lo], acc);
+      }
+      // a score of 0 times a value that is not finite is NaN: where an output is not
+      // finite, its steps are added one by one, those that it sees only
+      float worst = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) worst = fmaf(acc[i], 0.0f, worst);
+      if (__any(worst != 0.0f)) {
+        acc = before;
+        for (int s = 0; s < C; ++s) {
+          const float value = s_v[s][32 * wv + lo];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int t = 8 * (i >> 2) + 4 * hi + (i & 3);
+            const float more = fmaf(s_p[t][s], value, acc[i]);
+            acc[i] = ((s <= t) & (s >= dec.from[t])) ? more : acc[i];
+          }
+        }
+      }
+      at.store<F32Io, Layout>(w, r, acc, 0, c0, n, col, hi);
+      if (sums) {
         __syncthreads();
         if (tid < n) {
-          float sum = 0.0f, both = 0.0f;
+          float sum = 0.0f;
 #pragma unroll
           for (int i = 0; i < NW; ++i) sum += s_red[i][tid];
-          for (int i = 0; i <= tid / 32; ++i) both += s_row[i][tid];
           float* to = r.sums + (static_cast<int64_t>(at.tile) * w.heads + at.head) * w.rows + at.begin + at.token(tid, c0, n);
           to[0] = sum;
-          to[static_cast<int64_t>(w.tiles) * w.heads * w.rows] = both;
+          to[static_cast<int64_t>(w.tiles) * w.heads * w.rows] = s_row[tid];
         }
       }
     }
@@ -209,24 +259,29 @@ __global__ __launch_bounds__(64 * NW, 1) void walk_f32_kernel(MixCall w) {
   at.leave_state<Layout>(w, r, S, gone, col, hi);
 }
 
-template <int KT, int NW, int CT>
+template <int KT, int NW>
 hipError_t launch(const MixCall& w, hipStream_t stream) {
-  hipLaunchKernelGGL((walk_f32_kernel<KT, NW, CT>), dim3(static_cast<unsigned>(walk_units(w))), dim3(64 * NW), 0,
-                     stream, w);
+  bool sums = false;
+  for (int k = 0; k < w.roles; ++k) sums |= w.role[k].sums != nullptr && !w.role[k].local;
+  const dim3 grid(static_cast<unsigned>(walk_units(w)));
+  if (sums)
+    hipLaunchKernelGGL((walk_f32_kernel<KT, NW, true>), grid, dim3(64 * NW), 0, stream, w);
+  else
+    hipLaunchKernelGGL((walk_f32_kernel<KT, NW, false>), grid, dim3(64 * NW), 0, stream, w);
   return hipGetLastError();
+}
+
+template <int KT>
+hipError_t by_values(const MixCall& w, hipStream_t stream) {
+  // (two waves hold 64 channels, but with a state of 256 rows too few registers)
+  return KT < 8 && value_width(w.role[0].V) == 64 ? launch<KT, KT < 8 ? 2 : 4>(w, stream) : launch<KT, 4>(w, stream);
 }
 
 }  // namespace
 
-hipError_t launch_walk_f32(const MixCall& w, int chunk, hipStream_t stream) {
-  const int kt = key_tiles(w.role[0].K), nw = value_width(MAMBA_F32, w.role[0].K, w.role[0].V) / 32;
-  if (kt == 8) return launch<8, 2, 1>(w, stream);
-  if (chunk == 32) {
-    if (kt == 2) return nw == 2 ? launch<2, 2, 1>(w, stream) : launch<2, 4, 1>(w, stream);
-    return nw == 2 ? launch<4, 2, 1>(w, stream) : launch<4, 4, 1>(w, stream);
-  }
-  if (kt == 2) return nw == 2 ? launch<2, 2, 2>(w, stream) : launch<2, 4, 2>(w, stream);
-  return nw == 2 ? launch<4, 2, 2>(w, stream) : launch<4, 4, 2>(w, stream);
+hipError_t launch_walk_f32(const MixCall& w, hipStream_t stream) {
+  const int kt = key_tiles(w.role[0].K);
+  return kt == 2 ? by_values<2>(w, stream) : kt == 4 ? by_values<4>(w, stream) : by_values<8>(w, stream);
 }
 
 }  // namespace mscan

@@ -6,14 +6,10 @@
 
 namespace mscan {
 
-// 32-row tiles of a workgroup's state, and its value channels. (With 8 tiles, 128
-// registers of state, the float32 kernel has registers for two waves only.)
+// 32-row tiles of a workgroup's state, and its value channels.
 inline int key_tiles(int64_t K) { return K <= 64 ? 2 : K <= 128 ? 4 : 8; }
-inline int value_width(int io, int64_t K, int64_t V) { return V <= 64 || (io == MAMBA_F32 && key_tiles(K) == 8) ? 64 : 128; }
-inline int value_tiles(int io, int64_t K, int64_t V) {
-  const int width = value_width(io, K, V);
-  return static_cast<int>((V + width - 1) / width);
-}
+inline int value_width(int64_t V) { return V <= 64 ? 64 : 128; }
+inline int value_tiles(int64_t V) { return static_cast<int>((V + value_width(V) - 1) / value_width(V)); }
 inline int64_t walk_units(const MixCall& w) { return w.slots * w.heads * w.tiles * w.roles; }
 
 // Sum over the 32 lanes of a half wave, in each of them.
@@ -184,7 +180,7 @@ struct Walk {
   }
 };
 
-hipError_t launch_walk_f32(const MixCall& w, int chunk, hipStream_t stream);
+hipError_t launch_walk_f32(const MixCall& w, hipStream_t stream);
 hipError_t launch_walk_bf16(const MixCall& w, hipStream_t stream);
 
 }  // namespace mscan
