@@ -2,7 +2,7 @@
 // and its backward.
 //
 // Bound by HBM: every element is read once and written once (16384 tokens of 48 heads of
-// 128 bf16: 86 us, 4.7 TB/s; the gradients of 40 heads 112 us, 4.5 TB/s). A head's row is D / 8
+// 128 bf16: 86 us, 4.7 TB/s; the gradients of 40 heads 118 us, 4.3 TB/s). A head's row is D / 8
 // lanes of 8 channels each, chosen so that a lane holds whole pairs: four
 // channels i and the four rotary / 2 further on, or eight neighbours (interleaved
 // pairs, and channels that are not turned). The row's sums go over those lanes, the
@@ -134,8 +134,9 @@ __device__ __forceinline__ float rstd_of(float ms, float eps) { return 1.0f / sq
 
 // A wave takes `each` heads of one token at a time, 64 / LP of them side by side, one row per
 // lane in flight. (Rows loaded two, three and four ahead cost registers and with them waves:
-// 89 us became 94, 94 and 98, and 194 for a training step 266, 277 and 285. So did fewer
-// registers by spilling. INTER as a run-time choice took 97 and 213.)
+// 89 us became 94, 94 and 98, and 194 for a training step 266, 277 and 285. INTER as a
+// run-time choice took 97 and 213. Queries and keys in workgroups of their own need fewer
+// registers, one weight's, but took 91 and 207: a token's rows are no longer read together.)
 template <class IO, bool INTER>
 __global__ __launch_bounds__(kThreads) void qknorm_fwd_kernel(QkNormProblem p, int LP, int each, int64_t units, int parts) {
   using raw = typename IO::raw;
