@@ -13,7 +13,9 @@
  * g is the log of the decay, per token and head or one per head
  * (MAMBA_LINATTN_HEAD_DECAY). g <= -104, -inf included, is a decay that float32
  * holds as 0: the state before such a token is dropped, whatever it is, so that
- * the token starts anew. g > 0 makes the state grow, until it overflows.
+ * the token starts anew. g > 0 makes the state grow, until it overflows; where a sum
+ * of them passes 88 the factor is infinite, also for a state of zeros, which is
+ * NaN then.
  *
  * A token's values reach the outputs of its own and later tokens of its
  * sequence and no other's, non-finite ones too; within one sequence they reach
