@@ -74,8 +74,10 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk
 // marks and head: its waves form their chunks' sums side by side, and the first terms
 // follow from those. Bound by latency (8 x 2048 steps of 20 heads of 128 x 128: 31 us, of
 // which the 45 MB at a copy's rate are 9; 81 with the states' product read across their
-// rows and each chunk's sums loaded when they were needed).
-constexpr int kDecayThreads = 256;
+// rows and each chunk's sums loaded when they were needed). With 256, 512 and 1024 threads a
+// training step of that size takes 520, 516 and 516 us, one of 881 packed steps of 6 heads
+// of 40 x 72 in fp32 131, 126 and 126.
+constexpr int kDecayThreads = 512;
 
 struct DecayGrad {
   MixCall w;                 // sequences; per is not used
@@ -408,19 +410,27 @@ hipError_t zero_rest(const RestRows& z, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Workgroups of the backward's three runs for each sequence.
-int64_t bwd_walks(const LinattnSizes& n) { return n.heads * (value_tiles(n.V) + 2 * value_tiles(n.K)); }
+// The backward's three runs go in one launch if their operands have one shape: they are the
+// same rows. Else dv's is one and that of dk and dq another, each with segments of its own
+// (forward and backward of 4 x 1000 steps of 32 heads of 64 x 128 take 260 us, with segments
+// as for one launch of all 290).
+bool one_shape(const LinattnSizes& n) {
+  return key_tiles(n.K) == key_tiles(n.V) && value_width(n.V) == value_width(n.K) && value_tiles(n.V) == value_tiles(n.K);
+}
+int dv_per(const LinattnSizes& n) { return per_of(n, n.heads * value_tiles(n.V) * (one_shape(n) ? 3 : 1)); }
+int dk_dq_per(const LinattnSizes& n) { return per_of(n, n.heads * value_tiles(n.K) * (one_shape(n) ? 3 : 2)); }
 
 // The backward's workspace.
 struct BwdBytes {
-  SegmentBytes seg;
+  SegmentBytes dv, dk_dq;
   size_t marks, a, b, last, part, parts;
   int64_t mark_slots;
-  size_t total() const { return 3 * seg.total() + 2 * marks + a + b + last + 2 * part + parts; }
+  size_t total() const { return dv.total() + 2 * dk_dq.total() + 2 * marks + a + b + last + 2 * part + parts; }
 };
 BwdBytes bwd_bytes(const LinattnSizes& n, bool head_decay) {
   BwdBytes s;
-  s.seg = segment_bytes(n, per_of(n, bwd_walks(n)));
+  s.dv = segment_bytes(n, dv_per(n));
+  s.dk_dq = segment_bytes(n, dk_dq_per(n));
   s.mark_slots = slots_of(n.rows, n.batch, kMarkSteps);
   s.marks = r256(static_cast<size_t>(s.mark_slots) * n.heads * n.K * n.V * 4);
   s.a = r256(static_cast<size_t>(2 * value_tiles(n.V)) * n.heads * n.rows * 4);
@@ -515,9 +525,6 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
   };
   if (n.batch > 0) {
     MixCall w = call_of(f);
-    const int per = per_of(n, bwd_walks(n));
-    set_segments(w, n, per);
-    const bool cut = work && split(n, per);
     const int share = static_cast<int>(n.heads / n.groups), K = static_cast<int>(n.K), V = static_cast<int>(n.V);
     // dv: queries k, keys q, values dout, in reverse; the state is dS (K x V)
     MixRole dv{};
@@ -571,8 +578,10 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
     dq.reverse = false;
     dq.score = dq.from = f.scale;
     dq.to = 1.0f;
-    if (cut)
-      for (MixRole* r : {&dv, &dk, &dq}) give_segments(*r, s.seg, at);
+    const bool cut_dv = work && split(n, dv_per(n)), cut_dk_dq = work && split(n, dk_dq_per(n));
+    if (cut_dv) give_segments(dv, s.dv, at);
+    if (cut_dk_dq)
+      for (MixRole* r : {&dk, &dq}) give_segments(*r, s.dk_dq, at);
     DecayGrad d{};
     if (work && p.dg) {
       dv.e = f.v;
@@ -602,22 +611,21 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
       dq.part = take(s.part);
       dk.part = take(s.part);
     }
-    // roles of the same shape go in one launch: their operands are the same rows
-    const bool same = key_tiles(K) == key_tiles(V) && value_width(V) == value_width(K) &&
-                      value_tiles(V) == value_tiles(K);
+    set_segments(w, n, dv_per(n));
     w.role[0] = dv;
     w.roles = 1;
-    if (same) {
+    if (one_shape(n)) {
       w.role[1] = dk;
       w.role[2] = dq;
       w.roles = 3;
     }
-    if ((e = run(w, n, cut, stream)) != hipSuccess) return e;
-    if (!same) {
+    if ((e = run(w, n, cut_dv, stream)) != hipSuccess) return e;
+    if (!one_shape(n)) {
+      set_segments(w, n, dk_dq_per(n));
       w.role[0] = dk;
       w.role[1] = dq;
       w.roles = 2;
-      if ((e = run(w, n, cut, stream)) != hipSuccess) return e;
+      if ((e = run(w, n, cut_dk_dq, stream)) != hipSuccess) return e;
     }
     if (work && share > 1) {
       GroupSum gs{};
