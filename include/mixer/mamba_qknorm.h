@@ -22,7 +22,10 @@
  * Conventions as in mamba_scan.h and block/mamba_norm.h: io tensors are float32 or
  * bfloat16, weights, freqs and the weights' gradients float32, arithmetic
  * float32; non-finite values propagate within their head's row (in the backward
- * the row is NaN). Results are deterministic.
+ * the row is NaN). Sums of squares are float32 ones: a head whose sum is above their
+ * range (values of 1e19 and more) has rstd 0 as an infinite one has. With eps 0 a
+ * head of zeros has no norm and is NaN, and one whose squares are all below the range
+ * (values of 1e-23 and less) has an infinite rstd. Results are deterministic.
  */
 #ifndef MAMBA_QKNORM_H
 #define MAMBA_QKNORM_H

@@ -398,6 +398,17 @@ def test_norm_and_rotation_rows_of_zeros():
     assert d["dq_weight"].isfinite().all() and d["dk_weight"].isfinite().all()
 
 
+@pytest.mark.parametrize("io", [F32, BF])
+def test_norm_and_rotation_ends_of_the_range(io):
+    q, k, pos, freqs, wq, wk, dy, dz = turn_case(6, 3, 2, 1, 40, 16, None, io)
+    q[0, 0], q[1, 0], q[2, 0] = 0.0, 1e-24, 1e20
+    y, _ = qk_norm_rope_fwd(q, k, pos, freqs, wq, wk, eps=0.0)
+    assert y[0, 0].isnan().all() and y[1, 0].isinf().any() and not y[2, 0].any()
+    assert y[:, 1].isfinite().all()
+    y, _ = qk_norm_rope_fwd(q, k, pos, freqs, wq, wk)
+    assert not y[0, 0].any() and y[1, 0].isfinite().all()
+
+
 def layer(rows, pos, freqs, wq, wk, g, dims, offsets=None, h0=None):
     H, K, V = dims
     q, k = rows[..., :H * K].unflatten(-1, (H, K)), rows[..., H * K:2 * H * K].unflatten(-1, (H, K))
