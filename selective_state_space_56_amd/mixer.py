@@ -79,10 +79,10 @@ def _heads(t, name, shape, dtype, dev):
     layouts are recognised without a walk over the axes."""
     if t is None:
         return 0
-    heads, size = shape[-2:]
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev:
         if t.is_contiguous():
             return 0
+        heads, size = shape[-2:]
         step = t.stride()
         row = step[-3]
         if (step[-1] == 1 and step[-2] == size and row >= heads * size and heads > 1
@@ -90,7 +90,7 @@ def _heads(t, name, shape, dtype, dev):
             return row
     s = _row_stride(t, name, shape, dtype, dev, len(shape) - 3)
     # rows apart by less than a row's length share elements
-    if s < heads * size and t.numel():
+    if s < shape[-2] * shape[-1] and t.numel():
         raise ValueError(f"{name}: rows overlap")
     return s
 
