@@ -19,7 +19,7 @@
 // the channels go along its registers, and its outputs leave four at a time. Operands
 // whose k is the step come from LDS by the transposing load.
 //
-// Bound by issue: 8 x 2048 steps of 40 heads of 128 x 128 take 245 us, 2.7 TB/s of 5.3 that
+// Bound by issue: 8 x 2048 steps of 40 heads of 128 x 128 take 237 us, 2.9 TB/s of 5.3 that
 // a copy reaches. The matrix products alone would take 67 us of them; splitting the state
 // and the weighted values into parts, the scores' factors and LDS take the rest, and the
 // vector and matrix instructions of a compute unit's eight waves hardly overlap. So the
@@ -344,12 +344,13 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
 #pragma unroll
               for (int m = 0; m < kParts; ++m) part[m][e] = words[m];
             }
+            u32x4 b[kTT];
 #pragma unroll
-            for (int t = 0; t < kTT; ++t) {
-              const u32x4 b = row8(&s_q[32 * t + lo][k0 + 32 * kt + 16 * j + 8 * hi]);
+            for (int t = 0; t < kTT; ++t) b[t] = row8(&s_q[32 * t + lo][k0 + 32 * kt + 16 * j + 8 * hi]);
 #pragma unroll
-              for (int m = 0; m < kParts; ++m) acc[t] = mfma(part[m], b, acc[t]);
-            }
+            for (int m = 0; m < kParts; ++m)
+#pragma unroll
+              for (int t = 0; t < kTT; ++t) acc[t] = mfma(part[m], b[t], acc[t]);
           }
         const bool cut = __builtin_amdgcn_readfirstlane(dec.cut);
 #pragma unroll
@@ -537,11 +538,18 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
 #pragma unroll
         for (int m = 0; m < 3; ++m) part[m][e] = words[m];
       }
+      // products that follow one another go to different tiles, here and above (to one tile its
+      // parts' three in a row: prompts 244 us instead of 237)
+      constexpr int kSide = KT < 4 ? KT : 4;
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        const u32x4 a = column8<true>(&s_k[16 * j][k0 + 32 * kt], ldk, lane);
+      for (int kt = 0; kt < KT; kt += kSide) {
+        u32x4 a[kSide];
 #pragma unroll
-        for (int m = 0; m < 3; ++m) S[kt] = mfma(a, part[m], S[kt]);
+        for (int i = 0; i < kSide; ++i) a[i] = column8<true>(&s_k[16 * j][k0 + 32 * (kt + i)], ldk, lane);
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+#pragma unroll
+          for (int i = 0; i < kSide; ++i) S[kt + i] = mfma(a[i], part[m], S[kt + i]);
       }
     }
     gone.add(dec.cut, dec.total);
