@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk
 // leave. The first term goes from chunk to chunk, <S_out, dS_out> - sum a + sum b,
 // and is formed anew from the states at every mark. One workgroup per stretch between
 // marks and head: its waves form their chunks' sums side by side, and the first terms
-// follow from those. Bound by latency (8 x 2048 steps of 20 heads of 128 x 128: 31 us, of
+// follow from those. Bound by latency (8 x 2048 steps of 20 heads of 128 x 128: 24 us, of
 // which the 45 MB at a copy's rate are 9; 81 with the states' product read across their
 // rows and each chunk's sums loaded when they were needed). With 256, 512 and 1024 threads a
 // training step of that size takes 520, 516 and 516 us, one of 881 packed steps of 6 heads

@@ -19,7 +19,7 @@
 // the channels go along its registers, and its outputs leave four at a time. Operands
 // whose k is the step come from LDS by the transposing load.
 //
-// Bound by issue: 8 x 2048 steps of 40 heads of 128 x 128 take 237 us, 2.9 TB/s of 5.3 that
+// Bound by issue: 8 x 2048 steps of 40 heads of 128 x 128 take 235 us, 2.9 TB/s of 5.3 that
 // a copy reaches. The matrix products alone would take 67 us of them; splitting the state
 // and the weighted values into parts, the scores' factors and LDS take the rest, and the
 // vector and matrix instructions of a compute unit's eight waves hardly overlap. So the
