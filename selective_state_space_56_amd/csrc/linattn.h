@@ -36,7 +36,7 @@ struct MixRole {
   const float* s0;       // the state that enters a sequence, (batch, heads, K, V), or null
   const float* enter;    // the states that enter later segments, (slots, heads, K, V), or null
   float* last;           // (batch, heads, K, V) or null
-  float* marks;          // states at every kMarkSteps steps, (slots, heads, K, V), or null
+  float* marks;          // states at every kMarkSteps steps, (marks, heads, K, V), or null
   float* sums;           // (2, value tiles, heads, rows) or null: for each step t, e_t . what S_in gives
                          // of o_t, and sum_{s < t} of score (s, t) times e_t . v_s
   float* local;          // a segment's own state, (slots, heads, K, V), instead of outputs; or null
@@ -58,8 +58,12 @@ struct MixCall {
   uint32_t together;       // consecutive workgroups that read the same rows
 };
 
-// Steps between two marks: where the gradients of the decays start anew.
+// Steps between two marks: where the gradients of the decays start anew. Mark p >= 1 of a
+// sequence, p kMarkSteps steps into it, is the mark_of-th of all: a sequence's last one lies
+// before its end, and so its number below the next one's first.
 constexpr int kMarkSteps = 1024;
+__device__ __forceinline__ int64_t mark_of(int64_t begin, int64_t p) { return static_cast<uint32_t>(begin) / kMarkSteps + p; }
+inline int64_t marks_of(int64_t rows) { return rows / kMarkSteps + 1; }
 
 // Where a sequence lies. Offsets are read as they are found on the device, held
 // to 0 .. rows.

@@ -83,8 +83,8 @@ struct DecayGrad {
   MixCall w;                 // sequences; per is not used
   const float* a;            // (2, atiles, heads, rows): a, c
   const float* b;            // (2, btiles, heads, rows): b, d
-  const float* marks;        // (slots, heads, V, K): states
-  const float* dmarks;       // (slots, heads, K, V): their gradients
+  const float* marks;        // (marks, heads, V, K): states
+  const float* dmarks;       // (marks, heads, K, V): their gradients
   const float* last;         // (batch, heads, V, K) or null
   const float* dlast;        // (batch, heads, K, V) or null
   float* dg;                 // (rows, heads), or null:
@@ -120,8 +120,9 @@ __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) 
   const int count = static_cast<int>(begin + kMark < chunks ? kMark : chunks - begin);
   // <S, dS> at the stretch's end; S is there by value channels
   const int64_t size = static_cast<int64_t>(p.K) * p.V;
-  const float* S = p.marks + ((slot + 1) * w.heads + head) * size;
-  const float* dS = p.dmarks + ((slot + 1) * w.heads + head) * size;
+  const int64_t mark = mark_of(s.begin, m + 1) * w.heads + head;
+  const float* S = p.marks + mark * size;
+  const float* dS = p.dmarks + mark * size;
   if (begin + count == chunks) {
     S = p.last ? p.last + (static_cast<int64_t>(seq) * w.heads + head) * size : nullptr;
     dS = p.dlast ? p.dlast + (static_cast<int64_t>(seq) * w.heads + head) * size : nullptr;
@@ -424,20 +425,20 @@ int dk_dq_per(const LinattnSizes& n) { return per_of(n, n.heads * value_tiles(n.
 struct BwdBytes {
   SegmentBytes dv, dk_dq;
   size_t marks, a, b, last, part, parts;
-  int64_t mark_slots;
+  int64_t stretches;
   size_t total() const { return dv.total() + 2 * dk_dq.total() + 2 * marks + a + b + last + 2 * part + parts; }
 };
 BwdBytes bwd_bytes(const LinattnSizes& n, bool head_decay) {
   BwdBytes s;
   s.dv = segment_bytes(n, dv_per(n));
   s.dk_dq = segment_bytes(n, dk_dq_per(n));
-  s.mark_slots = slots_of(n.rows, n.batch, kMarkSteps);
-  s.marks = r256(static_cast<size_t>(s.mark_slots) * n.heads * n.K * n.V * 4);
+  s.stretches = slots_of(n.rows, n.batch, kMarkSteps);
+  s.marks = r256(static_cast<size_t>(marks_of(n.rows)) * n.heads * n.K * n.V * 4);
   s.a = r256(static_cast<size_t>(2 * value_tiles(n.V)) * n.heads * n.rows * 4);
   s.b = r256(static_cast<size_t>(2 * value_tiles(n.K)) * n.heads * n.rows * 4);
   s.last = r256(static_cast<size_t>(n.batch) * n.heads * n.K * n.V * 4);
   s.part = n.heads == n.groups ? 0 : r256(static_cast<size_t>(n.rows) * n.heads * n.K * 4);
-  s.parts = head_decay ? r256(static_cast<size_t>(s.mark_slots) * n.heads * 4) : 0;
+  s.parts = head_decay ? r256(static_cast<size_t>(s.stretches) * n.heads * 4) : 0;
   return s;
 }
 
@@ -651,13 +652,13 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (work && p.dg) {
-      const dim3 grid(static_cast<unsigned>(s.mark_slots * n.heads));
+      const dim3 grid(static_cast<unsigned>(s.stretches * n.heads));
       if (chunk_of(n) == 64)
         hipLaunchKernelGGL((decay_grad_kernel<64>), grid, dim3(kDecayThreads), 0, stream, d);
       else
         hipLaunchKernelGGL((decay_grad_kernel<32>), grid, dim3(kDecayThreads), 0, stream, d);
       if ((e = hipGetLastError()) != hipSuccess) return e;
-      if (f.head_decay) return launch_colsum(d.parts, s.mark_slots, n.heads, StoreFlat{p.dg}, stream);
+      if (f.head_decay) return launch_colsum(d.parts, s.stretches, n.heads, StoreFlat{p.dg}, stream);
     }
   }
   // no tokens: a decay that every token shares has the gradient 0

@@ -143,7 +143,7 @@ struct Walk {
                                              int part, int row0 = 0) const {
     const int between = reverse ? c + 1 : c, mark = kMarkSteps / C;
     if (!r.marks || between == 0 || between >= chunks || between % mark) return;
-    const int64_t at = first_slot(begin, seq, kMarkSteps) + between / mark;
+    const int64_t at = mark_of(begin, between / mark);
     write<L>(r, r.marks + (at * w.heads + head) * r.K * r.V, S, col, part, row0);
   }
 

@@ -187,6 +187,14 @@ def test_workspace(lib):
         assert call(lib, d, ws=10, ws_bytes=need, **far) == INVALID and "overlaps" in err(lib)
 
 
+def test_workspace_of_many_short_sequences(lib):
+    # one state for each, and little beside it: no states between stretches of sequences this short
+    d = ld(batch=4096, seqlen=64, heads=4, groups=4, K=128, V=128)
+    states = 4096 * 4 * 128 * 128 * 4
+    assert states <= lib.mamba_linattn_bwd_workspace_size(ref(d)) < 1.2 * states
+    assert lib.mamba_linattn_workspace_size(ref(d)) == 0
+
+
 def test_nothing_to_do(lib):
     for call in (fwd, bwd):
         assert call(lib, ld(batch=0), q=None) == 0

@@ -62,6 +62,14 @@ def test_many_short_sequences(io):
     check(make(51, (sum(lens),), 2, 1, 24, 16, io, states=len(lens)), offsets=off)
 
 
+@pytest.mark.parametrize("io", [F32, BF])
+def test_long_packed_sequences(io):
+    # several with states between stretches of 1024 steps, ends on both sides of a stretch's
+    lens = [1030, 1024, 2049, 1025, 5]
+    off = torch.tensor([3 + sum(lens[:i]) for i in range(len(lens) + 1)], device="cuda")
+    check(make(58, (int(off[-1]) + 2,), 2, 1, 16, 24, io, states=len(lens)), offsets=off)
+
+
 @pytest.mark.parametrize("seed", range(16))
 def test_drawn_shapes(seed):
     rnd = random.Random(seed)
