@@ -13,6 +13,8 @@
 // the running sum before the step.
 #pragma once
 
+#include <stddef.h>
+
 #include "block_math.h"
 #include "mamba_scan.h"
 #include "mixer.h"
@@ -106,8 +108,10 @@ __device__ __forceinline__ int sequence_at(const int64_t* offsets, int batch, in
 // are float64: among large decays the differences of float32 sums would lose the
 // small ones (at 6400, half a step is 2^-12). A decay of 0 is no summand but cuts:
 // step t sees steps s >= from[t] only. Steps past the chunk's end add nothing.
+// (Aligned for the 16-byte reads of `down` and `end`, also where two of them follow each
+// other in LDS.)
 template <int C>
-struct Decays {
+struct alignas(16) Decays {
   double ell[C];
   float in[C];     // of S_in in o_t, times `from`; 0 where a cut lies between
   float end[C];    // of a step in S_out, times `to`; 0 where a cut lies between
@@ -120,6 +124,9 @@ struct Decays {
   int cut;         // whether there is one
   double total;    // the sum of the others
 };
+static_assert(sizeof(Decays<32>) % 16 == 0 && offsetof(Decays<32>, down) % 16 == 0 && offsetof(Decays<32>, end) % 16 == 0 &&
+                  sizeof(Decays<64>) % 16 == 0 && offsetof(Decays<64>, down) % 16 == 0 && offsetof(Decays<64>, end) % 16 == 0,
+              "read 16 bytes at a time");
 
 // e^v for the difference of two sums; the float32 argument is off by 2^-24 of |v|
 __device__ __forceinline__ float exp_of(double v) { return hw_exp2(static_cast<float>(v) * kLog2e); }
