@@ -160,29 +160,30 @@ __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) 
     for (int k0 = 0; k0 < p.K; k0 += kBlock)
       for (int v0 = 0; v0 < p.V; v0 += kBlock) {
         constexpr int kPieces = kBlock * kBlock / 4 / kDecayThreads;
-        float4 u[kPieces], t[kPieces];
+        // (dlast lies at 4-byte alignment)
+        Words<float, 4, 4> u[kPieces], t[kPieces];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
           const int r = (tid + i * kDecayThreads) / (kBlock / 4), c = (tid + i * kDecayThreads) % (kBlock / 4) * 4;
-          u[i] = t[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          u[i] = t[i] = Words<float, 4, 4>{};
           if (k0 + r < p.K && v0 + c < p.V)
-            u[i] = *reinterpret_cast<const float4*>(dS + static_cast<int64_t>(k0 + r) * p.V + v0 + c);
+            u[i] = *reinterpret_cast<const Words<float, 4, 4>*>(dS + static_cast<int64_t>(k0 + r) * p.V + v0 + c);
           if (v0 + r < p.V && k0 + c < p.K)
-            t[i] = *reinterpret_cast<const float4*>(S + static_cast<int64_t>(v0 + r) * p.K + k0 + c);
+            t[i] = *reinterpret_cast<const Words<float, 4, 4>*>(S + static_cast<int64_t>(v0 + r) * p.K + k0 + c);
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
           const int r = (tid + i * kDecayThreads) / (kBlock / 4), c = (tid + i * kDecayThreads) % (kBlock / 4) * 4;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s_state[r][c + k] = (&u[i].x)[k];
+          for (int k = 0; k < 4; ++k) s_state[r][c + k] = u[i][k];
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
           const int r = (tid + i * kDecayThreads) / (kBlock / 4), c = (tid + i * kDecayThreads) % (kBlock / 4) * 4;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) dot += static_cast<double>(s_state[c + k][r]) * (&t[i].x)[k];
+          for (int k = 0; k < 4; ++k) dot += static_cast<double>(s_state[c + k][r]) * t[i][k];
         }
       }
   dot = over_wave(dot);
