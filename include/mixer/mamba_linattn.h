@@ -127,7 +127,11 @@ mamba_status mamba_linattn_fwd(const mamba_linattn_desc *desc,
  *   dq_t = scale S_t dout_t     dk_t = dS_t v_t     dv_t = dS_t^T k_t
  *   dg_t = exp(g_t) <dS_t, S_{t-1}>                 dh0 = exp(g_0) dS_0
  * dq and dk are sums over the heads of a group, rounded once; dg is a sum over
- * all tokens with HEAD_DECAY. A decay of 0 gets a zero gradient.
+ * all tokens with HEAD_DECAY. A decay of 0 gets a zero gradient. dg_t is added up
+ * from terms of its own, in float32 states and products and float64 sums: its error
+ * goes by the magnitudes of what crosses token t, not by other tokens' gradients,
+ * however large these are. For it the workspace takes the states at every 64 tokens
+ * (bfloat16) or 32 (float32), twice.
  *   q, k, v, g, h0, offsets : as given to the forward.
  *   dout       : (rows, H, V) io dtype.
  *   dlast      : (batch, H, K, V) float32 or NULL (zero).

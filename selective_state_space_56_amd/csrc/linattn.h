@@ -38,9 +38,10 @@ struct MixRole {
   const float* s0;       // the state that enters a sequence, (batch, heads, K, V), or null
   const float* enter;    // the states that enter later segments, (slots, heads, K, V), or null
   float* last;           // (batch, heads, K, V) or null
-  float* marks;          // states at every kMarkSteps steps, (marks, heads, K, V), or null
-  float* sums;           // (2, value tiles, heads, rows) or null: for each step t, e_t . what S_in gives
-                         // of o_t, and sum_{s < t} of score (s, t) times e_t . v_s
+  float* entering;       // the state that enters each chunk, (chunk slots, heads, entering_size), or null
+  float* sums;           // (value tiles, heads, rows) or null: for each step t, e_t . what S_in gives of o_t
+  float* pairs;          // with it, the same shape, or null: for each step t, what crosses it of the chunk's
+                         // own pairs, sum_{s < t <= u} of score (s, u) times e_u . v_s
   float* local;          // a segment's own state, (slots, heads, K, V), instead of outputs; or null
   float* gone;           // with it: the segment's whole decay, (slots, heads)
   bool s0_turned;        // s0 is (.., V, K)
@@ -60,12 +61,8 @@ struct MixCall {
   uint32_t together;       // consecutive workgroups that read the same rows
 };
 
-// Steps between two marks: where the gradients of the decays start anew. Mark p >= 1 of a
-// sequence, p kMarkSteps steps into it, is the mark_of-th of all: a sequence's last one lies
-// before its end, and so its number below the next one's first.
-constexpr int kMarkSteps = 1024;
-__device__ __forceinline__ int64_t mark_of(int64_t begin, int64_t p) { return static_cast<uint32_t>(begin) / kMarkSteps + p; }
-inline int64_t marks_of(int64_t rows) { return rows / kMarkSteps + 1; }
+// Elements of a state as the runs leave it for each chunk: whole tiles of 32 x 32.
+inline int64_t entering_size(int64_t K, int64_t V) { return (K + 31) / 32 * ((V + 31) / 32) * 1024; }
 
 // Where a sequence lies. Offsets are read as they are found on the device, held
 // to 0 .. rows.
@@ -136,6 +133,11 @@ __device__ __forceinline__ float exp_exactly(double v) {
   const double whole = rint(v2 < -400.0 ? -400.0 : v2 > 400.0 ? 400.0 : v2);
   return ldexpf(hw_exp2(static_cast<float>(v2 - whole)), static_cast<int>(whole));
 }
+
+// Whether the product of the states that a chunk's steps lie between has a part in the gradients of its
+// decays: not across a cut, nor where the decays between leave nothing in float32. `slack` (> 0) lets
+// what stores the states reach further than what reads them, whose sums are not the same bits.
+__device__ __forceinline__ bool passes(bool cut, double total, double slack = 0.0) { return !cut && !(total < -110.0 - slack); }
 
 // Returns `all`.
 template <int C>

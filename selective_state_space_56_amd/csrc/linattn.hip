@@ -62,34 +62,32 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk
 }
 
 // ---------------------------------------------------------------------------
-// Gradients of the decays. For step t of a chunk, with what the two runs' sums
-// hold (a_s = end_s k_s . (dS_out v_s), b_u = in_u scale q_u . (S_in dout_u), and of the
-// chunk's own pairs c_s, those that later steps make with s, and d_u, those that u makes
-// with earlier ones):
-//   dg_t = e^{ell_C} <S_in, dS_out> + sum_{s < t} a_s + sum_{u >= t} (b_u + d_u - c_u)
-// Every term is of the size of the result: the difference of q . dq and k . dk
-// summed from the sequence's end, which is the same, would lose what strong decays
-// leave. The first term goes from chunk to chunk, <S_out, dS_out> - sum a + sum b,
-// and is formed anew from the states at every mark. One workgroup per stretch between
-// marks and head: its waves form their chunks' sums side by side, and the first terms
-// follow from those. Bound by latency (8 x 2048 steps of 20 heads of 128 x 128: 24 us, of
-// which the 45 MB at a copy's rate are 9; 81 with the states' product read across their
-// rows and each chunk's sums loaded when they were needed). With 256, 512 and 1024 threads a
-// training step of that size takes 520, 516 and 516 us, one of 881 packed steps of 6 heads
-// of 40 x 72 in fp32 131, 126 and 126.
-constexpr int kDecayThreads = 512;
+// Gradients of the decays. dg_t is the sum of what crosses step t of a chunk,
+//   dg_t = e^{ell_C} <S_in, dS_out> + sum_{s < t} a_s + sum_{u >= t} b_u + pairs_t
+// with what the runs leave: the state S_in that enters the chunk and the gradient dS_out of the one
+// that leaves it (dq's and dk's run, as V x K both), a_s = end_s k_s . (dS_out v_s),
+// b_u = in_u scale q_u . (S_in dout_u), and the chunk's own pairs that t lies between. Every term is a part of
+// dg_t itself and none is subtracted: the difference of q . dq and k . dk summed from the
+// sequence's end, which is the same, or a product <S, dS> carried from chunk to chunk, leaves the
+// rounding of what other tokens add, which is more than strong decays, early tokens or small
+// gradients before large ones leave of dg_t.
+constexpr int kDecayThreads = 256;
+constexpr int kDecayAhead = 2;               // 16-byte pieces of each state in flight per thread
+constexpr int64_t kDecayGroups = int64_t(1) << 16;  // workgroups at most; each takes every kDecayGroups-th chunk and head
 
 struct DecayGrad {
   MixCall w;                 // sequences; per is not used
-  const float* a;            // (2, atiles, heads, rows): a, c
-  const float* b;            // (2, btiles, heads, rows): b, d
-  const float* marks;        // (marks, heads, V, K): states
-  const float* dmarks;       // (marks, heads, K, V): their gradients
-  const float* last;         // (batch, heads, V, K) or null
-  const float* dlast;        // (batch, heads, K, V) or null
+  const float* a;            // (tiles, heads, rows)
+  const float* b;            // the same
+  const float* pairs;        // the same
+  const float* S;            // (chunk slots, heads, size), in one order of elements
+  const float* dS;           // the same
+  bool first, last;          // whether a state enters a sequence's first chunk, a gradient its last
   float* dg;                 // (rows, heads), or null:
-  float* parts;              // (slots, heads): sums over the stretch
-  int atiles, btiles, K, V;
+  float* parts;              // (chunk slots, heads): sums over the chunk
+  int64_t slots;
+  int tiles;
+  int64_t size;
 };
 
 // Sum over a wave, in each lane.
@@ -102,148 +100,83 @@ __device__ __forceinline__ double over_wave(double v) {
 template <int C>
 __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) {
   const MixCall& w = p.w;
-  constexpr int kMark = kMarkSteps / C, kWaves = kDecayThreads / 64, kEach = kMark / kWaves;
-  constexpr int kBlock = 64;  // channels of the states' product at a time, each way
-  __shared__ float s_state[kBlock][kBlock + 1];
-  __shared__ double s_sum[kWaves], s_a[kMark], s_b[kMark];
-  __shared__ int s_keeps[kMark];
+  constexpr int kWaves = kDecayThreads / 64;
+  __shared__ double s_sum[2][kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int head = blockIdx.x % w.heads;
-  const int64_t slot = blockIdx.x / w.heads;
-  const int seq = sequence_at(w.offsets, w.batch, w.seqlen, w.rows, kMarkSteps, slot);
-  const Sequence s = sequence_of(w.offsets, seq, w.seqlen, w.rows);
-  const int64_t chunks = (s.len + C - 1) / C, m = slot - first_slot(s.begin, seq, kMarkSteps), begin = m * kMark;
-  if (m < 0 || begin >= chunks) {  // (nothing of a sequence of no steps)
-    if (p.parts && tid == 0) p.parts[slot * w.heads + head] = 0.0f;
-    return;
-  }
-  const int count = static_cast<int>(begin + kMark < chunks ? kMark : chunks - begin);
-  // <S, dS> at the stretch's end; S is there by value channels
-  const int64_t size = static_cast<int64_t>(p.K) * p.V;
-  const int64_t mark = mark_of(s.begin, m + 1) * w.heads + head;
-  const float* S = p.marks + mark * size;
-  const float* dS = p.dmarks + mark * size;
-  if (begin + count == chunks) {
-    S = p.last ? p.last + (static_cast<int64_t>(seq) * w.heads + head) * size : nullptr;
-    dS = p.dlast ? p.dlast + (static_cast<int64_t>(seq) * w.heads + head) * size : nullptr;
-  }
-  // each wave's chunks: lane = step
-  float g[kEach];
-  double a[kEach], b[kEach];
-  bool on[kEach];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int64_t at = (begin + wave + i * kWaves) * C + lane;
-    on[i] = wave + i * kWaves < count && lane < C && at < s.len;
-    g[i] = on[i] ? w.g[(s.begin + at) * w.g_step + head] : 0.0f;
-    a[i] = b[i] = 0.0;
-  }
-  const int64_t first = head * w.rows + s.begin + (begin + wave) * C + lane, plane = static_cast<int64_t>(w.heads) * w.rows;
-  for (int k = 0; k < p.atiles; ++k)
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (on[i]) {
-        const float* from = p.a + k * plane + first + i * kWaves * C;
-        a[i] += from[0];
-        b[i] -= from[p.atiles * plane];
+  int turn = 0;
+  for (int64_t unit = blockIdx.x; unit < p.slots * w.heads; unit += gridDim.x) {
+    const int head = static_cast<int>(unit % w.heads);
+    const int64_t slot = unit / w.heads;
+    const int seq = sequence_at(w.offsets, w.batch, w.seqlen, w.rows, C, slot);
+    const Sequence s = sequence_of(w.offsets, seq, w.seqlen, w.rows);
+    const int64_t chunks = (s.len + C - 1) / C, c = slot - first_slot(s.begin, seq, C);
+    if (c < 0 || c >= chunks) {  // (a slot that no chunk has)
+      if (p.parts && tid == 0) p.parts[unit] = 0.0f;
+      continue;
+    }
+    // every wave for itself, a step per lane
+    const int64_t left = s.len - c * C, row = s.begin + c * C + lane;
+    const bool on = lane < C && lane < left;
+    const float g = on ? w.g[row * w.g_step + head] : 0.0f;
+    const bool cut = on && g <= kNoDecay;
+    const uint64_t cuts = __ballot(cut);
+    const double total = over_wave(cut ? 0.0 : static_cast<double>(g));
+    const bool through = passes(cuts != 0, total) && (c > 0 || p.first) && (c + 1 < chunks || p.last);
+    double a = 0.0, b = 0.0, pairs = 0.0;
+    if (wave == 0 && on) {
+      for (int k = 0; k < p.tiles; ++k) {
+        const int64_t at = (static_cast<int64_t>(k) * w.heads + head) * w.rows + row;
+        a += p.a[at];
+        b += p.b[at];
+        pairs += p.pairs[at];
       }
-  for (int k = 0; k < p.btiles; ++k)
+    }
+    double dot = 0.0;
+    if (through) {
+      const float* S = p.S + unit * p.size;
+      const float* dS = p.dS + unit * p.size;
+      for (int64_t e0 = 4 * tid; e0 < p.size; e0 += 4 * kDecayThreads * kDecayAhead) {
+        Words<float, 4, 16> x[kDecayAhead] = {}, y[kDecayAhead] = {};
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (on[i]) {
-        const float* from = p.b + k * plane + first + i * kWaves * C;
-        b[i] += from[0];
-        b[i] += from[p.btiles * plane];
+        for (int k = 0; k < kDecayAhead; ++k) {
+          const int64_t e = e0 + 4 * kDecayThreads * k;
+          if (e < p.size) {
+            x[k] = __builtin_nontemporal_load(reinterpret_cast<const Words<float, 4, 16>*>(S + e));
+            y[k] = __builtin_nontemporal_load(reinterpret_cast<const Words<float, 4, 16>*>(dS + e));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kDecayAhead; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dot = fma(static_cast<double>(x[k][i]), static_cast<double>(y[k][i]), dot);
       }
-  double dot = 0.0;
-  if (S && dS)
-    for (int k0 = 0; k0 < p.K; k0 += kBlock)
-      for (int v0 = 0; v0 < p.V; v0 += kBlock) {
-        constexpr int kPieces = kBlock * kBlock / 4 / kDecayThreads;
-        // (dlast lies at 4-byte alignment)
-        Words<float, 4, 4> u[kPieces], t[kPieces];
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int r = (tid + i * kDecayThreads) / (kBlock / 4), c = (tid + i * kDecayThreads) % (kBlock / 4) * 4;
-          u[i] = t[i] = Words<float, 4, 4>{};
-          if (k0 + r < p.K && v0 + c < p.V)
-            u[i] = *reinterpret_cast<const Words<float, 4, 4>*>(dS + static_cast<int64_t>(k0 + r) * p.V + v0 + c);
-          if (v0 + r < p.V && k0 + c < p.K)
-            t[i] = *reinterpret_cast<const Words<float, 4, 4>*>(S + static_cast<int64_t>(v0 + r) * p.K + k0 + c);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int r = (tid + i * kDecayThreads) / (kBlock / 4), c = (tid + i * kDecayThreads) % (kBlock / 4) * 4;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s_state[r][c + k] = u[i][k];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int r = (tid + i * kDecayThreads) / (kBlock / 4), c = (tid + i * kDecayThreads) % (kBlock / 4) * 4;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) dot += static_cast<double>(s_state[c + k][r]) * t[i][k];
-        }
-      }
-  dot = over_wave(dot);
-  if (lane == 0) s_sum[wave] = dot;
-  // sums before and from each step on, and over all of a chunk
-  double within[kEach];
-  bool live[kEach];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int c = wave + i * kWaves;
-    const bool cut = on[i] && g[i] <= kNoDecay;
-    // sums up to here, and from here on as far as the next cut, which nothing reaches across
-    double pre = a[i], post = b[i];
-    int stop = __shfl_down(static_cast<int>(cut), 1);
+      dot = over_wave(dot);
+    }
+    turn ^= 1;  // (the sums of the barrier before may still be read)
+    if (lane == 0) s_sum[turn][wave] = dot;
+    __syncthreads();
+    if (wave > 0) continue;
+    // sums before and from each step on
+    double pre = a, post = b;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const double u = __shfl_up(pre, off), v = __shfl_down(post, off);
-      const int w = __shfl_down(stop, off);
       if (lane >= off) pre += u;
-      if (lane + off < 64 && !stop) {
-        post += v;
-        stop = w;
-      }
-    }
-    const bool cuts = __any(cut);
-    const double total = over_wave(cut ? 0.0 : static_cast<double>(g[i]));
-    if (lane == 63) s_a[c] = pre;
-    if (lane == 0) {
-      s_b[c] = post;
-      s_keeps[c] = !cuts && exp_exactly(total) != 0.0f;
+      if (lane + off < 64) post += v;
     }
     pre = __shfl_up(pre, 1);
-    within[i] = (lane == 0 ? 0.0 : pre) + post;
-    live[i] = on[i] && !cut;  // the gradient of a cut is 0
-    if (p.dg && cut) p.dg[(s.begin + (begin + c) * C + lane) * w.heads + head] = 0.0f;
-  }
-  __syncthreads();
-  double X = 0.0, all = 0.0;
-  for (int k = 0; k < kWaves; ++k) X += s_sum[k];
-  // from the stretch's end to its start, every wave for itself
-  for (int c = count - 1; c >= 0; --c) {
-    const double through = s_keeps[c] ? X - s_a[c] : 0.0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (c == wave + i * kWaves && live[i]) {
-        const double grad = through + within[i];
-        if (p.dg) p.dg[(s.begin + (begin + c) * C + lane) * w.heads + head] = static_cast<float>(grad);
-        all += grad;
-      }
-    X = through + s_b[c];
-  }
-  if (!p.parts) return;
-  all = over_wave(all);
-  __syncthreads();
-  if (lane == 0) s_sum[wave] = all;
-  __syncthreads();
-  if (tid == 0) {
-    double sum = 0.0;
-    for (int k = 0; k < kWaves; ++k) sum += s_sum[k];
-    p.parts[slot * w.heads + head] = static_cast<float>(sum);
+    double grad = (lane == 0 ? 0.0 : pre) + post + pairs;
+    if (through) {
+      double sum = 0.0;
+      for (int k = 0; k < kWaves; ++k) sum += s_sum[turn][k];
+      grad += exp_exactly(total) * sum;
+    }
+    if (!on || cut) grad = 0.0;  // the gradient of a cut is 0
+    if (p.dg && on) p.dg[row * w.heads + head] = static_cast<float>(grad);
+    if (p.parts) {
+      grad = over_wave(grad);
+      if (lane == 0) p.parts[unit] = static_cast<float>(grad);
+    }
   }
 }
 
@@ -425,21 +358,19 @@ int dk_dq_per(const LinattnSizes& n) { return per_of(n, n.heads * value_tiles(n.
 // The backward's workspace.
 struct BwdBytes {
   SegmentBytes dv, dk_dq;
-  size_t marks, a, b, last, part, parts;
-  int64_t stretches;
-  size_t total() const { return dv.total() + 2 * dk_dq.total() + 2 * marks + a + b + last + 2 * part + parts; }
+  size_t states, sums, part, parts;
+  int64_t slots;             // of chunks
+  size_t total() const { return dv.total() + 2 * dk_dq.total() + 2 * states + 3 * sums + 2 * part + parts; }
 };
 BwdBytes bwd_bytes(const LinattnSizes& n, bool head_decay) {
   BwdBytes s;
   s.dv = segment_bytes(n, dv_per(n));
   s.dk_dq = segment_bytes(n, dk_dq_per(n));
-  s.stretches = slots_of(n.rows, n.batch, kMarkSteps);
-  s.marks = r256(static_cast<size_t>(marks_of(n.rows)) * n.heads * n.K * n.V * 4);
-  s.a = r256(static_cast<size_t>(2 * value_tiles(n.V)) * n.heads * n.rows * 4);
-  s.b = r256(static_cast<size_t>(2 * value_tiles(n.K)) * n.heads * n.rows * 4);
-  s.last = r256(static_cast<size_t>(n.batch) * n.heads * n.K * n.V * 4);
+  s.slots = slots_of(n.rows, n.batch, chunk_of(n));
+  s.states = r256(static_cast<size_t>(s.slots) * n.heads * entering_size(n.V, n.K) * 4);
+  s.sums = r256(static_cast<size_t>(value_tiles(n.K)) * n.heads * n.rows * 4);
   s.part = n.heads == n.groups ? 0 : r256(static_cast<size_t>(n.rows) * n.heads * n.K * 4);
-  s.parts = head_decay ? r256(static_cast<size_t>(s.stretches) * n.heads * 4) : 0;
+  s.parts = head_decay ? r256(static_cast<size_t>(s.slots) * n.heads * 4) : 0;
   return s;
 }
 
@@ -586,28 +517,28 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
       for (MixRole* r : {&dk, &dq}) give_segments(*r, s.dk_dq, at);
     DecayGrad d{};
     if (work && p.dg) {
-      dv.e = f.v;
-      dv.se = f.sv;
-      dv.marks = take(s.marks);
-      dv.sums = take(s.a);
+      dk.e = f.k;
+      dk.se = f.sk;
+      dk.entering = take(s.states);
+      dk.sums = take(s.sums);
       dq.e = f.q;
       dq.se = f.sq;
-      dq.marks = take(s.marks);
-      dq.sums = take(s.b);
-      if (p.dlast) dq.last = take(s.last);
+      dq.entering = take(s.states);
+      dq.sums = take(s.sums);
+      dq.pairs = take(s.sums);
       d.w = w;
-      d.a = dv.sums;
+      d.a = dk.sums;
       d.b = dq.sums;
-      d.marks = dq.marks;
-      d.dmarks = dv.marks;
-      d.last = dq.last;
-      d.dlast = p.dlast;
+      d.pairs = dq.pairs;
+      d.S = dq.entering;
+      d.dS = dk.entering;
+      d.first = f.h0 != nullptr;
+      d.last = p.dlast != nullptr;
       d.dg = f.head_decay ? nullptr : p.dg;
       d.parts = f.head_decay ? take(s.parts) : nullptr;
-      d.atiles = value_tiles(V);
-      d.btiles = value_tiles(K);
-      d.K = K;
-      d.V = V;
+      d.slots = s.slots;
+      d.tiles = value_tiles(K);
+      d.size = entering_size(V, K);
     }
     if (work && share > 1) {
       dq.part = take(s.part);
@@ -653,13 +584,14 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (work && p.dg) {
-      const dim3 grid(static_cast<unsigned>(s.stretches * n.heads));
+      const int64_t units = s.slots * n.heads;
+      const dim3 grid(static_cast<unsigned>(units < kDecayGroups ? units : kDecayGroups));
       if (chunk_of(n) == 64)
         hipLaunchKernelGGL((decay_grad_kernel<64>), grid, dim3(kDecayThreads), 0, stream, d);
       else
         hipLaunchKernelGGL((decay_grad_kernel<32>), grid, dim3(kDecayThreads), 0, stream, d);
       if ((e = hipGetLastError()) != hipSuccess) return e;
-      if (f.head_decay) return launch_colsum(d.parts, s.stretches, n.heads, StoreFlat{p.dg}, stream);
+      if (f.head_decay) return launch_colsum(d.parts, s.slots, n.heads, StoreFlat{p.dg}, stream);
     }
   }
   // no tokens: a decay that every token shares has the gradient 0

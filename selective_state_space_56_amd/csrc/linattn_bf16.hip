@@ -210,7 +210,7 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
   const int vv = wv % NV, kh = wv / NV, k0 = 32 * KT * kh;      // this wave's channels and rows of the state
   const int col = at.tile * kV + 32 * vv + (threadIdx.x & 31);  // this lane's value channel
   const int vw = r.V - at.tile * kV;
-  const bool outputs = r.local == nullptr, sums = SUMS && r.sums;
+  const bool outputs = r.local == nullptr, sums = SUMS && r.sums, pairs = sums && r.pairs;
 
   f32x16 S[KT];
   at.enter_state<StateRows>(w, r, S, col, threadIdx.x % 64 / 32, k0);
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
       f32x16 p[kEach];
       {
         const int lane = fresh(threadIdx.x & 63), lo = lane & 31, hi = lane >> 5;
-        if (sums) at.leave_mark<StateRows>(w, r, S, c, C, col, hi, k0);
+        if (sums) at.leave_entering(w, r, S, c, dec, at.tile * NV + vv, KT * kh, lane);
         const bool flat = __builtin_amdgcn_readfirstlane(dec.flat);
 #pragma unroll
         for (int m = 0; m < kEach; ++m) {
@@ -391,24 +391,36 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
         RowsV::keep(x, tid, &s_q[0][0], ldq);  // the queries are done with
         if (next != at.stop) fetch_q(next);
         __syncthreads();
-        // pairs of steps: the scores times what the other operands' rows give, in float32
+        // pairs of steps: the scores times what the other operands' rows give, in float32, and of
+        // those what crosses each step (only sums of such pairs: a difference of sums over rows and
+        // columns would lose what strong decays leave)
+        if (pairs) {
 #pragma unroll
-        for (int m = 0; m < kEach; ++m) {
-          const int i = wv + m * NW, ti = i > 0, si = i > 1;
-          if (i >= kTiles) continue;
-          f32x16 u = {};
+          for (int m = 0; m < kEach; ++m) {
+            const int i = wv + m * NW, ti = i > 0, si = i > 1;
+            if (i >= kTiles) continue;
+            f32x16 u = {};
 #pragma unroll
-          for (int j = 0; j < kV; j += 16)
-            u = mfma(row8(&s_v[32 * si + lo][j + 8 * hi]), row8(&s_q[32 * ti + lo][j + 8 * hi]), u);
-          const int t = 32 * ti + lo, from = dec.from[t];
-          float sum = 0.0f;
+            for (int j = 0; j < kV; j += 16)
+              u = mfma(row8(&s_v[32 * si + lo][j + 8 * hi]), row8(&s_q[32 * ti + lo][j + 8 * hi]), u);
+            const int t = 32 * ti + lo, from = dec.from[t];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int s = 32 * si + 8 * (i >> 2) + 4 * hi + (i & 3);
-            sum += where((s < t) & (s >= from), u[i] * p[m][i]);
+            for (int i = 0; i < 16; ++i) {
+              const int s = 32 * si + 8 * (i >> 2) + 4 * hi + (i & 3);
+              u[i] = where((s < t) & (s >= from), u[i] * p[m][i]);
+            }
+            const float row = prefix_of(u, hi);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = where(32 * si + 8 * (i >> 2) + 4 * hi + (i & 3) < t, u[i]);
+            const float crossing = over_columns(u, lo);
+            // step s + 1 is crossed by tile (0, 0)'s and (1, 1)'s pairs, and up to step 32 by (1, 0)'s; those
+            // after it by the latter's later rows
+            if ((lo & 1) == 0) s_row(32 * si + column_step(lo, hi))[ti != si] = crossing;
+            if (ti != si) {
+              const float later = over_later(row, lo);
+              if (hi == 0) s_row(t)[1] = later;
+            }
           }
-          sum = over_halves(sum);
-          if (hi == 0) s_row(t)[si] = sum;
         }
         // and what the state that enters gives, with the same rows
 #pragma unroll
@@ -428,13 +440,13 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
         }
         __syncthreads();  // the outputs take the rows' place
         if (tid < n) {
-          float sum = 0.0f, both = 0.0f;
+          float sum = 0.0f, crossing = 0.0f;
 #pragma unroll
           for (int i = 0; i < NV; ++i) sum += s_red(tid)[i];
-          for (int i = 0; i <= tid / 32; ++i) both += s_row(tid)[i];
-          float* to = r.sums + (static_cast<int64_t>(at.tile) * w.heads + at.head) * w.rows + at.begin + at.token(tid, c0, n);
-          to[0] = sum;
-          to[static_cast<int64_t>(w.tiles) * w.heads * w.rows] = both;
+          if (pairs && tid > 0) crossing = s_row(tid - 1)[0] + s_row(tid > 32 ? tid : tid - 1)[1];
+          const int64_t to = (static_cast<int64_t>(at.tile) * w.heads + at.head) * w.rows + at.begin + at.token(tid, c0, n);
+          r.sums[to] = sum;
+          if (pairs) r.pairs[to] = crossing;
         }
       }
       const int lane = fresh(threadIdx.x & 63), lo = lane & 31, hi = lane >> 5;

@@ -50,10 +50,10 @@ struct Rows {
   __device__ __forceinline__ Rows(const void* p, int64_t first_row, int64_t stride_, int64_t first_col, int have_, bool reverse)
       : base(static_cast<const float*>(p) + first_row * stride_ + first_col), stride(stride_), have(have_), back(reverse) {}
   // rows of a chunk that starts c0 steps into the sequence and has n
-  __device__ __forceinline__ void load(f32x4 (&to)[2 * N], int64_t c0, int n) const {
+  __device__ __forceinline__ void load(f32x4 (&to)[2 * N], int tid, int64_t c0, int n) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int id = threadIdx.x + i * THREADS, row = id / kPer, x = 8 * (id % kPer);
+      const int id = tid + i * THREADS, row = id / kPer, x = 8 * (id % kPer);
       to[2 * i] = to[2 * i + 1] = f32x4{};
       if (row < n && x < have) {
         Piece<F32Io, 8> v;
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW, SUMS)) void walk_f32_k
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = at.tile * kV + 32 * wv + lo;  // this lane's value channel
   const int vw = r.V - at.tile * kV;            // value channels from this tile on
-  const bool outputs = r.local == nullptr, sums = SUMS && r.sums;
+  const bool outputs = r.local == nullptr, sums = SUMS && r.sums, pairs = sums && r.pairs;
 
   f32x16 S[KT];
   at.enter_state<Layout>(w, r, S, col, hi);
@@ -113,10 +113,12 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW, SUMS)) void walk_f32_k
   auto fetch = [&](int c) {
     const int64_t c0 = static_cast<int64_t>(c) * C;
     const int n = tokens(c);
-    rk.load(k, c0, n);
-    rv.load(v, c0, n);
-    if (outputs) rq.load(q, c0, n);
-    if (sums) re.load(x, c0, n);
+    int own = tid;
+    if (SUMS) asm volatile("" : "+v"(own));  // (addresses formed here, not kept in registers around the loop)
+    rk.load(k, own, c0, n);
+    rv.load(v, own, c0, n);
+    if (outputs) rq.load(q, own, c0, n);
+    if (sums) re.load(x, own, c0, n);
     if (wv == NW - 1) g = lane < n ? w.g[(at.begin + at.token(lane, c0, n)) * w.g_step + at.head] : 0.0f;
   };
 
@@ -133,7 +135,7 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW, SUMS)) void walk_f32_k
     if (next != at.stop) fetch(next);
     __syncthreads();
     if (outputs) {
-      at.leave_mark<Layout>(w, r, S, c, C, col, hi);
+      if (sums) at.leave_entering(w, r, S, c, dec, at.tile * NW + wv, 0, lane);
       // one wave makes the scores, transposed (earlier steps s as rows, steps t as columns),
       // and another what the other operands' rows give, each chunk the next ones
       const int scores = c % NW, others = (c + 1) % NW;
@@ -159,7 +161,7 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW, SUMS)) void walk_f32_k
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<f32x4*>(&s_p[lo][8 * i + 4 * hi]) = f32x4{p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]};
       }
-      if (sums && wv == others) {
+      if (pairs && wv == others) {
 #pragma unroll 4
         for (int j = 0; j < kV; j += 8) {
           const f32x4 a = *reinterpret_cast<const f32x4*>(&s_v[lo][j + 4 * hi]);
@@ -189,16 +191,22 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW, SUMS)) void walk_f32_k
         }
       }
       __syncthreads();
-      if (sums && wv == others) {
-        const int from = dec.from[lo];
-        float sum = 0.0f;
+      if (pairs && wv == others) {
+        // what crosses each step (sums only, as with bfloat16); the lane's places formed here, not
+        // kept in registers around the loop
+        int own = lane;
+        asm volatile("" : "+v"(own));
+        const int lo = own & 31, hi = own >> 5, from = dec.from[lo];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int s = 8 * (i >> 2) + 4 * hi + (i & 3);
-          sum += where((s < lo) & (s >= from), u[i] * s_p[lo][s]);
+          u[i] = where((s < lo) & (s >= from), u[i] * s_p[lo][s]);
         }
-        sum += __shfl_xor(sum, 32);
-        if (hi == 0) s_row[lo] = sum;
+        prefix_of(u, hi);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) u[i] = where(8 * (i >> 2) + 4 * hi + (i & 3) < lo, u[i]);
+        const float crossing = over_columns(u, lo);
+        if ((lo & 1) == 0) s_row[column_step(lo, hi)] = crossing;
       }
       const f32x16 before = acc;
 #pragma unroll
@@ -231,9 +239,9 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW, SUMS)) void walk_f32_k
           float sum = 0.0f;
 #pragma unroll
           for (int i = 0; i < NW; ++i) sum += s_red[i][tid];
-          float* to = r.sums + (static_cast<int64_t>(at.tile) * w.heads + at.head) * w.rows + at.begin + at.token(tid, c0, n);
-          to[0] = sum;
-          to[static_cast<int64_t>(w.tiles) * w.heads * w.rows] = s_row[tid];
+          const int64_t to = (static_cast<int64_t>(at.tile) * w.heads + at.head) * w.rows + at.begin + at.token(tid, c0, n);
+          r.sums[to] = sum;
+          if (pairs) r.pairs[to] = tid > 0 ? s_row[tid - 1] : 0.0f;
         }
       }
     }

@@ -31,6 +31,67 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 // its expression, the compiler branches around each one.
 __device__ __forceinline__ float where(bool on, float v) { return on ? v : 0.0f; }
 
+// A value from another lane of its row of 16, as a DPP control says; 0 from outside the row.
+template <int CTRL>
+__device__ __forceinline__ float from_row(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+constexpr int kMirror16 = 0x140, kMirror8 = 0x141, kSwapPairs = 0x4e, kSwapLanes = 0xb1;  // lane i: of 15 - i, 7 - i, i ^ 2, i ^ 1
+constexpr int kFirst = 0x150, kNext = 0x100;                                              // of lane 0; of i + n
+
+// Pairs of steps as a tile of D's registers: register i of a lane is step s = 8 (i / 4) + 4 hi + i % 4 with
+// step u, the lane's column. prefix_of: each becomes the sum over s up to its own; returns a column's sum. All
+// sums here are made in a fixed order, without LDS.
+template <class Tile>
+__device__ __forceinline__ float prefix_of(Tile& v, int hi) {
+  float before = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+#pragma unroll
+    for (int e = 1; e < 4; ++e) v[4 * j + e] += v[4 * j + e - 1];
+    const uint32_t own = __float_as_uint(v[4 * j + 3]);
+    const auto both = __builtin_amdgcn_permlane32_swap(own, own, false, false);
+    const float low = __uint_as_float(both[0]), high = __uint_as_float(both[1]);
+    const float base = hi ? before + low : before;
+    before += low + high;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * j + e] += base;
+  }
+  return before;
+}
+
+// The sums of each register over the 32 columns of a half wave, register i's in lanes 2 i and 2 i + 1: at each
+// step a lane keeps half of its registers and adds the other lane's.
+template <class Tile>
+__device__ __forceinline__ float over_columns(const Tile& v, int lo) {
+  float a[8], b[4], c[2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[8 + i]), false, false);
+    a[i] = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = (lo & 8 ? a[4 + i] : a[i]) + from_row<kMirror16>(lo & 8 ? a[i] : a[4 + i]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) c[i] = (lo & 4 ? b[2 + i] : b[i]) + from_row<kMirror8>(lo & 4 ? b[i] : b[2 + i]);
+  const float one = (lo & 2 ? c[1] : c[0]) + from_row<kSwapPairs>(lo & 2 ? c[0] : c[1]);
+  return one + from_row<kSwapLanes>(one);
+}
+
+// The step s of a tile that over_columns' result of this lane is for.
+__device__ __forceinline__ int column_step(int lo, int hi) { return 8 * (lo >> 3) + 4 * hi + ((lo >> 1) & 3); }
+
+// The sum over the columns from the lane's own to the half wave's last.
+__device__ __forceinline__ float over_later(float v, int lo) {
+  v += from_row<kNext + 1>(v);
+  v += from_row<kNext + 2>(v);
+  v += from_row<kNext + 4>(v);
+  v += from_row<kNext + 8>(v);
+  const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  const float upper = from_row<kFirst>(__uint_as_float(w[1]));
+  return lo < 16 ? v + upper : v;
+}
+
 // A segment's whole decay.
 struct Gone {
   double sum = 0.0;
@@ -136,15 +197,27 @@ struct Walk {
     }
   }
 
-  // The state between chunks, for the gradients of the decays: with time running
-  // forward what enters chunk c, in reverse what enters it from behind.
-  template <class L, class Tile, int N>
-  __device__ __forceinline__ void leave_mark(const MixCall& w, const MixRole& r, const Tile (&S)[N], int c, int C, int col,
-                                             int part, int row0 = 0) const {
-    const int between = reverse ? c + 1 : c, mark = kMarkSteps / C;
-    if (!r.marks || between == 0 || between >= chunks || between % mark) return;
-    const int64_t at = mark_of(begin, between / mark);
-    write<L>(r, r.marks + (at * w.heads + head) * r.K * r.V, S, col, part, row0);
+  // The state that enters chunk c (in reverse, from behind), for the gradients of the decays: as it
+  // stands in registers, 32 x 32 tiles of 16 bytes of each lane, since only its product with another run's
+  // is asked for. (A training step of 8 x 2048 steps of 20 heads of 128 x 128, bf16: 755 us with rows of the
+  // state written 4 bytes at a time, and 708 with 16, which is 685 with the non-temporal hint.)
+  template <class Tile, int N, int C>
+  __device__ __forceinline__ void leave_entering(const MixCall& w, const MixRole& r, const Tile (&S)[N], int c,
+                                                 const Decays<C>& dec, int col_tile, int row_tile, int lane) const {
+    typedef float Quad __attribute__((ext_vector_type(4)));
+    if (!r.entering || (!r.s0 && c == (reverse ? chunks - 1 : 0))) return;
+    if (!__builtin_amdgcn_readfirstlane(passes(dec.cut, dec.total, 1.0))) return;
+    const int rows = (r.K + 31) / 32, cols = (r.V + 31) / 32;
+    if (col_tile >= cols) return;
+    const int64_t at = (first_slot(begin, seq, C) + c) * w.heads + head;
+    Quad* to = reinterpret_cast<Quad*>(r.entering) + ((at * cols + col_tile) * rows + row_tile) * 256 + lane;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (row_tile + k >= rows) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        __builtin_nontemporal_store(Quad{S[k][4 * j], S[k][4 * j + 1], S[k][4 * j + 2], S[k][4 * j + 3]}, to + 256 * k + 64 * j);
+    }
   }
 
   template <class L, class Tile, int N>
