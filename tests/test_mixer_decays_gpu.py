@@ -37,6 +37,29 @@ def test_no_gradient_without_a_state(io):
 
 
 @pytest.mark.parametrize("io", [F32, BF])
+def test_what_a_cut_drops_reaches_no_later_gradient(io):
+    s, _ = case("strong steps", io, CPU)
+    cut = 90
+    s["g"][0, cut] = -math.inf
+    clean = {n: t.clone() for n, t in s.items()}
+    for n in ("q", "k", "v", "dout"):
+        s[n][0, 80:cut] = math.nan
+    want = rounded(D.dg(*arguments(clean)), F32)
+    d = gradients({n: t.cuda() for n, t in s.items()})
+    assert_within("dg", d["dg"][:, cut:], tuple(x[:, cut:] for x in want))
+    for n in ("dq", "dk", "dv"):
+        assert d[n][:, cut:].isfinite().all(), n
+    # and what comes behind it reaches no earlier one
+    s = {n: t.clone() for n, t in clean.items()}
+    for n in ("q", "k", "v", "dout"):
+        s[n][0, cut:cut + 5] = math.nan
+    d = gradients({n: t.cuda() for n, t in s.items()})
+    assert_within("dg", d["dg"][:, :cut + 1], tuple(x[:, :cut + 1] for x in want))
+    for n in ("dq", "dk", "dv"):
+        assert d[n][:, :cut].isfinite().all(), n
+
+
+@pytest.mark.parametrize("io", [F32, BF])
 @pytest.mark.parametrize("K,V", [(64, 64), (200, 136), (24, 256)])
 def test_strided_rows(K, V, io):
     """Column slices of one projection's rows give the bits of contiguous tensors."""
