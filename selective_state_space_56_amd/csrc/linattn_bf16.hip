@@ -295,8 +295,7 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
 #pragma unroll
           for (int j = 0; j < kK; j += 16)
             p[m] = mfma(row8(&s_k[32 * si + lo][j + 8 * hi]), row8(&s_q[32 * ti + lo][j + 8 * hi]), p[m]);
-          // times their decays: with t = s in the chunk's usual range, as one factor of each;
-          // -0 where t does not see s, and nowhere else
+          // times their decays, in the chunk's usual range as one factor of each step; 0 where t does not see s
           const int t = 32 * ti + lo, s0 = 32 * si + 4 * hi;
           if (flat) {
             const float up = dec.up[t];
@@ -304,11 +303,11 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
             for (int i = 0; i < 4; ++i) {
               const f32x4 down = *reinterpret_cast<const f32x4*>(&dec.down[s0 + 8 * i]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) p[m][4 * i + e] = fmaf(p[m][4 * i + e], up * down[e], 0.0f);
+              for (int e = 0; e < 4; ++e) p[m][4 * i + e] *= up * down[e];
             }
             if (ti == si) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) p[m][i] = 8 * (i >> 2) + 4 * hi + (i & 3) <= lo ? p[m][i] : -0.0f;
+              for (int i = 0; i < 16; ++i) p[m][i] = where(8 * (i >> 2) + 4 * hi + (i & 3) <= lo, p[m][i]);
             }
           } else {
             const int from = dec.from[t];
@@ -317,7 +316,7 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
             for (int i = 0; i < 16; ++i) {
               const int s = s0 + 8 * (i >> 2) + (i & 3);
               const float f = exp_of(ell - dec.ell[s]) * r.score;
-              p[m][i] = ((s <= t) & (s >= from)) ? fmaf(p[m][i], f, 0.0f) : -0.0f;
+              p[m][i] = where((s <= t) & (s >= from), p[m][i] * f);
             }
           }
 #pragma unroll
@@ -451,8 +450,8 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
       }
       const int lane = fresh(threadIdx.x & 63), lo = lane & 31, hi = lane >> 5;
       // A score of 0 times a value that is not finite is NaN: with such a value among this
-      // wave's, steps are added one by one, to the outputs that see them only (whose score
-      // is not -0).
+      // wave's, steps are added one by one, to the outputs that see them only (by their places: a
+      // score that they see may be 0 too).
       u32x4 values[C / 16];
       u16x2 most = {};
 #pragma unroll
@@ -468,9 +467,8 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
 #pragma unroll
           for (int t = 0; t < kOwn; ++t) {
             const int row = 32 * (first + t) + lo;
-            const uint16_t score = s_p[0][row][s];
-            const float f = Bf16Io::to_f32(score) + Bf16Io::to_f32(s_p[1][row][s]);
-            if ((score != 0x8000) & (s < 32 * (first + t + 1))) {
+            const float f = Bf16Io::to_f32(s_p[0][row][s]) + Bf16Io::to_f32(s_p[1][row][s]);
+            if ((s <= row) & (s >= dec.from[row])) {
 #pragma unroll
               for (int i = 0; i < 16; ++i)
                 acc[t][i] = fmaf(f, Bf16Io::to_f32(s_v[s][32 * vv + 8 * (i >> 2) + 4 * hi + (i & 3)]), acc[t][i]);
