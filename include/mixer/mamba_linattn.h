@@ -19,7 +19,8 @@
  *
  * A token's values reach the outputs of its own and later tokens of its
  * sequence and no other's, non-finite ones too; within one sequence they reach
- * later tokens until a decay of 0.
+ * later tokens until a decay of 0 (one g <= -104: decays that underflow together
+ * leave what is not finite as it is).
  *
  * Sequences are `batch` runs of seqlen tokens, or with MAMBA_LINATTN_PACKED lie
  * one after another in seqlen token rows: sequence i is rows offsets[i] ..

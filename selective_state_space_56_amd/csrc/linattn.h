@@ -43,7 +43,7 @@ struct MixRole {
   float* pairs;          // with it, the same shape, or null: for each step t, what crosses it of the chunk's
                          // own pairs, sum_{s < t <= u} of score (s, u) times e_u . v_s
   float* local;          // a segment's own state, (slots, heads, K, V), instead of outputs; or null
-  float* gone;           // with it: the segment's whole decay, (slots, heads)
+  float* gone;           // with it: the segment's whole decay, (slots, heads); -1 with a cut
   bool s0_turned;        // s0 is (.., V, K)
   bool reverse;
   float score, from, to; // factors of the chunk's scores, of what S_in gives, of what a step adds to S
@@ -110,15 +110,16 @@ __device__ __forceinline__ int sequence_at(const int64_t* offsets, int batch, in
 template <int C>
 struct alignas(16) Decays {
   double ell[C];
-  float in[C];     // of S_in in o_t, times `from`; 0 where a cut lies between
-  float end[C];    // of a step in S_out, times `to`; 0 where a cut lies between
-  int from[C];
+  float in[C];     // of S_in in o_t, times `from`; 0 where a cut lies between (from[t] >= 0) or where it underflows
+  float end[C];    // of a step in S_out, times `to`; 0 where a cut lies between (s < kept) or where it underflows
+  int from[C];     // -1 without a cut before
   // Scores' factors e^{ell_t - ell_s} as up[t] down[s] (times `score`), where that is safe:
   // `flat` without a cut, with no g above 0 and 100 of decay at most.
   float up[C], down[C];
   int flat;
   float all;       // of S_in in S_out; 0 with a cut
   int cut;         // whether there is one
+  int kept;        // the first step that S_out has
   double total;    // the sum of the others
 };
 static_assert(sizeof(Decays<32>) % 16 == 0 && offsetof(Decays<32>, down) % 16 == 0 && offsetof(Decays<32>, end) % 16 == 0 &&
@@ -176,12 +177,13 @@ __device__ __forceinline__ float chunk_decays(Decays<C>& d, float g, int n, bool
     d.in[i] = seen < 0 ? exp_exactly(ell) * from : 0.0f;
     d.up[i] = exp_exactly(ell - 0.5 * total) * score;
     d.down[i] = exp_exactly(0.5 * total - ell);
-    d.from[i] = seen < 0 ? 0 : reverse ? seen + 1 : seen;
+    d.from[i] = seen < 0 ? -1 : reverse ? seen + 1 : seen;
     d.end[i] = live && (reverse ? i > cuts : i >= cuts) ? exp_exactly(total - ell) * to : 0.0f;
     if (i == 0) {
       d.all = all;
       d.flat = flat;
       d.cut = cuts >= 0;
+      d.kept = cuts < 0 ? 0 : reverse ? cuts + 1 : cuts;
       d.total = total;
     }
   }

@@ -9,8 +9,8 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Segments. The state that enters segment p + 1 of a sequence is
-// gone_p enter_p + local_p, of which local and gone are known by then; enter takes
-// local's place. A thread takes four elements of one (sequence, head), and loads the next
+// gone_p enter_p + local_p, of which local and gone are known by then, and local_p alone behind a
+// cut, whatever enters; enter takes local's place. A thread takes four elements of one (sequence, head), and loads the next
 // segments' before it needs them: bound by that latency (25 segments of 20 states of
 // 128 x 128, 66 MB: 15 us).
 constexpr int kJoinThreads = 256;
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk
       piece.set(cur);
       piece.store(r.local + at * size + e);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) cur[k] = gone[i] != 0.0f ? fmaf(gone[i], cur[k], own[i][k]) : own[i][k];
+      for (int k = 0; k < 4; ++k) cur[k] = gone[i] < 0.0f ? own[i][k] : fmaf(gone[i], cur[k], own[i][k]);
     }
   }
 }

@@ -356,7 +356,7 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
         for (int t = 0; t < kTT; ++t) {
           const float f = dec.in[32 * t + lo];
           acc[t] *= f;
-          if (cut) drop(acc[t], f != 0.0f ? 0xffffffffu : 0u);  // what a cut drops may be anything
+          if (cut) drop(acc[t], dec.from[32 * t + lo] < 0 ? 0xffffffffu : 0u);  // what a cut drops may be anything
         }
       }
       __syncthreads();
@@ -520,11 +520,11 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
       __syncthreads();
       for (int id = tid; id < C * kK / 2; id += kThreads) {
         const int s = id / (kK / 2);
-        if (dec.end[s] == 0.0f) *reinterpret_cast<uint32_t*>(&s_k[s][2 * (id % (kK / 2))]) = 0;
+        if (s < dec.kept) *reinterpret_cast<uint32_t*>(&s_k[s][2 * (id % (kK / 2))]) = 0;
       }
       for (int id = tid; id < C * kV / 2; id += kThreads) {
         const int s = id / (kV / 2);
-        if (dec.end[s] == 0.0f) *reinterpret_cast<uint32_t*>(&s_v[s][2 * (id % (kV / 2))]) = 0;
+        if (s < dec.kept) *reinterpret_cast<uint32_t*>(&s_v[s][2 * (id % (kV / 2))]) = 0;
       }
       __syncthreads();
 #pragma unroll

@@ -183,8 +183,7 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW, SUMS)) void walk_f32_k
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int t = 8 * (i >> 2) + 4 * hi + (i & 3);
-        const float f = dec.in[t];
-        acc[i] = where(f != 0.0f, acc[i] * f);
+        acc[i] = where(dec.from[t] < 0, acc[i] * dec.in[t]);  // what a cut drops may be anything
         if (sums) {
           const float all = over_32(acc[i] * s_e[t][32 * wv + lo]);
           if (lo == 0) s_red[wv][t] = all;
@@ -246,17 +245,19 @@ __global__ __launch_bounds__(64 * NW, least_waves(KT, NW, SUMS)) void walk_f32_k
       }
     }
     const float all = dec.all;
+    const bool cut = dec.cut;
+    const int kept = dec.kept;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) S[kt][i] = where(all != 0.0f, S[kt][i] * all);
+      for (int i = 0; i < 16; ++i) S[kt][i] = where(!cut, S[kt][i] * all);
     }
     for (int s0 = 0; s0 < C; s0 += 8)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int s = s0 + 4 * hi + e;
         const float f = dec.end[s];
-        const bool on = f != 0.0f;
+        const bool on = s >= kept;
         const float b = where(on, s_v[s][32 * wv + lo] * f);
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) S[kt] = mfma(where(on, s_k[s][32 * kt + lo]), b, S[kt]);

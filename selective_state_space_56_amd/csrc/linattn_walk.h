@@ -226,7 +226,7 @@ struct Walk {
     const int64_t size = static_cast<int64_t>(r.K) * r.V;
     if (r.local) {
       write<L>(r, r.local + (slot * w.heads + head) * size, S, col, part, row0);
-      if (threadIdx.x == 0 && tile == 0) r.gone[slot * w.heads + head] = gone.cut ? 0.0f : exp_of(gone.sum);
+      if (threadIdx.x == 0 && tile == 0) r.gone[slot * w.heads + head] = gone.cut ? -1.0f : exp_of(gone.sum);
     } else if (r.last && exit) {
       write<L>(r, r.last + (static_cast<int64_t>(seq) * w.heads + head) * size, S, col, part, row0);
     }
