@@ -38,7 +38,7 @@ struct MixRole {
   const float* s0;       // the state that enters a sequence, (batch, heads, K, V), or null
   const float* enter;    // the states that enter later segments, (slots, heads, K, V), or null
   float* last;           // (batch, heads, K, V) or null
-  float* entering;       // the state that enters each chunk, (chunk slots, heads, entering_size), or null
+  float* entering;       // the state that enters each chunk, (chunk or inner slots, heads, entering_size), or null
   float* sums;           // (value tiles, heads, rows) or null: for each step t, e_t . what S_in gives of o_t
   float* pairs;          // with it, the same shape, or null: for each step t, what crosses it of the chunk's
                          // own pairs, sum_{s < t <= u} of score (s, u) times e_u . v_s
@@ -99,6 +99,24 @@ __device__ __forceinline__ int sequence_at(const int64_t* offsets, int batch, in
       hi = mid;
   }
   return lo;
+}
+
+// Slots of chunks of C steps, and of the ends of those that another one of their sequence follows: chunk c's
+// lies (c + 1) C steps into its sequence and before its end, so that counted through all rows its number is
+// below the next sequence's first.
+__device__ __forceinline__ int64_t chunk_slot(const int64_t* offsets, int64_t seqlen, int64_t begin, int64_t seq, int64_t c,
+                                              int C) {
+  return c + (offsets ? first_slot(begin, seq, C) : seq * ((seqlen + C - 1) / C));
+}
+__device__ __forceinline__ int64_t inner_slot(const int64_t* offsets, int64_t seqlen, int64_t begin, int64_t seq, int64_t c,
+                                              int C) {
+  return c + (offsets ? first_slot(begin, 1, C) : seq * ((seqlen + C - 1) / C - 1));
+}
+inline int64_t chunk_slots_of(const LinattnSizes& n, int64_t C) {
+  return n.packed ? slots_of(n.rows, n.batch, C) : n.batch * ((n.seqlen + C - 1) / C);
+}
+inline int64_t inner_slots_of(const LinattnSizes& n, int64_t C) {
+  return n.packed ? slots_of(n.rows, 1, C) : n.seqlen > 0 ? n.batch * ((n.seqlen + C - 1) / C - 1) : 0;
 }
 
 // The decays of one chunk of C <= 64 steps, by one wave, a step per lane. Sums

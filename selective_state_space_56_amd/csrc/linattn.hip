@@ -83,15 +83,20 @@ struct DecayGrad {
   const float* a;            // (tiles, heads, rows)
   const float* b;            // the same
   const float* pairs;        // the same
-  const float* S;            // (chunk slots, heads, size), in one order of elements
-  const float* dS;           // the same
-  bool first, last;          // whether a state enters a sequence's first chunk, a gradient its last
+  const float* S;            // (chunk slots, heads, size), in the runs' order of elements
+  const float* dS;           // (inner slots, heads, size), the same
+  const float* dlast;        // (batch, heads, K, V): for a sequence's last chunk; or null
+  bool first;                // whether a state enters a sequence's first chunk
   float* dg;                 // (rows, heads), or null:
   float* parts;              // (chunk slots, heads): sums over the chunk
   int64_t slots;
-  int tiles;
+  int tiles, K, V;
   int64_t size;
 };
+
+// Where a run leaves its registers 4 j .. 4 j + 3: the first of four rows of a 32 x 32 tile.
+template <int C>
+__device__ __forceinline__ int quad_row(int j, int hi) { return C == 64 ? 16 * (j >> 1) + 8 * hi + 4 * (j & 1) : 8 * j + 4 * hi; }
 
 // Sum over a wave, in each lane.
 __device__ __forceinline__ double over_wave(double v) {
@@ -110,9 +115,10 @@ __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) 
   for (int64_t unit = blockIdx.x; unit < p.slots * w.heads; unit += gridDim.x) {
     const int head = static_cast<int>(unit % w.heads);
     const int64_t slot = unit / w.heads;
-    const int seq = sequence_at(w.offsets, w.batch, w.seqlen, w.rows, C, slot);
+    const int seq = w.offsets ? sequence_at(w.offsets, w.batch, w.seqlen, w.rows, C, slot)
+                              : static_cast<int>(slot / ((w.seqlen + C - 1) / C));
     const Sequence s = sequence_of(w.offsets, seq, w.seqlen, w.rows);
-    const int64_t chunks = (s.len + C - 1) / C, c = slot - first_slot(s.begin, seq, C);
+    const int64_t chunks = (s.len + C - 1) / C, c = slot - chunk_slot(w.offsets, w.seqlen, s.begin, seq, 0, C);
     if (c < 0 || c >= chunks) {  // (a slot that no chunk has)
       if (p.parts && tid == 0) p.parts[unit] = 0.0f;
       continue;
@@ -124,7 +130,7 @@ __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) 
     const bool cut = on && g <= kNoDecay;
     const uint64_t cuts = __ballot(cut);
     const double total = over_wave(cut ? 0.0 : static_cast<double>(g));
-    const bool through = passes(cuts != 0, total) && (c > 0 || p.first) && (c + 1 < chunks || p.last);
+    const bool through = passes(cuts != 0, total) && (c > 0 || p.first) && (c + 1 < chunks || p.dlast);
     // keys before the last cut reach nothing behind the chunk, and what entered it no query from the first on: what
     // stands there may be anything
     double a = 0.0, b = 0.0, pairs = 0.0;
@@ -139,16 +145,25 @@ __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) 
     }
     double dot = 0.0;
     if (through) {
-      const float* S = p.S + unit * p.size;
-      const float* dS = p.dS + unit * p.size;
-      for (int64_t e0 = 4 * tid; e0 < p.size; e0 += 4 * kDecayThreads * kDecayAhead) {
-        Words<float, 4, 16> x[kDecayAhead] = {}, y[kDecayAhead] = {};
+      using Quad = Words<float, 4, 16>;
+      const Quad* S = reinterpret_cast<const Quad*>(p.S + unit * p.size);
+      const bool inner = c + 1 < chunks;
+      const int64_t at = inner ? inner_slot(w.offsets, w.seqlen, s.begin, seq, c, C) * w.heads + head : 0;
+      const Quad* dS = reinterpret_cast<const Quad*>(p.dS + at * p.size);
+      const float* dlast = inner ? nullptr : p.dlast + (static_cast<int64_t>(seq) * w.heads + head) * p.K * p.V;
+      const int quads = static_cast<int>(p.size / 4), down = (p.V + 31) / 32;
+      for (int e0 = tid; e0 < quads; e0 += kDecayThreads * kDecayAhead) {
+        Quad x[kDecayAhead] = {}, y[kDecayAhead] = {};
 #pragma unroll
         for (int k = 0; k < kDecayAhead; ++k) {
-          const int64_t e = e0 + 4 * kDecayThreads * k;
-          if (e < p.size) {
-            x[k] = __builtin_nontemporal_load(reinterpret_cast<const Words<float, 4, 16>*>(S + e));
-            y[k] = __builtin_nontemporal_load(reinterpret_cast<const Words<float, 4, 16>*>(dS + e));
+          const int e = e0 + kDecayThreads * k;
+          if (e >= quads) continue;
+          x[k] = __builtin_nontemporal_load(S + e);
+          if (inner) {
+            y[k] = __builtin_nontemporal_load(dS + e);
+          } else {  // from rows of keys, of any alignment
+            const int key = e / 256 / down * 32 + e % 32, value = e / 256 % down * 32 + quad_row<C>(e / 64 % 4, e / 32 % 2);
+            if (key < p.K && value < p.V) y[k] = *reinterpret_cast<const Words<float, 4, 4>*>(dlast + key * p.V + value);
           }
         }
 #pragma unroll
@@ -364,16 +379,18 @@ int dk_dq_per(const LinattnSizes& n) { return per_of(n, n.heads * value_tiles(n.
 // The backward's workspace.
 struct BwdBytes {
   SegmentBytes dv, dk_dq;
-  size_t states, sums, part, parts;
+  size_t S, dS, sums, part, parts;
   int64_t slots;             // of chunks
-  size_t total() const { return dv.total() + 2 * dk_dq.total() + 2 * states + 3 * sums + 2 * part + parts; }
+  size_t total() const { return dv.total() + 2 * dk_dq.total() + S + dS + 3 * sums + 2 * part + parts; }
 };
 BwdBytes bwd_bytes(const LinattnSizes& n, bool head_decay) {
   BwdBytes s;
   s.dv = segment_bytes(n, dv_per(n));
   s.dk_dq = segment_bytes(n, dk_dq_per(n));
-  s.slots = slots_of(n.rows, n.batch, chunk_of(n));
-  s.states = r256(static_cast<size_t>(s.slots) * n.heads * entering_size(n.V, n.K) * 4);
+  s.slots = chunk_slots_of(n, chunk_of(n));
+  const size_t state = static_cast<size_t>(n.heads) * entering_size(n.V, n.K) * 4;
+  s.S = r256(s.slots * state);
+  s.dS = r256(inner_slots_of(n, chunk_of(n)) * state);
   s.sums = r256(static_cast<size_t>(value_tiles(n.K)) * n.heads * n.rows * 4);
   s.part = n.heads == n.groups ? 0 : r256(static_cast<size_t>(n.rows) * n.heads * n.K * 4);
   s.parts = head_decay ? r256(static_cast<size_t>(s.slots) * n.heads * 4) : 0;
@@ -525,11 +542,11 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
     if (work && p.dg) {
       dk.e = f.k;
       dk.se = f.sk;
-      dk.entering = take(s.states);
+      dk.entering = take(s.dS);
       dk.sums = take(s.sums);
       dq.e = f.q;
       dq.se = f.sq;
-      dq.entering = take(s.states);
+      dq.entering = take(s.S);
       dq.sums = take(s.sums);
       dq.pairs = take(s.sums);
       d.w = w;
@@ -538,12 +555,14 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
       d.pairs = dq.pairs;
       d.S = dq.entering;
       d.dS = dk.entering;
+      d.dlast = p.dlast;
       d.first = f.h0 != nullptr;
-      d.last = p.dlast != nullptr;
       d.dg = f.head_decay ? nullptr : p.dg;
       d.parts = f.head_decay ? take(s.parts) : nullptr;
       d.slots = s.slots;
       d.tiles = value_tiles(K);
+      d.K = K;
+      d.V = V;
       d.size = entering_size(V, K);
     }
     if (work && share > 1) {

@@ -197,7 +197,7 @@ struct Walk {
     }
   }
 
-  // The state that enters chunk c (in reverse, from behind), for the gradients of the decays: as it
+  // The state that enters chunk c (in reverse, from behind, where another one follows), for the gradients of the decays: as it
   // stands in registers, 32 x 32 tiles of 16 bytes of each lane, since only its product with another run's
   // is asked for. (A training step of 8 x 2048 steps of 20 heads of 128 x 128, bf16: 755 us with rows of the
   // state written 4 bytes at a time, and 708 with 16, which is 685 with the non-temporal hint.)
@@ -205,11 +205,12 @@ struct Walk {
   __device__ __forceinline__ void leave_entering(const MixCall& w, const MixRole& r, const Tile (&S)[N], int c,
                                                  const Decays<C>& dec, int col_tile, int row_tile, int lane) const {
     typedef float Quad __attribute__((ext_vector_type(4)));
-    if (!r.entering || (!r.s0 && c == (reverse ? chunks - 1 : 0))) return;
+    if (!r.entering || (reverse ? c == chunks - 1 : c == 0 && !r.s0)) return;
     if (!__builtin_amdgcn_readfirstlane(passes(dec.cut, dec.total, 1.0))) return;
     const int rows = (r.K + 31) / 32, cols = (r.V + 31) / 32;
     if (col_tile >= cols) return;
-    const int64_t at = (first_slot(begin, seq, C) + c) * w.heads + head;
+    const int64_t at = (reverse ? inner_slot(w.offsets, w.seqlen, begin, seq, c, C)
+                                : chunk_slot(w.offsets, w.seqlen, begin, seq, c, C)) * w.heads + head;
     Quad* to = reinterpret_cast<Quad*>(r.entering) + ((at * cols + col_tile) * rows + row_tile) * 256 + lane;
 #pragma unroll
     for (int k = 0; k < N; ++k) {

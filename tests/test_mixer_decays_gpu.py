@@ -8,7 +8,7 @@ import torch
 import decay_ref as D
 from block_ref import assert_within, rounded
 from decay_cases import CASES, arguments, case
-from selective_state_space_56_amd import linear_attn_bwd
+from selective_state_space_56_amd import linear_attn_bwd, linear_attn_fwd
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -90,3 +90,45 @@ def test_many_chunks_and_heads(fixed, io):
     for at in (slice(0, 3), slice(H - 3, H)):
         part = {m: (t[at] if m == "g" and fixed else t[..., at] if m == "g" else t[:, :, at]).cpu() for m, t in s.items()}
         assert_within("dg", got[..., at], rounded(D.dg(*arguments(part)), F32))
+
+
+@pytest.mark.parametrize("io", [F32, BF])
+@pytest.mark.parametrize("name", ["40 x 72, shared keys, states", "65 steps", "packed", "one step"])
+def test_a_state_on_one_side_only(name, io):
+    s, off = case(name, io, CPU)
+    h0, dlast, zeros = s["h0"], s["dlast"], torch.zeros_like(s["h0"])
+    args, dev = arguments(s), {n: t.cuda() for n, t in s.items()}
+    off_d = None if off is None else off.cuda()
+    for mine, theirs in (((h0, zeros), (dev["h0"], None)), ((zeros, dlast), (None, dev["dlast"])), ((zeros, zeros), (None, None))):
+        got = linear_attn_bwd(*(dev[n] for n in "qkvg"), dev["dout"], h0=theirs[0], dlast=theirs[1], offsets=off_d)["dg"]
+        assert_within(name, got, rounded(D.dg(*args[:6], *mine, offsets=off), F32))
+
+
+@pytest.mark.parametrize("fixed", [False, True])
+@pytest.mark.parametrize("K,V,n", [(16, 24, 40), (64, 64, 70), (136, 32, 33)])
+def test_decays_against_differences(K, V, n, fixed):
+    """dg of one step (or head) against (loss(g + h) - loss(g - h)) / 2 h there, the loss from the forward's
+    outputs and states. Values are positive, so that the loss is the sum of its terms' magnitudes. A term
+    holds the step's decay once (a fixed one n times at most): the central difference is off by h^2 / 6 of the
+    loss (n^3 h^2 / 6). The forward rounds each term n + K + V + 64 times at most."""
+    gen = torch.Generator().manual_seed(3)
+
+    def values(*shape):
+        return torch.rand(shape, generator=gen).cuda()
+    q, k, v, dout = values(2, n, 1, K), values(2, n, 1, K), values(2, n, 2, V), values(2, n, 2, V)
+    h0, dlast = values(2, 2, K, V), values(2, 2, K, V)
+    g = -0.2 * values(2) if fixed else -0.2 * values(2, n, 2)
+    d = linear_attn_bwd(q, k, v, g, dout, h0=h0, dlast=dlast)["dg"]
+    h = 2.0 ** -9 if fixed else 2.0 ** -5
+
+    def loss(g):
+        out, last = linear_attn_fwd(q, k, v, g, h0=h0)
+        return (out.double() * dout.double()).sum() + (last.double() * dlast.double()).sum()
+    for at in ((0,), (1,)) if fixed else ((0, 0, 0), (1, 5, 1), (0, n // 2, 1), (1, n - 1, 0)):
+        up, down = g.clone(), g.clone()
+        up[at] += h
+        down[at] -= h
+        a, b, step = loss(up), loss(down), float(up[at].double() - down[at].double())
+        off = float(a) * (((n * h) ** 3 if fixed else h ** 3) / 6 + 2 * (2 * (n + K + V) + 128) * 2.0 ** -24)
+        assert abs(float(d[at]) * step - float(a - b)) <= 2 * off, at
+        assert off < 0.25 * abs(float(a - b))     # the difference says something
