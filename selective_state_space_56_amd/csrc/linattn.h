@@ -36,14 +36,14 @@ struct MixRole {
   int qdiv, kdiv, vdiv, ediv;  // heads that share the operand's head
   int K, V;
   const float* s0;       // the state that enters a sequence, (batch, heads, K, V), or null
-  const float* enter;    // the states that enter later segments, (slots, heads, K, V), or null
+  const float* enter;    // the states that enter later segments, (slots, some, K, V), or null
   float* last;           // (batch, heads, K, V) or null
-  float* entering;       // the state that enters each chunk, (chunk or inner slots, heads, entering_size), or null
+  float* entering;       // the state that enters each chunk, (chunk or inner slots, some, entering_size), or null
   float* sums;           // (value tiles, heads, rows) or null: for each step t, e_t . what S_in gives of o_t
   float* pairs;          // with it, the same shape, or null: for each step t, what crosses it of the chunk's
                          // own pairs, sum_{s < t <= u} of score (s, u) times e_u . v_s
-  float* local;          // a segment's own state, (slots, heads, K, V), instead of outputs; or null
-  float* gone;           // with it: the segment's whole decay, (slots, heads); -1 with a cut
+  float* local;          // a segment's own state, (slots, some, K, V), instead of outputs; or null
+  float* gone;           // with it: the segment's whole decay, (slots, some); -1 with a cut
   bool s0_turned;        // s0 is (.., V, K)
   bool reverse;
   float score, from, to; // factors of the chunk's scores, of what S_in gives, of what a step adds to S
@@ -57,6 +57,7 @@ struct MixCall {
   int64_t seqlen, rows;
   int64_t slots;           // segments at most, over all sequences
   int batch, heads, roles, tiles;
+  int head0, some;         // the heads of this call: `some` from head0 on; slots' arrays hold these
   int per;                 // chunks of a segment
   uint32_t together;       // consecutive workgroups that read the same rows
 };

@@ -21,15 +21,15 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk
   const int64_t size = static_cast<int64_t>(r.K) * r.V;
   const int64_t e = ((blockIdx.x % blocks) * kJoinThreads + threadIdx.x) * 4;
   const int64_t sh = blockIdx.x / blocks;
-  const int head = static_cast<int>(sh % w.heads);
-  const int64_t seq = sh / w.heads;
+  const int own_head = static_cast<int>(sh % w.some);
+  const int64_t seq = sh / w.some;
   if (e >= size) return;
   const Sequence s = sequence_of(w.offsets, seq, w.seqlen, w.rows);
   const int64_t base = first_slot(s.begin, seq, static_cast<uint32_t>(w.per) * chunk);
   const int segs = segments_of(static_cast<int>((s.len + chunk - 1) / chunk), w.per);
   float cur[4] = {};
   if (r.s0) {
-    const float* from = r.s0 + sh * size;
+    const float* from = r.s0 + (seq * w.heads + w.head0 + own_head) * size;
     for (int k = 0; k < 4; ++k)
       cur[k] = r.s0_turned ? from[(e + k) % r.V * r.K + (e + k) / r.V] : from[e + k];
   }
@@ -41,7 +41,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk
       Piece<F32Io, 4> piece = {};
       gone[i] = 0.0f;
       if (p0 + i + 1 < segs) {  // (nobody needs what the last one leaves)
-        const int64_t at = (base + (r.reverse ? segs - 1 - p0 - i : p0 + i)) * w.heads + head;
+        const int64_t at = (base + (r.reverse ? segs - 1 - p0 - i : p0 + i)) * w.some + own_head;
         piece.load(r.local + at * size + e);
         gone[i] = r.gone[at];
       }
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk
 #pragma unroll
     for (int i = 0; i < kJoinAhead; ++i) {
       if (p0 + i >= segs) break;
-      const int64_t at = (base + (r.reverse ? segs - 1 - p0 - i : p0 + i)) * w.heads + head;
+      const int64_t at = (base + (r.reverse ? segs - 1 - p0 - i : p0 + i)) * w.some + own_head;
       Piece<F32Io, 4> piece;
       piece.set(cur);
       piece.store(r.local + at * size + e);
@@ -83,8 +83,8 @@ struct DecayGrad {
   const float* a;            // (tiles, heads, rows)
   const float* b;            // the same
   const float* pairs;        // the same
-  const float* S;            // (chunk slots, heads, size), in the runs' order of elements
-  const float* dS;           // (inner slots, heads, size), the same
+  const float* S;            // (chunk slots, some, size), in the runs' order of elements
+  const float* dS;           // (inner slots, some, size), the same
   const float* dlast;        // (batch, heads, K, V): for a sequence's last chunk; or null
   bool first;                // whether a state enters a sequence's first chunk
   float* dg;                 // (rows, heads), or null:
@@ -112,15 +112,15 @@ __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) 
   __shared__ double s_sum[2][kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int turn = 0;
-  for (int64_t unit = blockIdx.x; unit < p.slots * w.heads; unit += gridDim.x) {
-    const int head = static_cast<int>(unit % w.heads);
-    const int64_t slot = unit / w.heads;
+  for (int64_t unit = blockIdx.x; unit < p.slots * w.some; unit += gridDim.x) {
+    const int own = static_cast<int>(unit % w.some), head = w.head0 + own;
+    const int64_t slot = unit / w.some;
     const int seq = w.offsets ? sequence_at(w.offsets, w.batch, w.seqlen, w.rows, C, slot)
                               : static_cast<int>(slot / ((w.seqlen + C - 1) / C));
     const Sequence s = sequence_of(w.offsets, seq, w.seqlen, w.rows);
     const int64_t chunks = (s.len + C - 1) / C, c = slot - chunk_slot(w.offsets, w.seqlen, s.begin, seq, 0, C);
     if (c < 0 || c >= chunks) {  // (a slot that no chunk has)
-      if (p.parts && tid == 0) p.parts[unit] = 0.0f;
+      if (p.parts && tid == 0) p.parts[slot * w.heads + head] = 0.0f;
       continue;
     }
     // every wave for itself, a step per lane
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) 
       using Quad = Words<float, 4, 16>;
       const Quad* S = reinterpret_cast<const Quad*>(p.S + unit * p.size);
       const bool inner = c + 1 < chunks;
-      const int64_t at = inner ? inner_slot(w.offsets, w.seqlen, s.begin, seq, c, C) * w.heads + head : 0;
+      const int64_t at = inner ? inner_slot(w.offsets, w.seqlen, s.begin, seq, c, C) * w.some + own : 0;
       const Quad* dS = reinterpret_cast<const Quad*>(p.dS + at * p.size);
       const float* dlast = inner ? nullptr : p.dlast + (static_cast<int64_t>(seq) * w.heads + head) * p.K * p.V;
       const int quads = static_cast<int>(p.size / 4), down = (p.V + 31) / 32;
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(kDecayThreads) void decay_grad_kernel(DecayGrad p) 
     if (p.dg && on) p.dg[row * w.heads + head] = static_cast<float>(grad);
     if (p.parts) {
       grad = over_wave(grad);
-      if (lane == 0) p.parts[unit] = static_cast<float>(grad);
+      if (lane == 0) p.parts[slot * w.heads + head] = static_cast<float>(grad);
     }
   }
 }
@@ -311,7 +311,7 @@ MixCall call_of(const LinattnProblem& p) {
   w.seqlen = p.n.seqlen;
   w.rows = p.n.rows;
   w.batch = static_cast<int>(p.n.batch);
-  w.heads = static_cast<int>(p.n.heads);
+  w.heads = w.some = static_cast<int>(p.n.heads);
   return w;
 }
 
@@ -325,9 +325,9 @@ struct SegmentBytes {
   size_t states, gone;
   size_t total() const { return states + gone; }
 };
-SegmentBytes segment_bytes(const LinattnSizes& n, int per) {
+SegmentBytes segment_bytes(const LinattnSizes& n, int per, int64_t heads) {
   if (!split(n, per)) return {0, 0};
-  const size_t at = static_cast<size_t>(slots_of(n.rows, n.batch, static_cast<int64_t>(per) * chunk_of(n))) * n.heads;
+  const size_t at = static_cast<size_t>(slots_of(n.rows, n.batch, static_cast<int64_t>(per) * chunk_of(n))) * heads;
   return {r256(at * n.K * n.V * 4), r256(at * 4)};
 }
 
@@ -350,7 +350,7 @@ hipError_t run(MixCall w, const LinattnSizes& n, bool cut, hipStream_t stream) {
     hipError_t e = walk(w, n.io, stream);
     if (e != hipSuccess) return e;
     const int64_t blocks = (n.K * n.V / 4 + kJoinThreads - 1) / kJoinThreads;
-    hipLaunchKernelGGL(join_kernel, dim3(static_cast<unsigned>(n.batch * n.heads * blocks), w.roles), dim3(kJoinThreads),
+    hipLaunchKernelGGL(join_kernel, dim3(static_cast<unsigned>(n.batch * w.some * blocks), w.roles), dim3(kJoinThreads),
                        0, stream, w, chunk, blocks);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
@@ -373,8 +373,22 @@ hipError_t zero_rest(const RestRows& z, hipStream_t stream) {
 bool one_shape(const LinattnSizes& n) {
   return key_tiles(n.K) == key_tiles(n.V) && value_width(n.V) == value_width(n.K) && value_tiles(n.V) == value_tiles(n.K);
 }
-int dv_per(const LinattnSizes& n) { return per_of(n, n.heads * value_tiles(n.V) * (one_shape(n) ? 3 : 1)); }
-int dk_dq_per(const LinattnSizes& n) { return per_of(n, n.heads * value_tiles(n.K) * (one_shape(n) ? 3 : 2)); }
+// For the decays' gradients a state and its gradient are kept for every chunk, as much as the io tensors of
+// 128 x 128 heads together. Where they would take more than this, the backward goes through its heads in turn,
+// some groups at a time, which fill the machine by segments.
+constexpr int64_t kStatesBytes = int64_t(8) << 30;
+
+int64_t state_bytes(const LinattnSizes& n, int64_t slots) { return slots * entering_size(n.V, n.K) * 4; }
+int64_t heads_at_a_time(const LinattnSizes& n) {
+  const int64_t share = n.heads / n.groups;
+  const int64_t group = share * state_bytes(n, chunk_slots_of(n, chunk_of(n)) + inner_slots_of(n, chunk_of(n)));
+  const int64_t fit = group > kStatesBytes ? 1 : group > 0 ? kStatesBytes / group : n.groups;
+  if (fit >= n.groups) return n.heads;
+  const int64_t turns = (n.groups + fit - 1) / fit;
+  return (n.groups + turns - 1) / turns * share;
+}
+int dv_per(const LinattnSizes& n) { return per_of(n, heads_at_a_time(n) * value_tiles(n.V) * (one_shape(n) ? 3 : 1)); }
+int dk_dq_per(const LinattnSizes& n) { return per_of(n, heads_at_a_time(n) * value_tiles(n.K) * (one_shape(n) ? 3 : 2)); }
 
 // The backward's workspace.
 struct BwdBytes {
@@ -385,12 +399,12 @@ struct BwdBytes {
 };
 BwdBytes bwd_bytes(const LinattnSizes& n, bool head_decay) {
   BwdBytes s;
-  s.dv = segment_bytes(n, dv_per(n));
-  s.dk_dq = segment_bytes(n, dk_dq_per(n));
+  const int64_t some = heads_at_a_time(n);
+  s.dv = segment_bytes(n, dv_per(n), some);
+  s.dk_dq = segment_bytes(n, dk_dq_per(n), some);
   s.slots = chunk_slots_of(n, chunk_of(n));
-  const size_t state = static_cast<size_t>(n.heads) * entering_size(n.V, n.K) * 4;
-  s.S = r256(s.slots * state);
-  s.dS = r256(inner_slots_of(n, chunk_of(n)) * state);
+  s.S = r256(some * state_bytes(n, s.slots));
+  s.dS = r256(some * state_bytes(n, inner_slots_of(n, chunk_of(n))));
   s.sums = r256(static_cast<size_t>(value_tiles(n.K)) * n.heads * n.rows * 4);
   s.part = n.heads == n.groups ? 0 : r256(static_cast<size_t>(n.rows) * n.heads * n.K * 4);
   s.parts = head_decay ? r256(static_cast<size_t>(s.slots) * n.heads * 4) : 0;
@@ -401,7 +415,7 @@ BwdBytes bwd_bytes(const LinattnSizes& n, bool head_decay) {
 
 size_t linattn_fwd_workspace_bytes(const LinattnSizes& n) {
   if (n.rows == 0 || n.heads == 0 || n.batch == 0) return 0;
-  return segment_bytes(n, per_of(n, n.heads * value_tiles(n.V))).total();
+  return segment_bytes(n, per_of(n, n.heads * value_tiles(n.V)), n.heads).total();
 }
 
 size_t linattn_bwd_workspace_bytes(const LinattnSizes& n, bool head_decay) {
@@ -447,7 +461,7 @@ hipError_t launch_linattn_fwd(const LinattnProblem& p, void* workspace, hipStrea
   r.to = 1.0f;
   const bool cut = n.rows > 0 && split(n, per);
   char* at = static_cast<char*>(workspace);
-  if (cut) give_segments(r, segment_bytes(n, per), at);
+  if (cut) give_segments(r, segment_bytes(n, per, n.heads), at);
   return run(w, n, cut, stream);
 }
 
@@ -569,21 +583,37 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
       dq.part = take(s.part);
       dk.part = take(s.part);
     }
-    set_segments(w, n, dv_per(n));
-    w.role[0] = dv;
-    w.roles = 1;
-    if (one_shape(n)) {
-      w.role[1] = dk;
-      w.role[2] = dq;
-      w.roles = 3;
-    }
-    if ((e = run(w, n, cut_dv, stream)) != hipSuccess) return e;
-    if (!one_shape(n)) {
-      set_segments(w, n, dk_dq_per(n));
-      w.role[0] = dk;
-      w.role[1] = dq;
-      w.roles = 2;
-      if ((e = run(w, n, cut_dk_dq, stream)) != hipSuccess) return e;
+    const int some = static_cast<int>(work ? heads_at_a_time(n) : n.heads);
+    for (int h = 0; h < n.heads; h += some) {
+      w.head0 = h;
+      w.some = n.heads - h < some ? static_cast<int>(n.heads) - h : some;
+      set_segments(w, n, dv_per(n));
+      w.role[0] = dv;
+      w.roles = 1;
+      if (one_shape(n)) {
+        w.role[1] = dk;
+        w.role[2] = dq;
+        w.roles = 3;
+      }
+      if ((e = run(w, n, cut_dv, stream)) != hipSuccess) return e;
+      if (!one_shape(n)) {
+        set_segments(w, n, dk_dq_per(n));
+        w.role[0] = dk;
+        w.role[1] = dq;
+        w.roles = 2;
+        if ((e = run(w, n, cut_dk_dq, stream)) != hipSuccess) return e;
+      }
+      if (work && p.dg) {
+        d.w.head0 = w.head0;
+        d.w.some = w.some;
+        const int64_t units = s.slots * w.some;
+        const dim3 grid(static_cast<unsigned>(units < kDecayGroups ? units : kDecayGroups));
+        if (chunk_of(n) == 64)
+          hipLaunchKernelGGL((decay_grad_kernel<64>), grid, dim3(kDecayThreads), 0, stream, d);
+        else
+          hipLaunchKernelGGL((decay_grad_kernel<32>), grid, dim3(kDecayThreads), 0, stream, d);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+      }
     }
     if (work && share > 1) {
       GroupSum gs{};
@@ -608,16 +638,7 @@ hipError_t launch_linattn_bwd(const LinattnBwdProblem& p, void* workspace, hipSt
         hipLaunchKernelGGL((group_sum_kernel<F32Io>), grid, dim3(256), 0, stream, gs);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    if (work && p.dg) {
-      const int64_t units = s.slots * n.heads;
-      const dim3 grid(static_cast<unsigned>(units < kDecayGroups ? units : kDecayGroups));
-      if (chunk_of(n) == 64)
-        hipLaunchKernelGGL((decay_grad_kernel<64>), grid, dim3(kDecayThreads), 0, stream, d);
-      else
-        hipLaunchKernelGGL((decay_grad_kernel<32>), grid, dim3(kDecayThreads), 0, stream, d);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-      if (f.head_decay) return launch_colsum(d.parts, s.slots, n.heads, StoreFlat{p.dg}, stream);
-    }
+    if (work && p.dg && f.head_decay) return launch_colsum(d.parts, s.slots, n.heads, StoreFlat{p.dg}, stream);
   }
   // no tokens: a decay that every token shares has the gradient 0
   if (!work && p.dg && f.head_decay) return launch_colsum(nullptr, 0, n.heads, StoreFlat{p.dg}, stream);

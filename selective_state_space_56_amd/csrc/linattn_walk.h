@@ -10,7 +10,7 @@ namespace mscan {
 inline int key_tiles(int64_t K) { return K <= 64 ? 2 : K <= 128 ? 4 : 8; }
 inline int value_width(int64_t V) { return V <= 64 ? 64 : 128; }
 inline int value_tiles(int64_t V) { return static_cast<int>((V + value_width(V) - 1) / value_width(V)); }
-inline int64_t walk_units(const MixCall& w) { return w.slots * w.heads * w.tiles * w.roles; }
+inline int64_t walk_units(const MixCall& w) { return w.slots * w.some * w.tiles * w.roles; }
 
 // Sum over the 32 lanes of a half wave, in each of them.
 __device__ __forceinline__ float over_32(float v) {
@@ -103,7 +103,7 @@ struct Gone {
 };
 
 struct Walk {
-  int role, tile, head, seq;
+  int role, tile, head, own, seq;  // own: the head among the call's
   int64_t slot, begin, len;
   int chunks;
   int first, stop, step;      // chunks: first, first + step, ... before stop
@@ -120,8 +120,9 @@ struct Walk {
     u /= w.roles;
     tile = u % w.tiles;
     u /= w.tiles;
-    head = u % w.heads;
-    slot = u / w.heads;
+    own = u % w.some;
+    head = w.head0 + own;
+    slot = u / w.some;
     const uint32_t steps = static_cast<uint32_t>(w.per) * C;
     // (the same in every lane, which the compiler cannot see of values read from memory)
     seq = __builtin_amdgcn_readfirstlane(sequence_at(w.offsets, w.batch, w.seqlen, w.rows, steps, slot));
@@ -179,7 +180,7 @@ struct Walk {
       for (int k = 0; k < N; ++k) S[k] = Tile{};
       return;
     }
-    from += ((entry ? static_cast<int64_t>(seq) : slot) * w.heads + head) * r.K * r.V;
+    from += (entry ? static_cast<int64_t>(seq) * w.heads + head : slot * w.some + own) * r.K * r.V;
     const auto rs = make_rsrc(from, static_cast<uint32_t>(r.K * r.V * 4));
     const bool turned = entry && r.s0_turned;
     const int first = row0 + L::kLane * part;
@@ -210,7 +211,7 @@ struct Walk {
     const int rows = (r.K + 31) / 32, cols = (r.V + 31) / 32;
     if (col_tile >= cols) return;
     const int64_t at = (reverse ? inner_slot(w.offsets, w.seqlen, begin, seq, c, C)
-                                : chunk_slot(w.offsets, w.seqlen, begin, seq, c, C)) * w.heads + head;
+                                : chunk_slot(w.offsets, w.seqlen, begin, seq, c, C)) * w.some + own;
     Quad* to = reinterpret_cast<Quad*>(r.entering) + ((at * cols + col_tile) * rows + row_tile) * 256 + lane;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -226,8 +227,8 @@ struct Walk {
                                               int col, int part, int row0 = 0) const {
     const int64_t size = static_cast<int64_t>(r.K) * r.V;
     if (r.local) {
-      write<L>(r, r.local + (slot * w.heads + head) * size, S, col, part, row0);
-      if (threadIdx.x == 0 && tile == 0) r.gone[slot * w.heads + head] = gone.cut ? -1.0f : exp_of(gone.sum);
+      write<L>(r, r.local + (slot * w.some + own) * size, S, col, part, row0);
+      if (threadIdx.x == 0 && tile == 0) r.gone[slot * w.some + own] = gone.cut ? -1.0f : exp_of(gone.sum);
     } else if (r.last && exit) {
       write<L>(r, r.last + (static_cast<int64_t>(seq) * w.heads + head) * size, S, col, part, row0);
     }

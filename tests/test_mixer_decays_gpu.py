@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import decay_ref as D
+import mixer_ref as R
 from block_ref import assert_within, rounded
 from decay_cases import CASES, arguments, case
 from selective_state_space_56_amd import linear_attn_bwd, linear_attn_fwd
@@ -132,3 +133,43 @@ def test_decays_against_differences(K, V, n, fixed):
         off = float(a) * (((n * h) ** 3 if fixed else h ** 3) / 6 + 2 * (2 * (n + K + V) + 128) * 2.0 ** -24)
         assert abs(float(d[at]) * step - float(a - b)) <= 2 * off, at
         assert off < 0.25 * abs(float(a - b))     # the difference says something
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_heads_in_turn(packed):
+    """Chunks' states of more than 8 GiB: the backward goes through the heads in turn. Its first and last
+    groups in the first and last sequences, and one decay for each head as the sum over all tokens."""
+    B, n, H, G, K = 2048, 128, 32, 16, 128
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(8)
+
+    def normal(*shape, io=BF):
+        return torch.randn(shape, generator=gen, device="cuda").to(io)
+    s = {"q": normal(B, n, G, K), "k": normal(B, n, G, K), "v": normal(B, n, H, K), "dout": normal(B, n, H, K),
+         "h0": normal(B, H, K, K, io=F32), "g": -0.2 * torch.rand((B, n, H), generator=gen, device="cuda")}
+    rows = {m: t.flatten(0, 1) if packed and m != "h0" else t for m, t in s.items()}
+    off = torch.arange(0, B * n + 1, n, device="cuda") if packed else None
+    d = gradients(rows, off)
+    for i in (0, B - 1):
+        for h in (0, H - 2):
+            heads, group = slice(h, h + 2), slice(h // 2, h // 2 + 1)
+            part = {m: t[i:i + 1, :, group if m in "qk" else heads].cpu() for m, t in s.items() if m != "h0"}
+            part["h0"] = s["h0"][i:i + 1, heads].cpu()
+            ref = R.linattn(*(part[m] for m in ("q", "k", "v", "g")), K ** -0.5, part["h0"], None, part["dout"])
+            for m in ("dq", "dk", "dv"):
+                got = d[m].view(s[m[1:]].shape)[i:i + 1, :, heads if m == "dv" else group]
+                assert_within(m, got, rounded(ref[m], BF))
+            assert_within("dh0", d["dh0"][i:i + 1, heads], rounded(ref["dh0"], F32))
+            args = [part[m] for m in ("q", "k", "v", "g")]
+            want = D.dg(*args, K ** -0.5, part["dout"], part["h0"])
+            assert_within("dg", d["dg"].view(B, n, H)[i:i + 1, :, heads], rounded(want, F32))
+    del d
+    fixed = -0.1 * torch.rand(H, generator=gen, device="cuda")
+    rows["g"] = fixed.expand(B, n, H).contiguous().view(-1, H) if packed else fixed.expand(B, n, H).contiguous()
+    each = gradients(rows, off)["dg"].double().view(-1, H)
+    rows["g"] = fixed
+    one = gradients(rows, off)["dg"].double()
+    # the same values but for the order: a float32 sum for each chunk, and of these
+    parts = 3 * B + 4
+    assert ((one - each.sum(0)).abs() <= (2 * parts + 4) * 2.0 ** -24 * each.abs().sum(0)).all() and one.all()
+
