@@ -132,7 +132,9 @@ mamba_status mamba_linattn_fwd(const mamba_linattn_desc *desc,
  * from terms of its own, in float32 states and products and float64 sums: its error
  * goes by the magnitudes of what crosses token t, not by other tokens' gradients,
  * however large these are. For it the workspace takes the states at every 64 tokens
- * (bfloat16) or 32 (float32), twice.
+ * (bfloat16) or 32 (float32), twice, of all heads or, past 8 GiB, of some at a
+ * time. With bfloat16 io dq, dk and dv are other roundings of the same sums where
+ * dg is NULL.
  *   q, k, v, g, h0, offsets : as given to the forward.
  *   dout       : (rows, H, V) io dtype.
  *   dlast      : (batch, H, K, V) float32 or NULL (zero).

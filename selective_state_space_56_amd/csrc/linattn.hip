@@ -72,8 +72,8 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(MixCall w, int chunk
 // rounding of what other tokens add, which is more than strong decays, early tokens or small
 // gradients before large ones leave of dg_t.
 // One workgroup for each chunk and head. Bound by HBM: both states are read (8 x 2048 steps of 20 heads of
-// 128 x 128, bf16: 671 MB in 108 us, 6.2 TB/s, part of it from the last-level cache; with four and eight
-// pieces in flight per thread the training step of that size takes 671 and 710 us, with two 661).
+// 128 x 128, bf16: 0.63 GB in 117 us, 5.4 TB/s; with four and eight pieces in flight per thread the training
+// step of that size takes 671 and 710 us, with two 661).
 constexpr int kDecayThreads = 256;
 constexpr int kDecayAhead = 2;               // 16-byte pieces of each state in flight per thread
 constexpr int64_t kDecayGroups = int64_t(1) << 16;  // workgroups at most; each takes every kDecayGroups-th chunk and head
@@ -281,8 +281,9 @@ int chunk_of(const LinattnSizes& n) { return n.io == MAMBA_F32 ? 32 : 64; }
 int64_t chunks_of(const LinattnSizes& n) { return (n.rows + chunk_of(n) - 1) / chunk_of(n); }
 
 // Chunks of a segment, when `walks` workgroups walk each sequence. One segment per
-// sequence reads everything once; more let few sequences fill the machine, two
-// workgroups for each compute unit, at the price of reading keys and values twice and of
+// sequence reads everything once; more let few sequences fill the machine, planned as two
+// workgroups for each compute unit (which hold one where a state has over 128 rows, and in float32 with
+// four tiles, two waves and sums: half of those wait), at the price of reading keys and values twice and of
 // the states between. Sequences of one length get as many segments as workgroups fit (one
 // more would wait for a place: 131072 steps of 20 heads, 500 workgroups 1.25 ms, 520 1.32).
 // Of packed sequences the lengths are not known here: they are cut as one would be, unless
@@ -368,8 +369,8 @@ hipError_t zero_rest(const RestRows& z, hipStream_t stream) {
 
 // The backward's three runs go in one launch if their operands have one shape: they are the
 // same rows. Else dv's is one and that of dk and dq another, each with segments of its own
-// (forward and backward of 4 x 1000 steps of 32 heads of 64 x 128 take 260 us, with segments
-// as for one launch of all 290).
+// (forward and backward of 4 x 1000 steps of 32 heads of 64 x 128 took 260 us, with segments
+// as for one launch of all 290; 279 since the decays' gradients take every chunk's states).
 bool one_shape(const LinattnSizes& n) {
   return key_tiles(n.K) == key_tiles(n.V) && value_width(n.V) == value_width(n.K) && value_tiles(n.V) == value_tiles(n.K);
 }

@@ -7,7 +7,9 @@
 // product each: the scores and the state in the outputs as two (2^-17 of each term),
 // the weighted values that make the state as three (exact: 8 + 8 + 8 bits), so that
 // the state is a float32 one; with the sums for the decays' gradients the state as
-// three there too.
+// three there too. (Of a prompt's outputs 0.23 % are not the bf16 next to the exact value, where
+// float32 sums leave 0.03 %. A third part of the scores would leave a compute unit room for one
+// workgroup only: 84 KB of LDS at least.)
 //
 // Operand layouts (wave64, lane l): A (32 x 16): row l % 32, k = 8 (l / 32) .. + 7;
 // B (16 x 32): column l % 32, the same k; D (32 x 32): register i is row
@@ -19,7 +21,7 @@
 // the channels go along its registers, and its outputs leave four at a time. Operands
 // whose k is the step come from LDS by the transposing load.
 //
-// Bound by issue: 8 x 2048 steps of 40 heads of 128 x 128 take 235 us, 2.9 TB/s of 5.3 that
+// Bound by issue: 8 x 2048 steps of 40 heads of 128 x 128 take 240 us, 2.9 TB/s of 5.3 that
 // a copy reaches. The matrix products alone would take 67 us of them; splitting the state
 // and the weighted values into parts, the scores' factors and LDS take the rest, and the
 // vector and matrix instructions of a compute unit's eight waves hardly overlap. So the
@@ -549,7 +551,7 @@ __global__ __launch_bounds__(64 * NV * KH, least_waves(KT, KH)) void walk_bf16_k
         for (int m = 0; m < 3; ++m) part[m][e] = words[m];
       }
       // products that follow one another go to different tiles, here and above (to one tile its
-      // parts' three in a row: prompts 244 us instead of 237)
+      // parts' three in a row: prompts 244 us where these took 237)
       constexpr int kSide = KT < 4 ? KT : 4;
 #pragma unroll
       for (int kt = 0; kt < KT; kt += kSide) {

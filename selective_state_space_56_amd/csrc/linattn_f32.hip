@@ -9,12 +9,12 @@
 // they make S and the scores usable as operands just as they stand in the
 // registers of D, and four of A's values are one 16-byte read.
 //
-// Bound by the matrix cores: 8 x 2048 steps of 40 heads of 128 x 128 take 1.05 ms, 49
+// Bound by the matrix cores: 8 x 2048 steps of 40 heads of 128 x 128 take 1.04 ms, 49
 // TFLOP/s of 152 that a large product reaches, since 320 workgroups on 256 compute units are
-// two rounds for some. Chunks of 32 steps, not 64 as with bf16: half the scores, and
+// two rounds for some, and since one wave makes a chunk's scores while the others wait. Chunks of 32 steps, not 64 as with bf16: half the scores, and
 // two workgroups fit a compute unit, one of which has products to issue while the other
 // waits (64 steps and one workgroup, rows loaded when they were needed: 1.80 ms, its
-// gradients 4.83 against 2.76). The next chunk's rows are loaded while one is worked on.
+// gradients 4.83 where they then took 2.76; 3.29 with every chunk's states for those of the decays). The next chunk's rows are loaded while one is worked on.
 #include "linattn_walk.h"
 
 namespace mscan {
