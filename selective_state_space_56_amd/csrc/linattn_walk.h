@@ -198,9 +198,9 @@ struct Walk {
     }
   }
 
-  // The state that enters chunk c (in reverse, from behind, where another one follows), for the gradients of the decays: as it
-  // stands in registers, 32 x 32 tiles of 16 bytes of each lane, since only its product with another run's
-  // is asked for. (A training step of 8 x 2048 steps of 20 heads of 128 x 128, bf16: 755 us with rows of the
+  // The state that enters chunk c (in reverse, from behind, where another one follows), for the gradients
+  // of the decays: as it stands in registers, 32 x 32 tiles of 16 bytes of each lane, since only its product
+  // with another run's is asked for. (A training step of 8 x 2048 steps of 20 heads of 128 x 128, bf16: 755 us with rows of the
   // state written 4 bytes at a time, and 708 with 16, which is 685 with the non-temporal hint.)
   template <class Tile, int N, int C>
   __device__ __forceinline__ void leave_entering(const MixCall& w, const MixRole& r, const Tile (&S)[N], int c,
